@@ -24,6 +24,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 CSA2_OK, CSA2_ERR_INVALID, CSA2_ERR_CUDA, CSA2_ERR_UNSUPPORTED, CSA2_ERR_TIMEOUT, CSA2_ERR_DEVICE = range(6)
 DEV_BAD_INDEX, DEV_BAD_PAGE, DEV_OVERFLOW, DEV_TIMEOUT, DEV_BAD_POOL, DEV_BAD_ALIGN = (
     0x1, 0x2, 0x4, 0x8, 0x10, 0x20)
+DEV_NONFINITE = 0x40
 MAX_TOPK = 2048
 POOL_BLOCKS = 2048
 BLOCK = 8
@@ -47,6 +48,24 @@ class Csa2Cache(ctypes.Structure):
 
 
 IDX_E4M3, IDX_MXFP4 = 0, 1
+
+
+class Csa2Kv8Cache(ctypes.Structure):
+    _fields_ = [
+        ("batch", _i32), ("kv_heads", _i32), ("dim", _i32), ("block", _i32), ("page_size", _i32),
+        ("max_pages_per_seq", _i32), ("max_len", _i32), ("num_pages", _i32), ("format", _i32),
+        ("k_codes", _p), ("v_codes", _p), ("k_scales", _p), ("v_scales", _p), ("mass", _p),
+        ("page_table", _p), ("seq_len", _p),
+    ]
+
+
+class Csa2Rows(ctypes.Structure):
+    _fields_ = [("data", _p), ("stride_b", _i64), ("stride_t", _i64), ("stride_h", _i64),
+                ("type", _i32)]
+
+
+KV8_E4M3, KV8_INT8 = 0, 1
+BF16, F16, F32 = 0, 1, 2
 
 
 def _sig(name, args, res=_i32):
@@ -80,13 +99,21 @@ _reset_status = _sig("csa2_reset_status", [_p, _p])
 _status_string = _sig("csa2_status_string", [_i32], ctypes.c_char_p)
 _set_launch_events = _sig("csa2_set_launch_events", [_i32, _p, _p])
 _set_wait_limit = _sig("csa2_set_wait_limit", [ctypes.c_uint64])
+_C8P, _RP = ctypes.POINTER(Csa2Kv8Cache), ctypes.POINTER(Csa2Rows)
+_kv8_workspace_size = _sig("csa2_kv8_workspace_size", [_C8P, _i32, _i32], ctypes.c_size_t)
+_kv8_append = _sig("csa2_kv8_append", [_C8P, _RP, _RP, _i32, _p, _p, _p, _p])
+_kv8_attn = _sig("csa2_kv8_attn", [_C8P, _RP, _i32, _i32, _p, ctypes.c_float, _RP, _p, _p, _p])
+_kv8_mass = _sig("csa2_kv8_mass", [_C8P, _RP, _i32, _i32, _p, _p, ctypes.c_float, ctypes.c_float,
+                                   _p, _p])
+_kv8_evict = _sig("csa2_kv8_evict", [_C8P, _C8P, _i32, _i32, _i32, _p, _p, _p])
 KERNEL_QUANT, KERNEL_INDEXER, KERNEL_SELECT, KERNEL_ATTENTION = 0, 1, 2, 3
 
 EXPORTED = ["csa2_workspace_size", "csa2_entry_bytes", "csa2_fp8_quant", "csa2_quant_append",
             "csa2_index_full", "csa2_index_reindex", "csa2_attn_decode", "csa2_attn_prefill",
             "csa2_get_status", "csa2_reset_status", "csa2_status_string",
             "csa2_set_launch_events", "csa2_index_full_noalloc", "csa2_quant_append_pairs",
-            "csa2_set_wait_limit", "csa2_attn_decode_layers"]
+            "csa2_set_wait_limit", "csa2_attn_decode_layers", "csa2_kv8_workspace_size",
+            "csa2_kv8_append", "csa2_kv8_attn", "csa2_kv8_mass", "csa2_kv8_evict"]
 
 
 class Csa2Error(RuntimeError):
@@ -301,3 +328,202 @@ class Cache:
             raise Csa2Error("invalid cache description")
         ws = torch.zeros(n, dtype=torch.uint8, device=self.codes.device)
         return ws
+
+
+# ------------------------------------------------------- the 8-bit K/V cache
+def kv8_workspace_size(cache: "Cache8 | Csa2Kv8Cache", T: int, heads: int) -> int:
+    c = cache.struct if isinstance(cache, Cache8) else cache
+    return int(_kv8_workspace_size(ctypes.byref(c), T, heads))
+
+
+class Cache8:
+    """Device storage of a K/V cache of grouped heads in 8 bits plus its C
+    description (csa2_kv8_cache): codes with one power-of-two scale for each
+    block of rows and head.
+
+    ``tensors`` gives existing storage instead of new: a dict of k_codes and
+    v_codes (uint8 [pages, kv_heads, page rows, dim]), k_scales and v_scales
+    (fp32 [pages, kv_heads, page rows / block]), seq_len (int32 [batch]) and,
+    where weights are accumulated, mass (fp32 [pages, kv_heads, page rows]).
+    pages and page rows are num_pages and page_size, or, contiguous
+    (page_size 0), batch and max_len.
+    """
+
+    def __init__(self, batch, kv_heads, dim, max_len, block=64, page_size=0, page_table=None,
+                 num_pages=0, fmt=KV8_E4M3, mass=False, device="cuda", tensors=None):
+        import torch
+        self.batch, self.kv_heads, self.dim, self.max_len = batch, kv_heads, dim, max_len
+        self.block, self.page_size, self.fmt = block, page_size, fmt
+        pages, rows = (num_pages, page_size) if page_size else (batch, max_len)
+        if page_size and page_table is None:
+            raise Csa2Error("Cache8: a paged cache needs a page table")
+        if not page_size and page_table is not None:
+            raise Csa2Error("Cache8: a contiguous cache (page_size 0) has no page table")
+        if min(batch, kv_heads, dim, max_len, block, pages, rows) < 1 or rows % block:
+            raise Csa2Error("invalid cache description")
+        shapes = {"k_codes": (torch.uint8, (pages, kv_heads, rows, dim)),
+                  "v_codes": (torch.uint8, (pages, kv_heads, rows, dim)),
+                  "k_scales": (torch.float32, (pages, kv_heads, rows // block)),
+                  "v_scales": (torch.float32, (pages, kv_heads, rows // block)),
+                  "mass": (torch.float32, (pages, kv_heads, rows)),
+                  "seq_len": (torch.int32, (batch,))}
+        if tensors is None:
+            tensors = {n: torch.zeros(shape, dtype=dt, device=device)
+                       for n, (dt, shape) in shapes.items() if n != "mass" or mass}
+        device = tensors["seq_len"].device
+        for n, (dt, shape) in shapes.items():
+            t = tensors.get(n)
+            if t is None and n == "mass":
+                continue
+            if t is None or t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous() \
+                    or t.device != device:
+                raise Csa2Error(f"Cache8: {n} must be a contiguous {dt} tensor of shape {shape} "
+                                f"on {device}")
+        for n in shapes:
+            setattr(self, n, tensors.get(n))
+        self.device, self.num_pages = device, num_pages if page_size else 0
+        if page_size:
+            self.page_table = page_table.to(device=device, dtype=torch.int32).contiguous()
+            if self.page_table.dim() != 2 or self.page_table.shape[0] != batch:
+                raise Csa2Error("Cache8: the page table is [batch, pages per sequence]")
+        else:
+            self.page_table = None
+        self.struct = Csa2Kv8Cache(
+            batch, kv_heads, dim, block, page_size,
+            self.page_table.shape[1] if page_size else 0, max_len, self.num_pages, fmt,
+            _ptr(self.k_codes), _ptr(self.v_codes), _ptr(self.k_scales), _ptr(self.v_scales),
+            _ptr(self.mass), _ptr(self.page_table), _ptr(self.seq_len))
+
+    def workspace(self, T, heads):
+        """Workspace for calls of at most T query rows per sequence and `heads` heads."""
+        import torch
+        n = kv8_workspace_size(self, T, heads)
+        if n == 0:
+            raise Csa2Error("invalid cache description")
+        return torch.zeros(n, dtype=torch.uint8, device=self.device)
+
+
+def _kv8_rows(cache, x, name, heads, types=("bfloat16", "float16")):
+    """(struct, T) of a [batch, T, heads, dim] tensor whose last dimension is contiguous."""
+    kind = str(x.dtype).replace("torch.", "")
+    if kind not in types:
+        raise Csa2Error(f"{name}: {kind}; it takes " + ", ".join(types))
+    if x.dim() != 4 or x.shape[0] != cache.batch or x.shape[3] != cache.dim or (
+            heads is not None and x.shape[2] != heads):
+        raise Csa2Error(f"{name}: shape {tuple(x.shape)}; it takes [batch {cache.batch}, T, "
+                        f"{'heads' if heads is None else heads}, dim {cache.dim}]")
+    if x.device != cache.device:
+        raise Csa2Error(f"{name}: on {x.device}, the cache on {cache.device}")
+    if x.numel() == 0:
+        return Csa2Rows(None, 0, 0, 0, {"bfloat16": BF16, "float16": F16, "float32": F32}[kind]), 0
+    es = x.element_size()
+    # the stride of a dimension of one element is not used
+    sb, st, sh = (x.stride(i) if x.shape[i] > 1 else 0 for i in range(3))
+    if x.stride(3) != 1 or x.data_ptr() % 16 or any(v * es % 16 for v in (sb, st, sh)):
+        raise Csa2Error(f"{name}: the last dimension must be contiguous and every row start on a "
+                        "multiple of 16 bytes")
+    return Csa2Rows(x.data_ptr(), sb, st, sh,
+                    {"bfloat16": BF16, "float16": F16, "float32": F32}[kind]), x.shape[1]
+
+
+def _kv8_arg(cache, x, name, dtype, shape):
+    """Pointer of an optional contiguous tensor of this type and shape on the cache's device."""
+    if x is None:
+        return None
+    if str(x.dtype) != "torch." + dtype or tuple(x.shape) != tuple(shape) or \
+            not x.is_contiguous() or x.device != cache.device:
+        raise Csa2Error(f"{name}: it takes a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                        f"{cache.device}")
+    return x.data_ptr()
+
+
+def _kv8_ws(cache, ws, T=0, heads=None):
+    need = kv8_workspace_size(cache, T, heads or cache.kv_heads)
+    if need == 0:
+        raise Csa2Error("the cache does not take a call of %d query rows and %s heads" % (T, heads))
+    if ws.device != cache.device or not ws.is_contiguous() or \
+            ws.numel() * ws.element_size() < need:
+        raise Csa2Error(f"workspace: it takes {need} contiguous bytes on {cache.device}")
+    return ws.data_ptr()
+
+
+class _On:
+    """The cache's device for the length of a call, and the stream on it."""
+
+    def __init__(self, cache, stream):
+        import torch
+        if cache.device.type != "cuda":
+            raise Csa2Error("the cache is not on a CUDA device")
+        self.guard, self.stream = torch.cuda.device(cache.device), stream
+
+    def __enter__(self):
+        self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *a):
+        return self.guard.__exit__(*a)
+
+
+def kv8_append(cache, k, v, ws, new_len=None, start=None, stream=None):
+    """Quantise and append the rows k, v [batch, T, kv_heads, dim] (bf16, f16 or
+    fp32): new_len[b] of them (int32 [batch], default T) from position start[b]
+    on (int32 [batch], default seq_len)."""
+    types = ("bfloat16", "float16", "float32")
+    (rk, T), (rv, Tv) = (_kv8_rows(cache, x, n, cache.kv_heads, types)
+                         for x, n in ((k, "k"), (v, "v")))
+    if T != Tv or rk.type != rv.type:
+        raise Csa2Error("k and v: one T and one type")
+    nl = _kv8_arg(cache, new_len, "new_len", "int32", (cache.batch,))
+    sp = _kv8_arg(cache, start, "start", "int32", (cache.batch,))
+    w = _kv8_ws(cache, ws)
+    with _On(cache, stream) as s:
+        _check(_kv8_append(ctypes.byref(cache.struct), ctypes.byref(rk), ctypes.byref(rv), T, nl,
+                           sp, w, s), "csa2_kv8_append")
+
+
+def kv8_attn(cache, q, out, ws, lse=None, q_len=None, softmax_scale=0.0, stream=None):
+    """Attention of the queries q [batch, T, heads, dim] (bf16 or f16) of each
+    sequence's last q_len[b] rows (int32 [batch], default T) over the cache, into
+    out (as q) and lse (fp32 [batch, T, heads], optional)."""
+    rq, T = _kv8_rows(cache, q, "q", None)
+    H = q.shape[2]
+    ro, To = _kv8_rows(cache, out, "out", H)
+    if To != T or ro.type != rq.type:
+        raise Csa2Error("out: shape and type of q")
+    ls = _kv8_arg(cache, lse, "lse", "float32", (cache.batch, T, H))
+    ql = _kv8_arg(cache, q_len, "q_len", "int32", (cache.batch,))
+    w = _kv8_ws(cache, ws, T, H)
+    with _On(cache, stream) as s:
+        _check(_kv8_attn(ctypes.byref(cache.struct), ctypes.byref(rq), H, T, ql,
+                         float(softmax_scale), ctypes.byref(ro), ls, w, s), "csa2_kv8_attn")
+
+
+def kv8_mass(cache, q, lse, ws, q_len=None, softmax_scale=0.0, decay=1.0, stream=None):
+    """cache.mass = decay * cache.mass + the weight that each row got from the
+    queries q, given the lse that kv8_attn returned for them."""
+    rq, T = _kv8_rows(cache, q, "q", None)
+    H = q.shape[2]
+    if cache.mass is None or lse is None:
+        raise Csa2Error("csa2_kv8_mass: the cache holds no mass, or no lse given")
+    ls = _kv8_arg(cache, lse, "lse", "float32", (cache.batch, T, H))
+    ql = _kv8_arg(cache, q_len, "q_len", "int32", (cache.batch,))
+    w = _kv8_ws(cache, ws, T, H)
+    with _On(cache, stream) as s:
+        _check(_kv8_mass(ctypes.byref(cache.struct), ctypes.byref(rq), H, T, ql, ls,
+                         float(softmax_scale), float(decay), w, s), "csa2_kv8_mass")
+
+
+def kv8_evict(cache, keep, sink, recent, kept, ws, dst=None, stream=None):
+    """Cut every sequence to at most `keep` rows: the first `sink`, the last
+    `recent`, and the heaviest by cache.mass between them, in place or into the
+    cache `dst`.  kept (int32 [batch, kv_heads, keep]): their former positions."""
+    kp = _kv8_arg(cache, kept, "kept", "int32", (cache.batch, cache.kv_heads, keep))
+    if kp is None or cache.mass is None:
+        raise Csa2Error("csa2_kv8_evict: it takes `kept`, and a cache with mass")
+    if dst is not None and dst.device != cache.device:
+        raise Csa2Error(f"dst: on {dst.device}, the cache on {cache.device}")
+    w = _kv8_ws(cache, ws)
+    with _On(cache, stream) as s:
+        _check(_kv8_evict(ctypes.byref(cache.struct),
+                          ctypes.byref(dst.struct) if dst is not None else None, keep, sink,
+                          recent, kp, w, s), "csa2_kv8_evict")

@@ -1,0 +1,237 @@
+// Shared pieces of the 8-bit K/V cache's kernels: the cache's addressing, the
+// code formats, the scale rule and the split of the cached rows over CTAs.
+//
+// Storage: codes [pages, kv_heads, page rows, D] (a page's rows of one head are
+// contiguous, so a tile of keys streams as one run), one fp32 scale per block
+// of rows and head, always a power of two.  With a power of two the division
+// x / s, the re-expression of a code under a larger scale and the product
+// code * s are exact in fp32 but for the one rounding to the 8-bit format, so
+// the stored bytes do not depend on how the arithmetic was arranged.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "codec.cuh"
+#include "launch.h"
+
+namespace csa2 {
+
+constexpr int kKv8Ctas = 512;      // upper bound of the split kernels' CTAs
+constexpr int kKv8SlotRows = 32;   // query rows of one partial result
+constexpr int kKv8Step = 128;      // cached rows of one step of a CTA
+
+struct Kv8 {
+  uint8_t* codes[2];               // K, V
+  float* scales[2];
+  float* mass;
+  const int32_t* page_table;
+  int32_t* seq_len;
+  int32_t batch, heads, block_shift, page_rows, max_pages, max_len, num_pages, format;
+  int32_t paged, page_shift;       // page_shift: log2(page_rows) or -1
+};
+
+// Page (physical) and row in the page of position t of sequence b; page -1
+// when the table's entry is out of range.
+__device__ __forceinline__ int kv8_page(const Kv8& c, int b, int t, int& in_page) {
+  if (!c.paged) {
+    in_page = t;
+    return b;
+  }
+  const uint32_t ut = (uint32_t)t;
+  uint32_t pg;
+  if (c.page_shift >= 0) {
+    pg = ut >> c.page_shift;
+    in_page = (int)(ut & (uint32_t)(c.page_rows - 1));
+  } else {
+    pg = ut / (uint32_t)c.page_rows;
+    in_page = (int)(ut - pg * (uint32_t)c.page_rows);
+  }
+  const int32_t phys = c.page_table[(int64_t)b * c.max_pages + pg];
+  return phys < 0 || phys >= c.num_pages ? -1 : phys;
+}
+// Row index over [pages, kv_heads, page rows]; times D for codes, as is for mass.
+__device__ __forceinline__ int64_t kv8_row(const Kv8& c, int page, int h, int in_page) {
+  return ((int64_t)page * c.heads + h) * c.page_rows + in_page;
+}
+// Index of the block's scale.
+__device__ __forceinline__ int64_t kv8_block(const Kv8& c, int page, int h, int in_page) {
+  return ((int64_t)page * c.heads + h) * (c.page_rows >> c.block_shift) + (in_page >> c.block_shift);
+}
+__device__ __forceinline__ int kv8_len(const Kv8& c, int b) {
+  const int n = c.seq_len[b];
+  return n < 0 ? 0 : (n > c.max_len ? c.max_len : n);
+}
+
+// ------------------------------------------------------------------- formats
+// The smallest power of two s >= 2^-126 with amax <= qmax * s (qmax 448 = 1.75
+// * 2^8, or 127 = 1.984375 * 2^6); 0 for amax = 0.  amax is finite.
+template <int FMT>
+__device__ __forceinline__ float kv8_scale_of(float amax) {
+  if (amax == 0.0f) return 0.0f;
+  const uint32_t u = __float_as_uint(amax);
+  const int top = FMT == CSA2_KV8_E4M3 ? 8 : 6;
+  const uint32_t lead = FMT == CSA2_KV8_E4M3 ? 0x600000u : 0x7E0000u;
+  int e = (int)(u >> 23) - 127 - top + ((u & 0x7FFFFFu) > lead ? 1 : 0);
+  e = e < -126 ? -126 : e;
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+// 1/s of a power of two in [2^-126, 2^126]; 0 for 0.
+__device__ __forceinline__ float kv8_inverse(float s) {
+  return s == 0.0f ? 0.0f : __uint_as_float((254u << 23) - __float_as_uint(s));
+}
+// Four values already divided by the scale -> four codes (round to nearest,
+// ties to even, saturating).
+template <int FMT>
+__device__ __forceinline__ uint32_t kv8_encode4(float a, float b, float c, float d) {
+  if (FMT == CSA2_KV8_E4M3) return e4m3x2_from_f32(a, b) | (e4m3x2_from_f32(c, d) << 16);
+  uint32_t r = 0;
+  const float v[4] = {a, b, c, d};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int q = __float2int_rn(fminf(fmaxf(v[i], -127.0f), 127.0f));
+    r |= ((uint32_t)q & 0xFFu) << (8 * i);
+  }
+  return r;
+}
+// Four codes -> two f16x2 (codes 0, 1 and 2, 3).  Exact.
+template <int FMT>
+__device__ __forceinline__ void kv8_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (FMT == CSA2_KV8_E4M3) {
+    lo = e4m3x2_to_f16x2(w & 0xFFFFu);
+    hi = e4m3x2_to_f16x2(w >> 16);
+  } else {
+    // v + 128 as the low byte of 1024 + (v + 128), then minus 1152
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 bias = __half2half2(__ushort_as_half((unsigned short)0x6480));
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    __half2 ha = __hsub2(*reinterpret_cast<__half2*>(&a), bias);
+    __half2 hb = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
+    lo = *reinterpret_cast<uint32_t*>(&ha);
+    hi = *reinterpret_cast<uint32_t*>(&hb);
+  }
+}
+template <int FMT>
+__device__ __forceinline__ void kv8_to_f32(uint32_t w, float (&v)[4]) {
+  uint32_t lo, hi;
+  kv8_to_f16<FMT>(w, lo, hi);
+  const float2 a = __half22float2(*reinterpret_cast<__half2*>(&lo));
+  const float2 b = __half22float2(*reinterpret_cast<__half2*>(&hi));
+  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+}
+// Largest magnitude among four codes as a number that grows with it.
+template <int FMT>
+__device__ __forceinline__ uint32_t kv8_max4(uint32_t w) {
+  const uint32_t m = FMT == CSA2_KV8_E4M3 ? (w & 0x7F7F7F7Fu) : __vabsss4(w);
+  const uint32_t x = __vmaxu4(m, m >> 16);
+  return max(x & 0xFFu, (x >> 8) & 0xFFu);
+}
+template <int FMT>
+__device__ __forceinline__ float kv8_mag(uint32_t m) {
+  return FMT == CSA2_KV8_E4M3 ? e4m3_decode(m) : (float)m;
+}
+// Four codes under scale s re-expressed with ratio = s / s_new.
+template <int FMT>
+__device__ __forceinline__ uint32_t kv8_recode(uint32_t w, float ratio) {
+  float v[4];
+  kv8_to_f32<FMT>(w, v);
+  return kv8_encode4<FMT>(v[0] * ratio, v[1] * ratio, v[2] * ratio, v[3] * ratio);
+}
+
+// ------------------------------------------------------------------ row types
+__device__ __forceinline__ void bf16x2_to_f32(uint32_t w, float& a, float& b) {
+  a = __uint_as_float(w << 16);
+  b = __uint_as_float(w & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint32_t pack16(float a, float b, int type) {
+  if (type == CSA2_BF16) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&x);
+  }
+  const __half2 x = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+
+__device__ __forceinline__ float kv8_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ------------------------------------------------- split of rows over the CTAs
+// The steps (of kKv8Step cached rows) of all units are numbered through,
+// sequence by sequence and within one unit by unit; CTA i of n takes the steps
+// [W i / n, W (i+1) / n).  All sequences share the CTAs evenly whatever their
+// lengths, which only the device knows.  Every sequence has at least one step.
+__device__ __forceinline__ int kv8_steps(const Kv8& c, int b) {
+  const int n = kv8_len(c, b);
+  return n <= kKv8Step ? 1 : (n + kKv8Step - 1) / kKv8Step;
+}
+// Steps of one unit of all sequences (every lane of the warp gets it).
+__device__ __forceinline__ int64_t kv8_total(const Kv8& c, int lane) {
+  int64_t s = 0;
+  for (int b = lane; b < c.batch; b += 32) s += kv8_steps(c, b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+// Steps in front of sequence b (of one unit each).
+__device__ __forceinline__ int64_t kv8_before(const Kv8& c, int lane, int b) {
+  int64_t s = 0;
+  for (int i = lane; i < b; i += 32) s += kv8_steps(c, i);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+// The sequence that holds step x when each has `units` units, and the step of
+// its first unit (whole warp; x below the total).
+__device__ __forceinline__ int kv8_find(const Kv8& c, int lane, int units, int64_t x,
+                                        int64_t& first) {
+  int64_t before = 0;
+  for (int base = 0;; base += 32) {
+    const int b = base + lane;
+    const int64_t mine = b < c.batch ? (int64_t)kv8_steps(c, b) * units : 0;
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, before + incl > x);
+    if (hit || base + 32 >= c.batch) {
+      const int l = hit ? __ffs(hit) - 1 : 31;
+      first = before + __shfl_sync(0xffffffffu, incl - mine, l);
+      return min(base + l, c.batch - 1);
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+// ------------------------------------------------------------------ launchers
+struct Kv8Rows {          // rows [B, T, heads, D] with element strides
+  const void* data;
+  int64_t sb, st, sh;
+  int32_t type;
+};
+struct Kv8Attn {
+  Kv8 c;
+  Kv8Rows q, out;         // out.data null: mass only
+  float* lse;             // [B, T, H] or null (attention); read by mass
+  const int32_t* q_len;   // [B] or null
+  int32_t T, H, G, D;
+  float scale_log2;
+  float decay;            // mass
+  float* part;            // partial results
+  uint32_t* status;
+};
+size_t kv8_part_bytes(int D);
+cudaError_t launch_kv8_append(const Kv8& c, int D, const Kv8Rows& k, const Kv8Rows& v, int T,
+                              const int32_t* new_len, const int32_t* start, uint32_t* status,
+                              cudaStream_t s);
+cudaError_t launch_kv8_attn(const Kv8Attn& a, int num_sms, cudaStream_t s);
+cudaError_t launch_kv8_mass(const Kv8Attn& a, int num_sms, cudaStream_t s);
+cudaError_t launch_kv8_evict(const Kv8& src, const Kv8& dst, bool in_place, int D, int keep,
+                             int sink, int recent, int32_t* kept, int32_t* old_len,
+                             uint32_t* status, int num_sms, cudaStream_t s);
+
+}  // namespace csa2

@@ -69,6 +69,7 @@ typedef enum csa2_status {
 #define CSA2_DEV_TIMEOUT 0x8u     /* a bounded on-chip wait gave up */
 #define CSA2_DEV_BAD_POOL 0x10u   /* pool block id outside the visible blocks */
 #define CSA2_DEV_BAD_ALIGN 0x20u  /* on-chip buffer misaligned (kernel skipped work) */
+#define CSA2_DEV_NONFINITE 0x40u  /* csa2_kv8_append met an infinity or a NaN */
 
 /* Largest k and the pool capacity (blocks of 8 positions). */
 #define CSA2_MAX_TOPK 2048
@@ -343,6 +344,132 @@ csa2_status csa2_attn_prefill(const csa2_cache *cache, const uint16_t *q, int32_
                               const int32_t *q_pos, const int32_t *idx, const int32_t *cnt,
                               int32_t kcap, const uint8_t *swa, int32_t W, float softmax_scale,
                               float *out, void *ws, void *stream);
+
+/* ------------------------------------------------------------------------
+ * A K/V cache of grouped heads in 8 bits, for the layers with ordinary (dense)
+ * attention beside the CSA2 layers.  Hkv heads of K and of V rows of D
+ * channels each; H = Hkv * G query heads, query head h reads K/V head h / G.
+ *
+ * Storage.  Row r of page g and head h is at row index (g * Hkv + h) * P + r
+ * with P = page_size (paged) or max_len (page_size 0: page g is sequence g):
+ *   k_codes, v_codes    uint8 [pages, Hkv, P, D]
+ *   k_scales, v_scales  fp32 [pages, Hkv, P / block]: one scale for each block
+ *                       of rows and head; a row's values are code * scale
+ *   mass                fp32 [pages, Hkv, P] or NULL: the attention weight that
+ *                       each row got (csa2_kv8_mass; the rank of csa2_kv8_evict)
+ * Position t of sequence b is row t % P of page page_table[b, t / P] (paged).
+ *
+ * Scales are powers of two: the scale of values with the largest magnitude
+ * amax > 0 is the smallest 2^e, e >= -126, with amax <= qmax * 2^e (qmax = 448
+ * for E4M3, 127 for INT8), and 0 for amax = 0 (all codes 0).  A value's code is
+ * the format's nearest to value / scale, ties to even.
+ *
+ * Sequences whose page-table rows name a common page may share it for reading.
+ * A page that csa2_kv8_append or csa2_kv8_evict writes must be in one row only.
+ */
+typedef struct csa2_kv8_cache {
+  int32_t batch;              /* B sequences */
+  int32_t kv_heads;           /* Hkv, 1..1024 */
+  int32_t dim;                /* D: 64 or 128 */
+  int32_t block;              /* rows per scale: 16, 32, 64 or 128 */
+  int32_t page_size;          /* rows per page, a multiple of block; 0 = contiguous */
+  int32_t max_pages_per_seq;  /* columns of page_table (paged only) */
+  int32_t max_len;            /* capacity in rows per sequence; <= CSA2_MAX_LEN; a
+                                 multiple of block when page_size == 0 */
+  int32_t num_pages;          /* physical pages (paged), used for bounds checks */
+  int32_t format;             /* CSA2_KV8_E4M3 or CSA2_KV8_INT8 */
+  uint8_t *k_codes, *v_codes;   /* 16-byte aligned */
+  float *k_scales, *v_scales;
+  float *mass;                /* or NULL */
+  const int32_t *page_table;  /* [B, max_pages_per_seq] or NULL when page_size == 0 */
+  int32_t *seq_len;           /* [B] rows held */
+} csa2_kv8_cache;
+
+#define CSA2_KV8_E4M3 0
+#define CSA2_KV8_INT8 1
+
+/* Rows [B, T, heads, D] of a tensor whose last dimension is contiguous; the
+ * strides are in elements.  data and the strides in bytes are multiples of 16. */
+typedef struct csa2_rows {
+  void *data;
+  int64_t stride_b, stride_t, stride_h;
+  int32_t type;               /* CSA2_BF16, CSA2_F16 or CSA2_F32 */
+} csa2_rows;
+
+#define CSA2_BF16 0
+#define CSA2_F16 1
+#define CSA2_F32 2
+
+/* Workspace bytes for the calls below on `cache` (at most T query rows per
+ * sequence and H query heads); 0 when the description is invalid. */
+size_t csa2_kv8_workspace_size(const csa2_kv8_cache *cache, int32_t T, int32_t H);
+
+/*
+ * Append.  k, v: rows [B, T, Hkv, D] of one type.  Of sequence b the first
+ * new_len[b] rows (device int32 [B], clamped to 0..T; NULL: T) land at the
+ * positions start[b] + i (device int32 [B]; NULL: seq_len[b]); afterwards
+ * seq_len[b] = start[b] + new_len[b].  A start below seq_len[b] drops the rows
+ * from there on (proposed tokens that were refused); the rows in front of
+ * start must be held.
+ * A block that begins with the append takes the scale of its new rows.  A
+ * block with earlier rows takes the larger of its scale and that of the new
+ * rows; when that raises it, the earlier rows' codes become the format's
+ * nearest to code * old / new.
+ * Infinities and NaN do not count for the scale and set CSA2_DEV_NONFINITE; an
+ * infinity is stored as the largest code of its sign (0 under scale 0), a NaN
+ * as 0.  Rows past max_len are left out and set CSA2_DEV_OVERFLOW, as does a
+ * start outside [0, max_len].  mass, when there is one, is 0 at the new rows.
+ */
+csa2_status csa2_kv8_append(const csa2_kv8_cache *cache, const csa2_rows *k, const csa2_rows *v,
+                            int32_t T, const int32_t *new_len, const int32_t *start, void *ws,
+                            void *stream);
+
+/*
+ * Attention.  q: bf16 or f16 rows [B, T, H, D]; out: rows of q's type and
+ * shape.  Of sequence b the first q_len[b] query rows count (device int32 [B],
+ * clamped to 0..T; NULL: T): they are the queries of the last q_len[b] cached
+ * rows, and query i sees rows 0 .. seq_len[b] - q_len[b] + i.  T = 1 is a
+ * decode step.
+ *   o = sum_j softmax_j(softmax_scale * q . k_j) v_j
+ *   lse (fp32 [B, T, H] or NULL) = ln sum_j exp(softmax_scale * q . k_j)
+ * A query that sees no row gives zeros and lse = -inf.  out and lse behind
+ * q_len[b] are left as they were.  softmax_scale <= 0 selects 1/sqrt(D).
+ * Rows on a page outside [0, num_pages) are left out (CSA2_DEV_BAD_PAGE).
+ */
+csa2_status csa2_kv8_attn(const csa2_kv8_cache *cache, const csa2_rows *q, int32_t H, int32_t T,
+                          const int32_t *q_len, float softmax_scale, const csa2_rows *out,
+                          float *lse, void *ws, void *stream);
+
+/*
+ * Accumulated weight: for every cached row j of sequence b and K/V head
+ *   mass_j = decay * mass_j + sum over the head's G query heads and the queries
+ *            that see row j of exp(softmax_scale * q . k_j - lse)
+ * with q, q_len and softmax_scale as given to csa2_kv8_attn, whose lse it takes
+ * (fp32 [B, T, H]; a query with lse = -inf adds nothing).  decay 1 accumulates,
+ * 0 starts anew (whatever mass held).  Rows behind seq_len are left as they were.
+ */
+csa2_status csa2_kv8_mass(const csa2_kv8_cache *cache, const csa2_rows *q, int32_t H, int32_t T,
+                          const int32_t *q_len, const float *lse, float softmax_scale, float decay,
+                          void *ws, void *stream);
+
+/*
+ * Eviction.  Of a sequence with more than `keep` rows every K/V head keeps, in
+ * their order, its first `sink` rows, its last `recent` rows and of those
+ * between the keep - sink - recent with the largest mass (equal ones: the lower
+ * row; NaN counts as the largest, a row on a bad page as the smallest);
+ * sink + recent <= keep.  kept (int32
+ * [B, Hkv, keep]) gets the rows' former positions, -1 behind them.
+ * dst NULL: in place, seq_len[b] becomes keep; sequences with at most `keep`
+ * rows are not touched.  Otherwise the rows go to dst, another cache of the
+ * same batch, kv_heads, dim, block and format with max_len >= keep, whose
+ * seq_len becomes min(seq_len, keep); it may lie in the same pool but shares no
+ * page with `cache`, which stays as it is.
+ * A block of the result whose rows all keep their positions keeps its codes
+ * and scale.  Any other holds what an append of its rows' values would give.
+ * mass moves with the rows.  Rows behind the new length are left as they were.
+ */
+csa2_status csa2_kv8_evict(const csa2_kv8_cache *cache, const csa2_kv8_cache *dst, int32_t keep,
+                           int32_t sink, int32_t recent, int32_t *kept, void *ws, void *stream);
 
 /* Copies the device status word to *host_status after the stream drains.
  * Returns CSA2_ERR_DEVICE when any bit is set. */
