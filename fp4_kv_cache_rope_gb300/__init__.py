@@ -354,6 +354,9 @@ class Cache8:
         import torch
         self.batch, self.kv_heads, self.dim, self.max_len = batch, kv_heads, dim, max_len
         self.block, self.page_size, self.fmt = block, page_size, fmt
+        self.int32, self.float32, self.needs = torch.int32, torch.float32, {}
+        self.kinds = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
+        self.cuda = torch.cuda, torch._C._cuda_getCurrentRawStream
         pages, rows = (num_pages, page_size) if page_size else (batch, max_len)
         if page_size and page_table is None:
             raise Csa2Error("Cache8: a paged cache needs a page table")
@@ -382,6 +385,7 @@ class Cache8:
         for n in shapes:
             setattr(self, n, tensors.get(n))
         self.device, self.num_pages = device, num_pages if page_size else 0
+        self.index = device.index if device.type == "cuda" else None
         if page_size:
             self.page_table = page_table.to(device=device, dtype=torch.int32).contiguous()
             if self.page_table.dim() != 2 or self.page_table.shape[0] != batch:
@@ -403,114 +407,118 @@ class Cache8:
         return torch.zeros(n, dtype=torch.uint8, device=self.device)
 
 
-def _kv8_rows(cache, x, name, heads, types=("bfloat16", "float16")):
+# The calls below are made once per layer and token, so their checks are kept to
+# a few attribute reads, and a refusal's text is put together only when it is raised.
+def _kv8_rows(cache, x, name, heads=None, wide=False):
     """(struct, T) of a [batch, T, heads, dim] tensor whose last dimension is contiguous."""
-    kind = str(x.dtype).replace("torch.", "")
-    if kind not in types:
-        raise Csa2Error(f"{name}: {kind}; it takes " + ", ".join(types))
-    if x.dim() != 4 or x.shape[0] != cache.batch or x.shape[3] != cache.dim or (
-            heads is not None and x.shape[2] != heads):
-        raise Csa2Error(f"{name}: shape {tuple(x.shape)}; it takes [batch {cache.batch}, T, "
+    kind, shape = cache.kinds.get(x.dtype), x.shape
+    if kind is None or (kind == F32 and not wide):
+        raise Csa2Error(f"{name}: {x.dtype}; it takes bfloat16, float16"
+                        + (" or float32" if wide else ""))
+    if len(shape) != 4 or shape[0] != cache.batch or shape[3] != cache.dim or (
+            heads is not None and shape[2] != heads):
+        raise Csa2Error(f"{name}: shape {tuple(shape)}; it takes [batch {cache.batch}, T, "
                         f"{'heads' if heads is None else heads}, dim {cache.dim}]")
     if x.device != cache.device:
         raise Csa2Error(f"{name}: on {x.device}, the cache on {cache.device}")
-    if x.numel() == 0:
-        return Csa2Rows(None, 0, 0, 0, {"bfloat16": BF16, "float16": F16, "float32": F32}[kind]), 0
-    es = x.element_size()
-    # the stride of a dimension of one element is not used
-    sb, st, sh = (x.stride(i) if x.shape[i] > 1 else 0 for i in range(3))
-    if x.stride(3) != 1 or x.data_ptr() % 16 or any(v * es % 16 for v in (sb, st, sh)):
-        raise Csa2Error(f"{name}: the last dimension must be contiguous and every row start on a "
-                        "multiple of 16 bytes")
-    return Csa2Rows(x.data_ptr(), sb, st, sh,
-                    {"bfloat16": BF16, "float16": F16, "float32": F32}[kind]), x.shape[1]
+    T = shape[1]
+    if T == 0 or shape[2] == 0:
+        return Csa2Rows(None, 0, 0, 0, kind), T
+    sb, st, sh, sd = x.stride()
+    at, part = x.data_ptr(), 3 if kind == F32 else 7   # strides in steps of 16 bytes
+    if sd != 1 or at & 15 or (sb | st | sh) & part:
+        # the stride of a dimension of one element is not used
+        sb, st, sh = (v if n > 1 else 0 for v, n in zip((sb, st, sh), shape))
+        if sd != 1 or at & 15 or (sb | st | sh) & part:
+            raise Csa2Error(f"{name}: the last dimension must be contiguous and every row start "
+                            "on a multiple of 16 bytes")
+    return Csa2Rows(at, sb, st, sh, kind), T
 
 
 def _kv8_arg(cache, x, name, dtype, shape):
     """Pointer of an optional contiguous tensor of this type and shape on the cache's device."""
     if x is None:
         return None
-    if str(x.dtype) != "torch." + dtype or tuple(x.shape) != tuple(shape) or \
-            not x.is_contiguous() or x.device != cache.device:
-        raise Csa2Error(f"{name}: it takes a contiguous {dtype} tensor of shape {tuple(shape)} on "
+    if x.dtype != getattr(cache, dtype) or x.shape != shape or not x.is_contiguous() \
+            or x.device != cache.device:
+        raise Csa2Error(f"{name}: it takes a contiguous {dtype} tensor of shape {shape} on "
                         f"{cache.device}")
     return x.data_ptr()
 
 
 def _kv8_ws(cache, ws, T=0, heads=None):
-    need = kv8_workspace_size(cache, T, heads or cache.kv_heads)
-    if need == 0:
-        raise Csa2Error("the cache does not take a call of %d query rows and %s heads" % (T, heads))
-    if ws.device != cache.device or not ws.is_contiguous() or \
-            ws.numel() * ws.element_size() < need:
+    heads = cache.kv_heads if heads is None else heads
+    need = cache.needs.get((T, heads))
+    if need is None:
+        need = kv8_workspace_size(cache, T, heads)
+        if need == 0:
+            raise Csa2Error(f"the cache does not take a call of {T} query rows and {heads} heads")
+        if len(cache.needs) > 256:
+            cache.needs.clear()
+        cache.needs[T, heads] = need
+    if ws.device != cache.device or ws.numel() * ws.element_size() < need or not ws.is_contiguous():
         raise Csa2Error(f"workspace: it takes {need} contiguous bytes on {cache.device}")
     return ws.data_ptr()
 
 
-class _On:
-    """The cache's device for the length of a call, and the stream on it."""
-
-    def __init__(self, cache, stream):
-        import torch
-        if cache.device.type != "cuda":
-            raise Csa2Error("the cache is not on a CUDA device")
-        self.guard, self.stream = torch.cuda.device(cache.device), stream
-
-    def __enter__(self):
-        self.guard.__enter__()
-        return _stream(self.stream)
-
-    def __exit__(self, *a):
-        return self.guard.__exit__(*a)
+def _kv8_run(cache, what, call, stream, *args):
+    """call(*args, stream) with the cache's device current."""
+    if cache.index is None:
+        raise Csa2Error("the cache is not on a CUDA device")
+    cuda, raw = cache.cuda
+    if cuda.current_device() != cache.index:
+        with cuda.device(cache.index):
+            return _kv8_run(cache, what, call, stream, *args)
+    if stream is None:
+        stream = raw(cache.index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    code = call(*args, stream)
+    if code:
+        _check(code, what)
 
 
 def kv8_append(cache, k, v, ws, new_len=None, start=None, stream=None):
     """Quantise and append the rows k, v [batch, T, kv_heads, dim] (bf16, f16 or
     fp32): new_len[b] of them (int32 [batch], default T) from position start[b]
     on (int32 [batch], default seq_len)."""
-    types = ("bfloat16", "float16", "float32")
-    (rk, T), (rv, Tv) = (_kv8_rows(cache, x, n, cache.kv_heads, types)
-                         for x, n in ((k, "k"), (v, "v")))
+    rk, T = _kv8_rows(cache, k, "k", cache.kv_heads, True)
+    rv, Tv = _kv8_rows(cache, v, "v", cache.kv_heads, True)
     if T != Tv or rk.type != rv.type:
         raise Csa2Error("k and v: one T and one type")
     nl = _kv8_arg(cache, new_len, "new_len", "int32", (cache.batch,))
     sp = _kv8_arg(cache, start, "start", "int32", (cache.batch,))
-    w = _kv8_ws(cache, ws)
-    with _On(cache, stream) as s:
-        _check(_kv8_append(ctypes.byref(cache.struct), ctypes.byref(rk), ctypes.byref(rv), T, nl,
-                           sp, w, s), "csa2_kv8_append")
+    _kv8_run(cache, "csa2_kv8_append", _kv8_append, stream, ctypes.byref(cache.struct),
+             ctypes.byref(rk), ctypes.byref(rv), T, nl, sp, _kv8_ws(cache, ws))
 
 
 def kv8_attn(cache, q, out, ws, lse=None, q_len=None, softmax_scale=0.0, stream=None):
     """Attention of the queries q [batch, T, heads, dim] (bf16 or f16) of each
     sequence's last q_len[b] rows (int32 [batch], default T) over the cache, into
     out (as q) and lse (fp32 [batch, T, heads], optional)."""
-    rq, T = _kv8_rows(cache, q, "q", None)
+    rq, T = _kv8_rows(cache, q, "q")
     H = q.shape[2]
     ro, To = _kv8_rows(cache, out, "out", H)
     if To != T or ro.type != rq.type:
         raise Csa2Error("out: shape and type of q")
     ls = _kv8_arg(cache, lse, "lse", "float32", (cache.batch, T, H))
     ql = _kv8_arg(cache, q_len, "q_len", "int32", (cache.batch,))
-    w = _kv8_ws(cache, ws, T, H)
-    with _On(cache, stream) as s:
-        _check(_kv8_attn(ctypes.byref(cache.struct), ctypes.byref(rq), H, T, ql,
-                         float(softmax_scale), ctypes.byref(ro), ls, w, s), "csa2_kv8_attn")
+    _kv8_run(cache, "csa2_kv8_attn", _kv8_attn, stream, ctypes.byref(cache.struct),
+             ctypes.byref(rq), H, T, ql, softmax_scale, ctypes.byref(ro), ls,
+             _kv8_ws(cache, ws, T, H))
 
 
 def kv8_mass(cache, q, lse, ws, q_len=None, softmax_scale=0.0, decay=1.0, stream=None):
     """cache.mass = decay * cache.mass + the weight that each row got from the
     queries q, given the lse that kv8_attn returned for them."""
-    rq, T = _kv8_rows(cache, q, "q", None)
+    rq, T = _kv8_rows(cache, q, "q")
     H = q.shape[2]
     if cache.mass is None or lse is None:
         raise Csa2Error("csa2_kv8_mass: the cache holds no mass, or no lse given")
     ls = _kv8_arg(cache, lse, "lse", "float32", (cache.batch, T, H))
     ql = _kv8_arg(cache, q_len, "q_len", "int32", (cache.batch,))
-    w = _kv8_ws(cache, ws, T, H)
-    with _On(cache, stream) as s:
-        _check(_kv8_mass(ctypes.byref(cache.struct), ctypes.byref(rq), H, T, ql, ls,
-                         float(softmax_scale), float(decay), w, s), "csa2_kv8_mass")
+    _kv8_run(cache, "csa2_kv8_mass", _kv8_mass, stream, ctypes.byref(cache.struct),
+             ctypes.byref(rq), H, T, ql, ls, softmax_scale, decay, _kv8_ws(cache, ws, T, H))
 
 
 def kv8_evict(cache, keep, sink, recent, kept, ws, dst=None, stream=None):
@@ -522,8 +530,6 @@ def kv8_evict(cache, keep, sink, recent, kept, ws, dst=None, stream=None):
         raise Csa2Error("csa2_kv8_evict: it takes `kept`, and a cache with mass")
     if dst is not None and dst.device != cache.device:
         raise Csa2Error(f"dst: on {dst.device}, the cache on {cache.device}")
-    w = _kv8_ws(cache, ws)
-    with _On(cache, stream) as s:
-        _check(_kv8_evict(ctypes.byref(cache.struct),
-                          ctypes.byref(dst.struct) if dst is not None else None, keep, sink,
-                          recent, kp, w, s), "csa2_kv8_evict")
+    _kv8_run(cache, "csa2_kv8_evict", _kv8_evict, stream, ctypes.byref(cache.struct),
+             None if dst is None else ctypes.byref(dst.struct), keep, sink, recent, kp,
+             _kv8_ws(cache, ws))

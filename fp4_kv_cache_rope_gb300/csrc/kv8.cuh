@@ -12,12 +12,15 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "codec.cuh"
 #include "launch.h"
 
 namespace csa2 {
 
 constexpr int kKv8Ctas = 512;      // upper bound of the split kernels' CTAs
+constexpr int kKv8SplitCtas = 256; // upper bound of the CTAs of a split prefill
 constexpr int kKv8SlotRows = 32;   // query rows of one partial result
 constexpr int kKv8Step = 128;      // cached rows of one step of a CTA
 
@@ -208,6 +211,38 @@ __device__ __forceinline__ int kv8_find(const Kv8& c, int lane, int units, int64
 }
 
 // ------------------------------------------------------------------ launchers
+constexpr int kKv8Devices = 64;
+
+// Gives the kernel `smem` dynamic bytes and the largest shared-memory carveout;
+// the attributes stay with the device, so once per device and kernel (`seen` is
+// the kernel's).  Setting them again, from another thread too, does no harm.
+template <typename Kernel>
+inline cudaError_t kv8_prepare(Kernel kern, int smem, std::atomic<uint64_t>& seen) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < kKv8Devices ? 1ull << dev : 0;
+  if (seen.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = prefer_max_shared(kern);
+  if (e == cudaSuccess) seen.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+// One launch that may overlap the tail of the previous one of its stream.
+template <typename... A>
+inline cudaError_t kv8_launch(void (*kern)(A...), dim3 grid, int threads, size_t smem,
+                              cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 struct Kv8Rows {          // rows [B, T, heads, D] with element strides
   const void* data;
   int64_t sb, st, sh;
@@ -225,6 +260,8 @@ struct Kv8Attn {
   uint32_t* status;
 };
 size_t kv8_part_bytes(int D);
+size_t kv8_prefill_part_bytes(int D);
+cudaError_t launch_kv8_prefill(const Kv8Attn& a, int num_sms, cudaStream_t s);
 cudaError_t launch_kv8_append(const Kv8& c, int D, const Kv8Rows& k, const Kv8Rows& v, int T,
                               const int32_t* new_len, const int32_t* start, uint32_t* status,
                               cudaStream_t s);

@@ -2,6 +2,8 @@
 // Every entry point returns a csa2_status and never throws.
 #include <math.h>
 
+#include <atomic>
+
 #include "kv8.cuh"
 
 using namespace csa2;
@@ -66,14 +68,19 @@ Kv8Rows rows_of(const csa2_rows& r) {
   return Kv8Rows{r.data, r.stride_b, r.stride_t, r.stride_h, r.type};
 }
 
-// SMs of the current device.
+// SMs of the current device, looked up once per device.
 int sms() {
+  static std::atomic<int> known[kKv8Devices];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
+  if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
+  if (dev >= 0 && dev < kKv8Devices && (n = known[dev].load(std::memory_order_relaxed)) > 0)
+    return n;
+  if (dev < 0 ||
       cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
     cudaGetLastError();
-    n = 148;
+    return 148;
   }
+  if (dev < kKv8Devices) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -90,13 +97,14 @@ Kv8Ws kv8_ws(const csa2_kv8_cache* c) {
   Kv8Ws w{};
   w.old_len = 256;
   w.part = align256(w.old_len + 4 * (size_t)c->batch);
-  w.total = align256(w.part + kv8_part_bytes(c->dim));
+  const size_t few = kv8_part_bytes(c->dim), many = kv8_prefill_part_bytes(c->dim);
+  w.total = align256(w.part + (few > many ? few : many));
   return w;
 }
 
 bool heads_ok(const csa2_kv8_cache* c, int32_t T, int32_t H) {
   return H > 0 && H % c->kv_heads == 0 && H <= 65536 && T >= 0 && T <= CSA2_MAX_LEN &&
-         (int64_t)c->batch * H * (T + 1) <= (int64_t)1 << 31;
+         (int64_t)c->batch * H * (T + 1) < (int64_t)1 << 31;
 }
 
 Kv8Attn attn_of(const csa2_kv8_cache* c, const csa2_rows* q, int32_t H, int32_t T,
@@ -151,7 +159,10 @@ csa2_status csa2_kv8_attn(const csa2_kv8_cache* cache, const csa2_rows* q, int32
   Kv8Attn a = attn_of(cache, q, H, T, q_len, softmax_scale, ws);
   a.out = rows_of(*out);
   a.lse = lse;
-  return done(launch_kv8_attn(a, sms(), (cudaStream_t)stream));
+  // Up to 64 query rows per (sequence, K/V head) the bytes of the cache bound
+  // the call; above that the tensor cores do.
+  return done(a.T * a.G <= 64 ? launch_kv8_attn(a, sms(), (cudaStream_t)stream)
+                              : launch_kv8_prefill(a, sms(), (cudaStream_t)stream));
 }
 
 csa2_status csa2_kv8_mass(const csa2_kv8_cache* cache, const csa2_rows* q, int32_t H, int32_t T,

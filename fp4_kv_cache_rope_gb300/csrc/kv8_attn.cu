@@ -661,29 +661,15 @@ __global__ void __launch_bounds__(kThreads) kv8_mass_kernel(DecodeParams p) {
   }
 }
 
-template <typename... A>
-cudaError_t launch(void (*kern)(A...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1] = {pdl_attribute()};
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 template <int D, int MT, int FMT>
 cudaError_t decode_as(const DecodeParams& p, cudaStream_t s) {
   auto kern = kv8_decode_kernel<D, MT, FMT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       DecodeSmem<D>::kBytes);
-  if (e == cudaSuccess) e = prefer_max_shared(kern);
+  static std::atomic<uint64_t> seen;
+  cudaError_t e = kv8_prepare(kern, DecodeSmem<D>::kBytes, seen);
   if (e != cudaSuccess) return e;
-  e = launch(kern, dim3(p.ctas), kThreads, DecodeSmem<D>::kBytes, s, p);
+  e = kv8_launch(kern, dim3(p.ctas), kThreads, DecodeSmem<D>::kBytes, s, p);
   if (e != cudaSuccess) return e;
-  return launch(kv8_combine_kernel<D>, dim3(p.a.c.batch * p.a.c.heads * p.tiles, 16 * MT), D, 0, s, p,
+  return kv8_launch(kv8_combine_kernel<D>, dim3(p.a.c.batch * p.a.c.heads * p.tiles, 16 * MT), D, 0, s, p,
                 16 * MT);
 }
 template <int D, int FMT>
@@ -694,7 +680,7 @@ cudaError_t decode_of(DecodeParams p, cudaStream_t s) {
 }
 template <int D, int FMT>
 cudaError_t mass_as(const DecodeParams& p, cudaStream_t s) {
-  return launch(kv8_mass_kernel<D, FMT>, dim3(p.ctas), kThreads, 0, s, p);
+  return kv8_launch(kv8_mass_kernel<D, FMT>, dim3(p.ctas), kThreads, 0, s, p);
 }
 
 }  // namespace

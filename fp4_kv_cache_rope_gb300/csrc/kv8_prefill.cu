@@ -1,0 +1,646 @@
+// Attention over the 8-bit K/V cache for many query rows (prompts, chunks of
+// prompts) on the tcgen05 tensor cores.
+//
+// A CTA takes 256 query rows of one (sequence, K/V head): token-major rows
+// (token, head of the group), two M = 128 tiles.  It walks the cached rows in
+// tiles of 128:
+//
+//   S = Q K^T      M 128 x N 128 x K D, f16 operands from shared memory;
+//   P = 2^(S - m)  by the softmax warps, one thread per query row, written to
+//                  tensor memory over S as f16;
+//   O += P V       A = P from tensor memory, B = V (row-major as it lies).
+//
+// With both query tiles in flight the tensor cores work on one while the
+// exponentials of the other are taken.  The arithmetic per cached byte is
+// 256 rows' worth, so the tensor cores (4 D flop per query row and cached row)
+// bound it; converting a tile's codes to f16 is paid once per 256 query rows.
+//
+// Exactness.  Queries are scaled per row by a power of two into f16's range;
+// codes are converted to f16 times their block's scale over the largest scale
+// in the CTA's range (both powers of two), so one factor per query row, and
+// none per cached row, is left for the softmax.  A block whose scale is 2^12
+// below the largest still keeps every bit; below that a value is off by at most
+// 2^-25 of that largest scale, i.e. by 2^-31 of the range's largest value.
+// The running maximum is raised only when a logit exceeds it by 2^8 (the rare
+// rescaling of O stays off the common path), and P is taken times 2^7: at most
+// 2^15, with f16's full precision down to 2^-21.  l is summed in fp32 from the
+// unrounded weights.
+//
+// Warps (416 threads): 0-3 and 4-7 softmax of query tile 0 and 1; 8-11 turn the
+// cache's codes into f16 tiles, from registers loaded one tile ahead (no raw
+// copy in shared memory, whose bandwidth the MMAs need); 12 issues the MMAs.
+#include "kv8.cuh"
+
+namespace csa2 {
+namespace {
+
+constexpr int kTileKeys = 128;
+constexpr int kTileRows = 256;
+constexpr int kThreads = 416;
+
+template <int D>
+struct PreSmem {
+  static constexpr int kSlab = 128 * 128;            // [128 rows x 64 channels] f16, swizzled
+  static constexpr int kSlabs = D / 64;
+  static constexpr int kQ = 0;                       // 2 query tiles
+  static constexpr int kK = kQ + 2 * kSlabs * kSlab; // 2 stages
+  static constexpr int kV = kK + 2 * kSlabs * kSlab;
+  static constexpr int kMisc = kV + 2 * kSlabs * kSlab;
+  static constexpr int kBars = kMisc;                // 32 mbarriers
+  static constexpr int kFlags = kMisc + 256;         // abort, tmem, tile masks [4], reduce [8]
+  // tensor memory holds one CTA, so a second is kept off the SM
+  static constexpr int kBytes = kMisc + 512 < 120 * 1024 ? 120 * 1024 : kMisc + 512;
+};
+
+struct PreParams {
+  Kv8Attn a;
+  int32_t rows, row_tiles, splits;
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void reg_fence32(uint32_t (&r)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+// D[tmem] (+)= A[tmem] * B[smem]^T, f16 operands, fp32 accumulate.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ void st_swizzled(uint8_t* slab, int row, int chunk, uint4 v) {
+  *reinterpret_cast<uint4*>(slab + row * 128 + ((chunk ^ (row & 7)) << 4)) = v;
+}
+__device__ __forceinline__ void bar_sync(int id, int n) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
+  using L = PreSmem<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Kv8& c = p.a.c;
+  if ((smem_u32(smem) & 1023u) != 0) {
+    if (tid == 0) set_status(p.a.status, CSA2_DEV_BAD_ALIGN);
+    return;
+  }
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
+  uint64_t* q_ready = bars;          // 8 warps
+  uint64_t* k_full = bars + 1;       // [2] 4 warps
+  uint64_t* k_empty = bars + 3;      // [2] commit
+  uint64_t* v_full = bars + 5;       // [2] 4 warps
+  uint64_t* v_empty = bars + 7;      // [2] commit
+  uint64_t* s_full = bars + 9;       // [2 query tiles] commit
+  uint64_t* p_full = bars + 11;      // [2] 4 warps
+  uint64_t* pv_done = bars + 13;     // [2] commit
+  uint64_t* drain = bars + 15;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kFlags);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kFlags + 4);
+  volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + L::kFlags + 8);
+  float* red = reinterpret_cast<float*>(smem + L::kFlags + 32);     // [4][2]
+
+  if (tid == 0) {
+    mbar_init(q_ready, 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(k_full + i, 4);
+      mbar_init(k_empty + i, 1);
+      mbar_init(v_full + i, 4);
+      mbar_init(v_empty + i, 1);
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + i, 4);
+      mbar_init(pv_done + i, 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 12) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // ---- this CTA's share: heads fastest, then key splits, sequences, row tiles
+  // (the last rows, which see the most keys, first)
+  int id = blockIdx.x;
+  const int h = id % c.heads;
+  id /= c.heads;
+  const int split = id % p.splits;
+  id /= p.splits;
+  const int b = id % c.batch;
+  const int rt = p.row_tiles - 1 - id / c.batch;
+  const int n = kv8_len(c, b);
+  int ql = p.a.q_len ? p.a.q_len[b] : p.a.T;
+  ql = ql < 0 ? 0 : (ql > p.a.T ? p.a.T : ql);
+  const int row0 = rt * kTileRows;
+  const int rows = min(kTileRows, ql * p.a.G - row0);       // <= 0: nothing to do
+  const int last_tok = rows > 0 ? (row0 + rows - 1) / p.a.G : 0;
+  const int keys = rows > 0 ? max(0, min(n, n - ql + last_tok + 1)) : 0;
+  const int all_tiles = (keys + kTileKeys - 1) / kTileKeys;
+  const int t0 = (int)((int64_t)all_tiles * split / p.splits);
+  const int nt = (int)((int64_t)all_tiles * (split + 1) / p.splits) - t0;
+  const int mts = rows > 128 ? 2 : 1;                       // query tiles with rows
+
+  // ---- largest scales in the range (a power of two; 0 when all are)
+  if (warp < 4) {
+    float mx[2] = {0.0f, 0.0f};
+    const int blk = 1 << c.block_shift;
+    const int end = min(keys, (t0 + nt) * kTileKeys);
+    for (int pos = t0 * kTileKeys / blk * blk + tid * blk; pos < end; pos += 128 * blk) {
+      int in_page;
+      const int page = kv8_page(c, b, pos, in_page);
+      if (page < 0) continue;
+      const int64_t at = kv8_block(c, page, h, in_page);
+      mx[0] = fmaxf(mx[0], c.scales[0][at]);
+      mx[1] = fmaxf(mx[1], c.scales[1][at]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
+      mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
+    }
+    if (lane == 0) {
+      red[2 * warp] = mx[0];
+      red[2 * warp + 1] = mx[1];
+    }
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const float kref = fmaxf(fmaxf(red[0], red[2]), fmaxf(red[4], red[6]));
+  const float vref = fmaxf(fmaxf(red[1], red[3]), fmaxf(red[5], red[7]));
+  bool ok = true;   // this thread's view: false once a wait gave up
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (ok && !mbar_wait(bar, parity, abort_flag)) ok = false;
+    ok = __all_sync(0xffffffffu, ok);
+  };
+
+  if (warp < 8) {
+    // ============================================================ softmax warps
+    const int mt = warp >> 2;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t tS = tmem + lanes + 128 * mt, tO = tmem + lanes + 256 + D * mt;
+    const int r = 128 * mt + 32 * (warp & 3) + lane;       // this thread's query row
+    const int gr = row0 + r, tok = gr / p.a.G, hd = h * p.a.G + gr % p.a.G;
+    const bool real = r < rows;
+    const int lim = real ? min(n, n - ql + tok + 1) : 0;
+    float mul = 0.0f;
+    if (nt > 0) {
+      // the row as f16 in the swizzled tile
+      const uint4* src = reinterpret_cast<const uint4*>(
+          static_cast<const char*>(p.a.q.data) +
+          2 * (b * p.a.q.sb + tok * p.a.q.st + hd * p.a.q.sh));
+      float amax = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 w = real ? src[i] : make_uint4(0, 0, 0, 0);
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float x, y;
+          if (p.a.q.type == CSA2_BF16) {
+            bf16x2_to_f32(ww[j], x, y);
+          } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&ww[j]));
+            x = f.x;
+            y = f.y;
+          }
+          amax = fmaxf(amax, fmaxf(fabsf(x), fabsf(y)));
+        }
+      }
+      const int e = (int)(__float_as_uint(amax) >> 23);
+      const int shift = e == 0 || e == 255 ? 0 : 134 - e;
+      const float up = __uint_as_float((uint32_t)(127 + (shift > 127 ? 127 : shift)) << 23);
+      // (kept above zero: hidden columns are -inf times it)
+      mul = fmaxf(p.a.scale_log2 / up * (kref > 0.0f ? kref : 1.0f), 1.2e-38f);
+      uint8_t* tile = smem + L::kQ + mt * L::kSlabs * L::kSlab;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 w = real ? src[i] : make_uint4(0, 0, 0, 0);
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float x, y;
+          if (p.a.q.type == CSA2_BF16) {
+            bf16x2_to_f32(ww[j], x, y);
+          } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&ww[j]));
+            x = f.x;
+            y = f.y;
+          }
+          o[j] = pack16(x * up, y * up, CSA2_F16);
+        }
+        st_swizzled(tile + (i >> 3) * L::kSlab, r & 127, i & 7, make_uint4(o[0], o[1], o[2], o[3]));
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_ready);
+    }
+
+    float m = -INFINITY, l = 0.0f;
+    for (int i = 0; mt < mts && i < nt; ++i) {
+      wait(s_full + mt, i & 1);
+      tc_fence_after();
+      if (!ok) break;
+      // written before the tile's K was handed over, and not written again
+      // before QK of tile i + 1, which waits for this tile's P
+      const uint32_t groups = masks[i & 3];
+      const int key0 = (t0 + i) * kTileKeys;
+      const bool masked = groups != 0xFFu || __any_sync(0xffffffffu, lim < key0 + kTileKeys);
+      uint32_t s[32];
+      // whether column j of 32-column part u is hidden
+      auto hide = [&](int u) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (key0 + 32 * u + j >= lim || !((groups >> (2 * u + (j >> 4))) & 1u))
+            s[j] = 0xFF800000u;
+      };
+      float top = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        tmem_ld32(tS + 32 * u, s);
+        tmem_ld_wait();
+        reg_fence32(s);
+        if (masked) hide(u);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(s[j]));
+      }
+      top *= mul;
+      if (__any_sync(0xffffffffu, top > m + 8.0f)) {
+        const float up = fmaxf(m, top);
+        const float alpha = m == -INFINITY ? 0.0f : kv8_exp2(m - up);
+        l *= alpha;
+        m = up;
+        if (i > 0) {
+          wait(pv_done + mt, (i - 1) & 1);
+          tc_fence_after();
+          if (!ok) break;
+#pragma unroll 1
+          for (int u = 0; u < D / 32; ++u) {
+            tmem_ld32(tO + 32 * u, s);
+            tmem_ld_wait();
+            reg_fence32(s);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) * alpha);
+            tmem_st32(tO + 32 * u, s);
+          }
+          tmem_st_wait();
+        }
+      }
+      // One fused multiply-add gives the exponent: m's own rounding is then the
+      // same for the whole row and cancels in P / l.  Where m is so large that
+      // it would carry P out of range (ulp(2^16) = 2^-7), the logits are rounded
+      // like m, which makes the largest difference 0 again.
+      const bool plain = !masked && !__any_sync(0xffffffffu, fabsf(m) > 65536.0f);
+      const float mm = m == -INFINITY ? 0.0f : m, use = mm - 7.0f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        tmem_ld32(tS + 32 * u, s);
+        tmem_ld_wait();
+        reg_fence32(s);
+        if (plain) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            s[j] = __float_as_uint(fmaf(__uint_as_float(s[j]), mul, -use));
+        } else {
+          hide(u);
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            s[j] = __float_as_uint((__fmul_rn(__uint_as_float(s[j]), mul) - mm) + 7.0f);
+        }
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float x = kv8_exp2(__uint_as_float(s[2 * j]));
+          const float y = kv8_exp2(__uint_as_float(s[2 * j + 1]));
+          l += x;
+          l += y;
+          w[j] = pack16(x, y, CSA2_F16);
+        }
+        tmem_st16(tS + 16 * u, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full + mt);
+    }
+    // ---- the row's result
+    if (nt > 0 && mt < mts) wait(pv_done + mt, (nt - 1) & 1);
+    tc_fence_after();
+    const bool empty = l == 0.0f;
+    const float base2 = empty ? -INFINITY : m + log2f(l) - 7.0f;
+    if (p.splits == 1) {
+      const float f = empty ? 0.0f : vref / l;
+      uint16_t* out = static_cast<uint16_t*>(const_cast<void*>(p.a.out.data)) + b * p.a.out.sb +
+                      tok * p.a.out.st + hd * p.a.out.sh;
+#pragma unroll
+      for (int u = 0; u < D / 32; ++u) {
+        uint32_t s[32];
+        if (nt > 0 && mt < mts && ok) {
+          tmem_ld32(tO + 32 * u, s);
+          tmem_ld_wait();
+          reg_fence32(s);
+        }
+        if (!real || !ok) continue;
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            w[q] = empty ? 0u
+                         : pack16(__uint_as_float(s[j + 2 * q]) * f,
+                                  __uint_as_float(s[j + 2 * q + 1]) * f, p.a.out.type);
+          *reinterpret_cast<uint4*>(out + 32 * u + j) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      if (real && ok && p.a.lse)
+        p.a.lse[((int64_t)b * p.a.T + tok) * p.a.H + hd] =
+            empty ? -INFINITY : base2 * 0.6931471805599453f;
+    } else {
+      float* part = p.a.part + (int64_t)blockIdx.x * kTileRows * (D + 2);
+      const float f = empty ? 0.0f : vref;
+#pragma unroll
+      for (int u = 0; u < D / 32; ++u) {
+        uint32_t s[32];
+        if (nt > 0 && mt < mts && ok) {
+          tmem_ld32(tO + 32 * u, s);
+          tmem_ld_wait();
+          reg_fence32(s);
+        }
+        if (!real || !ok) continue;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4)
+          *reinterpret_cast<float4*>(part + r * D + 32 * u + j) =
+              empty ? make_float4(0, 0, 0, 0)
+                    : make_float4(__uint_as_float(s[j]) * f, __uint_as_float(s[j + 1]) * f,
+                                  __uint_as_float(s[j + 2]) * f, __uint_as_float(s[j + 3]) * f);
+      }
+      if (real) {
+        part[kTileRows * D + r] = m;
+        part[kTileRows * (D + 1) + r] = ok ? l : 0.0f;
+      }
+    }
+  } else if (warp < 12) {
+    // ========================================================== converter warps
+    // Thread: 16-byte chunk cc (of a 64-channel half) of rows r4 + 32 v.  Eight
+    // neighbouring lanes then store to two rows' chunks of all eight positions.
+    const int ct = tid - 256, cc = ct & 3, r4 = ct >> 2;
+    constexpr int kPer = L::kSlabs * 4;
+    const float kinv = kv8_inverse(kref), vinv = kv8_inverse(vref);
+    // lanes 0..7: the tile's eight 16-row groups
+    int64_t grow = -1;
+    float gk = 0.0f, gv = 0.0f;
+    auto resolve = [&](int i) {
+      grow = -1;
+      gk = gv = 0.0f;
+      const int pos = (t0 + i) * kTileKeys + 16 * (lane & 7);
+      if (i < nt && pos < keys) {
+        int in_page;
+        const int page = kv8_page(c, b, pos, in_page);
+        if (page >= 0) {
+          grow = kv8_row(c, page, h, in_page);
+          const int64_t at = kv8_block(c, page, h, in_page);
+          gk = c.scales[0][at] * kinv;
+          gv = c.scales[1][at] * vinv;
+        } else if (lane < 8) {
+          set_status(p.a.status, CSA2_DEV_BAD_PAGE);
+        }
+      }
+    };
+    uint4 raw[2][kPer];
+    float fac[2][4];
+    auto load = [&](int side, int i) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int row = r4 + 32 * v;
+        const int64_t g = __shfl_sync(0xffffffffu, grow, row >> 4);
+        fac[side][v] = __shfl_sync(0xffffffffu, side ? gv : gk, row >> 4);
+        // rows the CTA does not see stay 0: their scales are not in the range
+        const bool in = g >= 0 && (t0 + i) * kTileKeys + row < keys;
+        const uint8_t* from = c.codes[side] + (g + (row & 15)) * D + 16 * cc;
+#pragma unroll
+        for (int s = 0; s < L::kSlabs; ++s) {
+          raw[side][s * 4 + v] = make_uint4(0, 0, 0, 0);
+          if (in) raw[side][s * 4 + v] = *reinterpret_cast<const uint4*>(from + 64 * s);
+        }
+      }
+    };
+    auto convert = [&](int side, uint8_t* tile) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const __half2 f = __float2half2_rn(fac[side][v]);
+#pragma unroll
+        for (int s = 0; s < L::kSlabs; ++s) {
+          const uint4 w = raw[side][s * 4 + v];
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+          uint32_t o[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t a0, a1;
+            kv8_to_f16<FMT>(ww[j], a0, a1);
+            __half2 x = __hmul2(*reinterpret_cast<__half2*>(&a0), f);
+            __half2 y = __hmul2(*reinterpret_cast<__half2*>(&a1), f);
+            o[2 * j] = *reinterpret_cast<uint32_t*>(&x);
+            o[2 * j + 1] = *reinterpret_cast<uint32_t*>(&y);
+          }
+          const int row = r4 + 32 * v;
+          st_swizzled(tile + s * L::kSlab, row, 2 * cc, make_uint4(o[0], o[1], o[2], o[3]));
+          st_swizzled(tile + s * L::kSlab, row, 2 * cc + 1, make_uint4(o[4], o[5], o[6], o[7]));
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+    };
+    // K and V of the next tile are loaded as soon as this tile's registers are
+    // free, their pages and scales one tile earlier still
+    uint32_t good = 0, good_next = 0;
+    if (nt > 0) {
+      resolve(0);
+      load(0, 0);
+      load(1, 0);
+      good = __ballot_sync(0xffffffffu, grow >= 0) & 0xFFu;
+      resolve(1);
+    }
+    for (int i = 0; i < nt; ++i) {
+      const int st = i & 1;
+      if (i >= 2) wait(k_empty + st, ((i >> 1) - 1) & 1);
+      if (!ok) break;
+      convert(0, smem + L::kK + st * L::kSlabs * L::kSlab);
+      if (warp == 8 && lane == 0) masks[i & 3] = good;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(k_full + st);
+      if (i + 1 < nt) load(0, i + 1);
+      if (i >= 2) wait(v_empty + st, ((i >> 1) - 1) & 1);
+      if (!ok) break;
+      convert(1, smem + L::kV + st * L::kSlabs * L::kSlab);
+      if (lane == 0) mbar_arrive(v_full + st);
+      if (i + 1 < nt) {
+        load(1, i + 1);
+        good_next = __ballot_sync(0xffffffffu, grow >= 0) & 0xFFu;
+        resolve(i + 2);
+      }
+      good = good_next;
+    }
+  } else if (lane == 0 && nt > 0) {
+    // ================================================================ MMA thread
+    constexpr uint32_t idesc_qk = instr_desc(0, 0, false, false, 128, 128);
+    constexpr uint32_t idesc_pv = instr_desc(0, 0, false, true, 128, D);
+    const uint64_t qd = smem_desc(smem_u32(smem + L::kQ), 16, 1024, 2);
+    const uint64_t kd = smem_desc(smem_u32(smem + L::kK), 16, 1024, 2);
+    const uint64_t vd = smem_desc(smem_u32(smem + L::kV), L::kSlab, 1024, 2);
+    constexpr uint64_t kTileDesc = L::kSlabs * L::kSlab / 16;
+    auto qk = [&](int mt, int st) {
+#pragma unroll
+      for (int s = 0; s < L::kSlabs; ++s)
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_f16(tmem + 128 * mt, qd + mt * kTileDesc + (s * L::kSlab + kk * 32) / 16,
+                  kd + st * kTileDesc + (s * L::kSlab + kk * 32) / 16, idesc_qk, (s | kk) ? 1u : 0u);
+    };
+    bool issued = false;
+    ok = mbar_wait(q_ready, 0, abort_flag) && mbar_wait(k_full, 0, abort_flag);
+    if (ok) {
+      tc_fence_after();
+      issued = true;
+      for (int mt = 0; mt < mts; ++mt) {
+        qk(mt, 0);
+        mma_commit(s_full + mt);
+      }
+      mma_commit(k_empty);
+    }
+    for (int i = 0; ok && i < nt; ++i) {
+      const int st = i & 1, sn = st ^ 1;
+      for (int mt = 0; ok && mt < mts; ++mt) {
+        ok = mbar_wait(p_full + mt, i & 1, abort_flag) &&
+             mbar_wait(v_full + st, (i >> 1) & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_f16_ts(tmem + 256 + D * mt, tmem + 128 * mt + 8 * kk,
+                     vd + st * kTileDesc + kk * 2048 / 16, idesc_pv, (i | kk) ? 1u : 0u);
+        mma_commit(pv_done + mt);
+        if (mt == mts - 1) mma_commit(v_empty + st);
+        if (i + 1 < nt) {
+          ok = mbar_wait(k_full + sn, ((i + 1) >> 1) & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          qk(mt, sn);
+          mma_commit(s_full + mt);
+          if (mt == mts - 1) mma_commit(k_empty + sn);
+        }
+      }
+    }
+    if (issued) {   // let every issued MMA land before tensor memory is freed
+      mma_commit(drain);
+      mbar_wait_drain(drain, 0);
+    }
+  }
+  __syncwarp();
+  if (!ok) set_status(p.a.status, CSA2_DEV_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the key splits of a query row: one warp per row.
+template <int D>
+__global__ void __launch_bounds__(256) kv8_prefill_combine_kernel(PreParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const Kv8& c = p.a.c;
+  const int lane = threadIdx.x & 31, h = blockIdx.y % c.heads, b = blockIdx.y / c.heads;
+  const int gr = blockIdx.x * 8 + (threadIdx.x >> 5);
+  int ql = p.a.q_len ? p.a.q_len[b] : p.a.T;
+  ql = ql < 0 ? 0 : (ql > p.a.T ? p.a.T : ql);
+  if (gr >= ql * p.a.G) return;
+  const int rt = gr / kTileRows, r = gr % kTileRows;
+  const int tok = gr / p.a.G, hd = h * p.a.G + gr % p.a.G;
+  constexpr int kPer = D / 32;
+  float top = -INFINITY, l = 0.0f, o[kPer] = {};
+  for (int s = 0; s < p.splits; ++s) {
+    const int64_t id =
+        (((int64_t)(p.row_tiles - 1 - rt) * c.batch + b) * p.splits + s) * c.heads + h;
+    const float* part = p.a.part + id * kTileRows * (D + 2);
+    const float m = part[kTileRows * D + r], pl = part[kTileRows * (D + 1) + r];
+    if (pl == 0.0f) continue;
+    const float nt = fmaxf(top, m);
+    const float f = kv8_exp2(top - nt), fm = kv8_exp2(m - nt);
+    l = l * f + pl * fm;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) o[i] = o[i] * f + part[r * D + kPer * lane + i] * fm;
+    top = nt;
+  }
+  uint16_t* out = static_cast<uint16_t*>(const_cast<void*>(p.a.out.data)) + b * p.a.out.sb +
+                  tok * p.a.out.st + hd * p.a.out.sh + kPer * lane;
+  const float f = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+  for (int i = 0; i < kPer; i += 2)
+    *reinterpret_cast<uint32_t*>(out + i) = pack16(o[i] * f, o[i + 1] * f, p.a.out.type);
+  if (p.a.lse && lane == 0)
+    p.a.lse[((int64_t)b * p.a.T + tok) * p.a.H + hd] =
+        l == 0.0f ? -INFINITY : (top + log2f(l) - 7.0f) * 0.6931471805599453f;
+}
+
+template <int D, int FMT>
+cudaError_t prefill_as(const PreParams& p, cudaStream_t s) {
+  auto kern = kv8_prefill_kernel<D, FMT>;
+  static std::atomic<uint64_t> seen;
+  cudaError_t e = kv8_prepare(kern, PreSmem<D>::kBytes, seen);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = (int64_t)p.a.c.heads * p.splits * p.a.c.batch * p.row_tiles;
+  e = kv8_launch(kern, dim3((unsigned)grid), kThreads, PreSmem<D>::kBytes, s, p);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  return kv8_launch(kv8_prefill_combine_kernel<D>,
+                    dim3((p.rows + 7) / 8, p.a.c.heads * p.a.c.batch), 256, 0, s, p);
+}
+
+}  // namespace
+
+size_t kv8_prefill_part_bytes(int D) { return (size_t)kKv8SplitCtas * kTileRows * (D + 2) * 4; }
+
+cudaError_t launch_kv8_prefill(const Kv8Attn& a, int num_sms, cudaStream_t s) {
+  PreParams p{a, a.T * a.G, (a.T * a.G + kTileRows - 1) / kTileRows, 1};
+  // Fewer CTAs than SMs: the cached rows are split, into parts of at least 8 tiles.
+  const int64_t base = (int64_t)a.c.heads * a.c.batch * p.row_tiles;
+  const int limit = num_sms < kKv8SplitCtas ? num_sms : kKv8SplitCtas;
+  if (2 * base <= limit) {
+    const int most = (a.c.max_len + 8 * kTileKeys - 1) / (8 * kTileKeys);
+    p.splits = (int)(limit / base) < most ? (int)(limit / base) : most;
+  }
+  if (a.c.format == CSA2_KV8_E4M3)
+    return a.D == 64 ? prefill_as<64, CSA2_KV8_E4M3>(p, s) : prefill_as<128, CSA2_KV8_E4M3>(p, s);
+  return a.D == 64 ? prefill_as<64, CSA2_KV8_INT8>(p, s) : prefill_as<128, CSA2_KV8_INT8>(p, s);
+}
+
+cudaError_t set_wait_limit_kv8(unsigned long long ns) { return set_wait_limit_here(ns); }
+
+}  // namespace csa2

@@ -208,34 +208,21 @@ __global__ void kv8_advance_kernel(AppendParams p) {
   p.c.seq_len[b] = sp.start + sp.t;
 }
 
-template <typename... A>
-cudaError_t launch(void (*kern)(A...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1] = {pdl_attribute()};
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 template <int D, int ES, int FMT>
 cudaError_t append_as(const AppendParams& p0, cudaStream_t s) {
   AppendParams p = p0;
   if (p.T <= kFewRows) {
     const int warps = 2 * p.c.heads < 32 ? 2 * p.c.heads : 32;
-    return launch(kv8_append_few_kernel<D, ES, FMT>, dim3(p.c.batch), dim3(32 * warps), 0, s, p);
+    return kv8_launch(kv8_append_few_kernel<D, ES, FMT>, dim3(p.c.batch), 32 * warps, 0, s, p);
   }
   const int block = 1 << p.c.block_shift;
   // with `start` given nothing in the launch reads seq_len, so it may write it
   p.own_len = p.start != nullptr;
-  cudaError_t e = launch(kv8_append_kernel<D, ES, FMT>,
+  cudaError_t e = kv8_launch(kv8_append_kernel<D, ES, FMT>,
                          dim3((p.T + block - 2) / block + 1, 2 * p.c.heads, p.c.batch),
-                         dim3(kAppendThreads), 0, s, p);
+                         kAppendThreads, 0, s, p);
   if (e != cudaSuccess || p.own_len) return e;
-  return launch(kv8_advance_kernel, dim3((p.c.batch + 127) / 128), dim3(128), 0, s, p);
+  return kv8_launch(kv8_advance_kernel, dim3((p.c.batch + 127) / 128), 128, 0, s, p);
 }
 template <int D>
 cudaError_t append_of(const AppendParams& p, cudaStream_t s) {
@@ -458,8 +445,8 @@ __global__ void __launch_bounds__(kMoveThreads) kv8_evict_move_kernel(EvictParam
 template <int D, int FMT>
 cudaError_t move_as(const EvictParams& p, cudaStream_t s) {
   const int blocks = (p.keep + (1 << p.dst.block_shift) - 1) >> p.dst.block_shift;
-  return launch(kv8_evict_move_kernel<D, FMT>,
-                dim3(p.in_place ? 1 : blocks, p.src.heads, p.src.batch), dim3(kMoveThreads), 0, s, p);
+  return kv8_launch(kv8_evict_move_kernel<D, FMT>,
+                dim3(p.in_place ? 1 : blocks, p.src.heads, p.src.batch), kMoveThreads, 0, s, p);
 }
 
 }  // namespace
@@ -475,7 +462,7 @@ cudaError_t launch_kv8_evict(const Kv8& src, const Kv8& dst, bool in_place, int 
                              int sink, int recent, int32_t* kept, int32_t* old_len,
                              uint32_t* status, int num_sms, cudaStream_t s) {
   EvictParams p{src, dst, keep, sink, recent, kept, old_len, status, in_place ? 1 : 0};
-  cudaError_t e = launch(kv8_evict_select_kernel, dim3(src.heads, src.batch), dim3(kSelThreads), 0,
+  cudaError_t e = kv8_launch(kv8_evict_select_kernel, dim3(src.heads, src.batch), kSelThreads, 0,
                          s, p);
   if (e != cudaSuccess) return e;
   if (src.format == CSA2_KV8_E4M3)

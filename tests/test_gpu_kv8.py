@@ -176,6 +176,10 @@ SHAPES = [
     (1, 1, 1, 128, [257], 257, None, 128, 0, "bf16"),
     (1, 8, 20, 64, [200], 70, None, 64, 64, "f16"),
     (1, 2, 1, 64, [640], 520, None, 32, 32, "bf16"),
+    (1, 2, 13, 128, [5000], 5, None, 64, 64, "bf16"),          # 65 rows: key splits
+    (2, 1, 16, 64, [3001, 40], 9, [9, 3], 128, 256, "f16"),    # 144 rows, splits with nothing
+    (3, 2, 8, 128, [0, 1, 700], 33, [33, 20, 0], 16, 48, "bf16"),
+    (2, 1, 2, 128, [1100, 130], 129, None, 64, 0, "f16"),
 ]
 
 
