@@ -178,6 +178,11 @@ __device__ __forceinline__ int64_t kv8_total(const Kv8& c, int lane) {
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
 }
+// CTAs that take part: each has a step at least, so that a unit's CTAs are
+// consecutive and every partial result between them was written by this call.
+__device__ __forceinline__ int kv8_sharers(int64_t total, int ctas) {
+  return total < ctas ? (int)total : ctas;
+}
 // Steps in front of sequence b (of one unit each).
 __device__ __forceinline__ int64_t kv8_before(const Kv8& c, int lane, int b) {
   int64_t s = 0;

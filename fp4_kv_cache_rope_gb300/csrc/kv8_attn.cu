@@ -161,9 +161,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(DecodeParams p)
 
   const int units = c.heads * p.tiles;
   const int64_t total = kv8_total(c, lane) * units;
-  int64_t x = total * blockIdx.x / p.ctas;
-  const int64_t x1 = total * (blockIdx.x + 1) / p.ctas;
-  if (x >= x1) return;
+  const int ctas = kv8_sharers(total, p.ctas);
+  if ((int)blockIdx.x >= ctas) return;
+  int64_t x = total * blockIdx.x / ctas;
+  const int64_t x1 = total * (blockIdx.x + 1) / ctas;
   int64_t first;
   int b = kv8_find(c, lane, units, x, first);
   int n = kv8_len(c, b), steps = kv8_steps(c, b);
@@ -506,21 +507,40 @@ __global__ void __launch_bounds__(D) kv8_combine_kernel(DecodeParams p, int tile
   const int64_t total = kv8_total(c, lane) * units;
   const int steps = kv8_steps(c, b);
   const int64_t x0 = kv8_before(c, lane, b) * units + (int64_t)unit * steps, x1 = x0 + steps;
-  const int c0 = (int)(((x0 + 1) * p.ctas - 1) / total), c1 = (int)((x1 * p.ctas - 1) / total);
+  const int ctas = kv8_sharers(total, p.ctas);
+  const int c0 = (int)(((x0 + 1) * ctas - 1) / total), c1 = (int)((x1 * ctas - 1) / total);
   if (c0 == c1) return;
-  float top = -INFINITY, l = 0.0f, o = 0.0f;
-  for (int i = c0; i <= c1; ++i) {
-    const float* part = p.a.part + (2 * (int64_t)i + (i == c0 ? 1 : 0)) * slot_floats(D);
-    const float m = part[kKv8SlotRows * D + row];
-    const float pl = part[kKv8SlotRows * (D + 1) + row];
-    const float po = part[row * D + threadIdx.x];
-    if (pl == 0.0f) continue;
-    const float nt = fmaxf(top, m);
-    const float f = kv8_exp2(top - nt), fm = kv8_exp2(m - nt);
-    l = l * f + pl * fm;
-    o = o * f + po * fm;
-    top = nt;
+  // the unit began in CTA c0's second slot and went on in the others' first
+  __shared__ float w[kKv8Ctas], red[2][D / 32];
+  const int parts = c1 - c0 + 1;
+  auto slot = [&](int i) { return p.a.part + (2 * (int64_t)(c0 + i) + (i == 0)) * slot_floats(D); };
+  float top = -INFINITY;
+  for (int i = threadIdx.x; i < parts; i += D) {
+    w[i] = slot(i)[kKv8SlotRows * D + row];
+    top = fmaxf(top, w[i]);
   }
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+  if (lane == 0) red[0][threadIdx.x >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) top = fmaxf(top, red[0][k]);
+  float l = 0.0f;
+  for (int i = threadIdx.x; i < parts; i += D) {
+    const float pl = slot(i)[kKv8SlotRows * (D + 1) + row];
+    w[i] = pl == 0.0f ? 0.0f : kv8_exp2(w[i] - top);   // NaN sums stay NaN
+    l += pl == 0.0f ? 0.0f : pl * w[i];
+  }
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+  if (lane == 0) red[1][threadIdx.x >> 5] = l;
+  __syncthreads();
+  l = 0.0f;
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) l += red[1][k];
+  float o = 0.0f;
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) o = fmaf(slot(i)[row * D + threadIdx.x], w[i], o);
   const float y = l == 0.0f ? 0.0f : o / l;
   uint16_t* out = static_cast<uint16_t*>(const_cast<void*>(p.a.out.data)) + b * p.a.out.sb +
                   tok * p.a.out.st + hd * p.a.out.sh + threadIdx.x;
@@ -542,9 +562,10 @@ __global__ void __launch_bounds__(kThreads) kv8_mass_kernel(DecodeParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const int64_t total = kv8_total(c, lane) * c.heads;
-  int64_t x = total * blockIdx.x / p.ctas;
-  const int64_t x1 = total * (blockIdx.x + 1) / p.ctas;
-  if (x >= x1) return;
+  const int ctas = kv8_sharers(total, p.ctas);
+  if ((int)blockIdx.x >= ctas) return;
+  int64_t x = total * blockIdx.x / ctas;
+  const int64_t x1 = total * (blockIdx.x + 1) / ctas;
   int64_t first;
   int b = kv8_find(c, lane, c.heads, x, first);
   int n = kv8_len(c, b), steps = kv8_steps(c, b);

@@ -135,6 +135,7 @@ def run_attention(p, q, G, q_lens=None, scale=0.0, out=None):
     """kv8_attn against the oracle; q [B, T, H, D] on the host."""
     B, T, H, D = q.shape
     ws = p.c.workspace(T, H)
+    ws[256:] = 0xFF          # an earlier call's leavings: NaN
     qd = q.cuda() if q.device.type == "cpu" else q
     out = torch.full((B, T, H, D), 7.0, dtype=q.dtype, device="cuda") if out is None else out
     lse = torch.full((B, T, H), 7.0, device="cuda")
