@@ -104,7 +104,8 @@ csa2_status csa2_set_wait_limit(uint64_t ns) {
   cudaError_t e = set_wait_limit_indexer(v);
   if (e == cudaSuccess) e = set_wait_limit_attention(v);
   if (e == cudaSuccess) e = set_wait_limit_quant(v);
-  if (e == cudaSuccess) e = set_wait_limit_kv8(v);
+  if (e == cudaSuccess) e = set_wait_limit_kv8_prefill(v);
+  if (e == cudaSuccess) e = set_wait_limit_kv8_mass(v);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   return from_cuda(e);
 }

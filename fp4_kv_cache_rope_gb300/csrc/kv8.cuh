@@ -101,8 +101,10 @@ __device__ __forceinline__ uint32_t kv8_encode4(float a, float b, float c, float
 template <int FMT>
 __device__ __forceinline__ void kv8_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if (FMT == CSA2_KV8_E4M3) {
-    lo = e4m3x2_to_f16x2(w & 0xFFFFu);
-    hi = e4m3x2_to_f16x2(w >> 16);
+    asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\n"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
   } else {
     // v + 128 as the low byte of 1024 + (v + 128), then minus 1152
     const uint32_t u = w ^ 0x80808080u;
@@ -259,7 +261,8 @@ struct Kv8Attn {
   float* lse;             // [B, T, H] or null (attention); read by mass
   const int32_t* q_len;   // [B] or null
   int32_t T, H, G, D;
-  float scale_log2;
+  float scale_log2;       // softmax scale * log2(e), and
+  float scale_low;        // what its rounding to fp32 left (mass)
   float decay;            // mass
   float* part;            // partial results
   uint32_t* status;
@@ -271,7 +274,8 @@ cudaError_t launch_kv8_append(const Kv8& c, int D, const Kv8Rows& k, const Kv8Ro
                               const int32_t* new_len, const int32_t* start, uint32_t* status,
                               cudaStream_t s);
 cudaError_t launch_kv8_attn(const Kv8Attn& a, int num_sms, cudaStream_t s);
-cudaError_t launch_kv8_mass(const Kv8Attn& a, int num_sms, cudaStream_t s);
+cudaError_t launch_kv8_mass_few(const Kv8Attn& a, int num_sms, cudaStream_t s);
+cudaError_t launch_kv8_mass_many(const Kv8Attn& a, int num_sms, cudaStream_t s);
 cudaError_t launch_kv8_evict(const Kv8& src, const Kv8& dst, bool in_place, int D, int keep,
                              int sink, int recent, int32_t* kept, int32_t* old_len,
                              uint32_t* status, int num_sms, cudaStream_t s);

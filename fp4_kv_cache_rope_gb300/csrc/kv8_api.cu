@@ -118,7 +118,9 @@ Kv8Attn attn_of(const csa2_kv8_cache* c, const csa2_rows* q, int32_t H, int32_t 
   a.H = H;
   a.G = H / c->kv_heads;
   a.D = c->dim;
-  a.scale_log2 = (scale > 0.0f ? scale : 1.0f / sqrtf((float)c->dim)) * 1.4426950408889634f;
+  const double to2 = (scale > 0.0f ? (double)scale : 1.0 / sqrt((double)c->dim)) * 1.4426950408889634;
+  a.scale_log2 = (float)to2;
+  a.scale_low = (float)(to2 - (double)a.scale_log2);
   a.part = reinterpret_cast<float*>(w + kv8_ws(c).part);
   a.status = reinterpret_cast<uint32_t*>(w);
   return a;
@@ -176,7 +178,9 @@ csa2_status csa2_kv8_mass(const csa2_kv8_cache* cache, const csa2_rows* q, int32
   Kv8Attn a = attn_of(cache, T ? q : nullptr, H, T, q_len, softmax_scale, ws);
   a.lse = const_cast<float*>(lse);
   a.decay = decay;
-  return done(launch_kv8_mass(a, sms(), (cudaStream_t)stream));
+  // Up to 32 query rows per (sequence, K/V head) stay in a warp's registers.
+  return done(T * a.G <= 32 ? launch_kv8_mass_few(a, sms(), (cudaStream_t)stream)
+                            : launch_kv8_mass_many(a, sms(), (cudaStream_t)stream));
 }
 
 csa2_status csa2_kv8_evict(const csa2_kv8_cache* cache, const csa2_kv8_cache* dst, int32_t keep,

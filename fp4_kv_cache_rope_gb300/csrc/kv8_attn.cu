@@ -1,22 +1,27 @@
 // Attention over the 8-bit K/V cache for few query rows, and the weights that
-// each cached row gets.
+// each cached row gets from them.
 //
 //   o_r = sum_j softmax_j(c q_r . k_j) v_j,   k_j = s_K(block) * code,  v_j alike
 //
 // Few query rows share each cached row (the heads of a group times the tokens
 // of the call), so these kernels are bound by the bytes of the cache: 2 D per
 // row and head.  The codes go from shared memory into registers, are converted
-// there to f16 (exact for both formats) and feed mma.sync; a 16-row tile of
-// queries then needs well under half of that pipe's rate at full HBM bandwidth
-// (tcgen05 would need the codes expanded to f16 in shared memory first, which
-// costs more shared-memory bandwidth than the pass has).
+// there to f16 (exact for both formats) and feed mma.sync with the cached rows
+// (then the channels) as M and eight query rows as N, so a group of up to eight
+// heads wastes nothing:
+//
+//   S^T [keys x queries] = K Q^T,   O^T [channels x queries] += V^T P^T
+//
+// The eight-query tile needs a quarter of that pipe's rate at full HBM
+// bandwidth; tcgen05 would want the codes expanded to f16 in shared memory
+// first, more shared-memory traffic than the pass has time for.
 //
 // Exactness.  Queries are scaled per row by a power of two into f16's range
 // (the logit factor absorbs it); logits, maxima, sums and outputs are fp32.
-// The weights P go to f16 for the P V product times 2^15 and times the block's
-// V scale over the largest V scale so far: a weight keeps f16's 11 bits down to
-// 2^-29 of the largest weight, and the sum of the weights is taken in fp32
-// before that rounding.
+// The running maximum is raised when a logit exceeds it by 2^8.  The weights P
+// go to f16 for the P V product times 2^7 and times the block's V scale over
+// the largest V scale so far: at most 2^15, with f16's full 11 bits down to
+// 2^-21; their sum is taken in fp32 before that rounding.
 #include "kv8.cuh"
 
 namespace csa2 {
@@ -125,6 +130,14 @@ __device__ __forceinline__ float load_query(const Kv8Rows& q, int64_t at, bool o
   return scale_log2 / up;
 }
 
+// 8x8 matrix of 16-bit elements, row lane / 4, columns 2 (lane % 4) + {0, 1}:
+// its transpose in the same layout.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 template <int D>
 struct DecodeSmem {
   static constexpr int kStages = D == 128 ? 3 : 6;
@@ -133,20 +146,51 @@ struct DecodeSmem {
   static constexpr int kRingWarp = kStages * kStage;
   static constexpr int kMeta = kWarps * kRingWarp;       // per warp and stage: 4 scales, 2 flags
   static constexpr int kMetaWarp = kStages * 32;
-  static constexpr int kRed = kMeta + kWarps * kMetaWarp;  // fp32 [16][D + 4] merge buffer
-  static constexpr int kStat = kRed + 16 * (D + 4) * 4;    // m, l: fp32 [kWarps][32] each
+  static constexpr int kStat = kMeta + kWarps * kMetaWarp;  // m, l: fp32 [kWarps][32] each
   static constexpr int kBytes = kStat + 2 * kWarps * 32 * 4;
+  static constexpr int kRedRow = D + 4;                  // merge buffer (over the ring)
+  static_assert(kWarps * 32 * kRedRow * 4 <= kMeta, "merge buffer");
 };
 
 // Where a unit's partial result of CTA i goes: slot 2 i when the unit began in
 // an earlier CTA, 2 i + 1 when it begins in CTA i and ends in a later one.
 __host__ __device__ constexpr int64_t slot_floats(int D) { return kKv8SlotRows * (D + 2); }
 
-template <int D, int MT, int FMT>
+// The two 16-row groups of a warp's tile of cached rows.
+struct Groups {
+  int64_t row[2];   // row index of the group's first row, -1: none
+  int64_t blk[2];   // index of its scale
+};
+// Every lane gets both; lane parity does one lookup each.
+__device__ __forceinline__ Groups resolve_groups(const Kv8& c, int b, int h, int pos, int n,
+                                                 uint32_t* status, int lane) {
+  int64_t row = -1, blk = 0;
+  const int mine = pos + 16 * (lane & 1);
+  if (mine < n) {
+    int in_page;
+    const int page = kv8_page(c, b, mine, in_page);
+    if (page >= 0) {
+      row = kv8_row(c, page, h, in_page);
+      blk = kv8_block(c, page, h, in_page);
+    } else if (lane < 2) {
+      set_status(status, CSA2_DEV_BAD_PAGE);
+    }
+  }
+  Groups g;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    g.row[u] = __shfl_sync(0xffffffffu, row, u);
+    g.blk[u] = __shfl_sync(0xffffffffu, blk, u);
+  }
+  return g;
+}
+
+// NT: tiles of eight query rows.
+template <int D, int NT, int FMT>
 __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(DecodeParams p) {
   using L = DecodeSmem<D>;
-  constexpr int kChunks = D / 16;
-  constexpr int kNT = D / 8;                 // 8-channel tiles of the output
+  constexpr int kHalf = D / 64;
+  constexpr int kMT = D / 16;                // 16-channel tiles of the output
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const Kv8& c = p.a.c;
@@ -155,7 +199,6 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(DecodeParams p)
 
   uint8_t* ring = smem + warp * L::kRingWarp;
   uint8_t* meta = smem + L::kMeta + warp * L::kMetaWarp;
-  float* red = reinterpret_cast<float*>(smem + L::kRed);
   float* sm = reinterpret_cast<float*>(smem + L::kStat);
   float* sl = sm + kWarps * 32;
 
@@ -170,97 +213,94 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(DecodeParams p)
   int n = kv8_len(c, b), steps = kv8_steps(c, b);
   int unit = (int)((x - first) / steps), st0 = (int)((x - first) % steps);
 
+  // this lane's places in a stage: 16-byte chunk `lane + 32 i` of the tile's
+  // codes goes to dst[i & 1] + 512 i (D 128; rows of 64 bytes: dst[0] + 512 i)
+  const int dst0 = chunk_at<D>(lane * 16 / D, lane % (D / 16));
+  const int dst1 = D == 128 ? chunk_at<D>(lane * 16 / D + 4, lane % (D / 16)) - 512 : dst0;
+
   while (x < x1) {
     const int st1 = (int)min((int64_t)steps, st0 + (x1 - x));
-    const int h = unit / p.tiles, row0 = (unit % p.tiles) * 16 * MT;
+    const int h = unit / p.tiles, row0 = (unit % p.tiles) * 8 * NT;
     int ql = p.a.q_len ? p.a.q_len[b] : p.a.T;
     ql = ql < 0 ? 0 : (ql > p.a.T ? p.a.T : ql);
 
-    // ---- queries of this unit; lim: how many cached rows each query row sees
-    uint32_t qf[MT][D / 16][4];
-    float mul[MT][2];
-    int lim[MT][2];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = row0 + 16 * m + 8 * r + g;
-        const int tok = row / p.a.G, hd = h * p.a.G + row % p.a.G;
-        const bool ok = row < p.rows && tok < ql;
-        uint32_t fr[D / 16][2];
-        mul[m][r] = load_query<D>(p.a.q, b * p.a.q.sb + tok * p.a.q.st + hd * p.a.q.sh, ok, t,
-                                  p.a.scale_log2, fr);
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          qf[m][s][r] = fr[s][0];
-          qf[m][s][2 + r] = fr[s][1];
-        }
-        lim[m][r] = ok ? min(n, n - ql + tok + 1) : 0;
-      }
-
     // ---- pipeline over this warp's tiles st0 .. st1
-    int64_t base[2];       // code row of the next tile's two 16-row groups, -1: none
-    int64_t sbase[2];
+    Groups next;
     auto resolve = [&](int st) {
-      const int pos = st * kKv8Step + warp * kSub;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        base[u] = -1;
-        sbase[u] = 0;
-        if (st < st1 && pos + 16 * u < n) {
-          int in_page;
-          const int page = kv8_page(c, b, pos + 16 * u, in_page);
-          if (page >= 0) {
-            base[u] = kv8_row(c, page, h, in_page);
-            sbase[u] = kv8_block(c, page, h, in_page);
-          } else if (lane == 0) {
-            set_status(p.a.status, CSA2_DEV_BAD_PAGE);
-          }
-        }
-      }
+      next = resolve_groups(c, b, h, st * kKv8Step + warp * kSub, st < st1 ? n : 0, p.a.status, lane);
     };
     auto issue = [&](int st, int stage) {
       if (st < st1) {
         const int left = n - (st * kKv8Step + warp * kSub);
         uint8_t* k = ring + stage * L::kStage;
+        const int64_t at[2] = {next.row[0] * D + lane * 16, next.row[1] * D + lane * 16};
+        if (left >= kSub && next.row[0] >= 0 && next.row[1] >= 0) {
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-          const int id = lane + 32 * i, row = id / kChunks, ch = id % kChunks;
-          const int64_t gb = row < 16 ? base[0] : base[1];
-          const bool ok = gb >= 0 && row < left;
-          const int64_t off = ok ? (gb + (row & 15)) * D + ch * 16 : 0;
-          const int at = chunk_at<D>(row, ch);
-          cp_async16_zfill(k + at, c.codes[0] + off, ok);
-          cp_async16_zfill(k + L::kTile + at, c.codes[1] + off, ok);
+          for (int i = 0; i < D / 16; ++i) {
+            const int64_t off = at[i / (D / 32)] + 512 * (i % (D / 32));
+            uint8_t* to = k + (i & 1 ? dst1 : dst0) + 512 * i;
+            cp_async16(to, c.codes[0] + off);
+            cp_async16(to + L::kTile, c.codes[1] + off);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const bool ok = next.row[i / (D / 32)] >= 0 && (lane + 32 * i) * 16 / D < left;
+            const int64_t off = ok ? at[i / (D / 32)] + 512 * (i % (D / 32)) : 0;
+            uint8_t* to = k + (i & 1 ? dst1 : dst0) + 512 * i;
+            cp_async16_zfill(to, c.codes[0] + off, ok);
+            cp_async16_zfill(to + L::kTile, c.codes[1] + off, ok);
+          }
         }
         float* m = reinterpret_cast<float*>(meta + stage * 32);
-        if (lane < 4) {
-          const int64_t sb = lane & 1 ? sbase[1] : sbase[0];
-          const bool ok = (lane & 1 ? base[1] : base[0]) >= 0;
-          cp_async4_zfill(m + lane, c.scales[lane >> 1] + (ok ? sb : 0), ok);
-        }
-        if (lane < 2) reinterpret_cast<int*>(m)[4 + lane] = (lane ? base[1] : base[0]) >= 0;
+        const bool ok = (lane & 1 ? next.row[1] : next.row[0]) >= 0;
+        const int64_t sc = lane & 1 ? next.blk[1] : next.blk[0];
+        if (lane < 4) cp_async4_zfill(m + lane, c.scales[lane >> 1] + (ok ? sc : 0), ok);
+        if (lane < 2) reinterpret_cast<int*>(m)[4 + lane] = ok;
       }
       cp_async_commit();
     };
-
-    float o[MT][kNT][4];
-    float mx[MT][2], ls[MT][2];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-      for (int j = 0; j < kNT; ++j) o[m][j][0] = o[m][j][1] = o[m][j][2] = o[m][j][3] = 0.0f;
-      mx[m][0] = mx[m][1] = -INFINITY;
-      ls[m][0] = ls[m][1] = 0.0f;
-    }
-    float vref = 0.0f;     // the largest V scale so far (a power of two)
-
     resolve(st0);
 #pragma unroll
     for (int i = 0; i < L::kStages - 1; ++i) {
       issue(st0 + i, i);
       resolve(st0 + i + 1);
     }
+
+    // ---- queries of this unit: row 8 u + g as B fragments; the logit factor
+    // and the number of visible cached rows of the rows 8 u + 2 t + e
+    uint32_t qf[NT][D / 16][2];
+    float mul[NT][2];
+    int lim[NT][2], full = 0x7FFFFFFF;   // rows below `full` are seen by every query row
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      const int row = row0 + 8 * u + g;
+      const int tok = row / p.a.G, hd = h * p.a.G + row % p.a.G;
+      const bool ok = row < p.rows && tok < ql;
+      const float f = load_query<D>(p.a.q, b * p.a.q.sb + tok * p.a.q.st + hd * p.a.q.sh, ok, t,
+                                    p.a.scale_log2, qf[u]);
+      // a row without a query is never written: it may see everything
+      const int see = ok ? min(n, n - ql + tok + 1) : 0x7FFFFFFF;
+      full = min(full, see);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mul[u][e] = __shfl_sync(0xffffffffu, f, 4 * (2 * t + e));
+        lim[u][e] = __shfl_sync(0xffffffffu, see, 4 * (2 * t + e));
+      }
+    }
+    full = __reduce_min_sync(0xffffffffu, full);
+
+    float o[NT][kMT][4];
+    float mx[NT][2], ls[NT][2];
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+#pragma unroll
+      for (int j = 0; j < kMT; ++j) o[u][j][0] = o[u][j][1] = o[u][j][2] = o[u][j][3] = 0.0f;
+      mx[u][0] = mx[u][1] = -INFINITY;
+      ls[u][0] = ls[u][1] = 0.0f;
+    }
+    float vref = 0.0f;     // the largest V scale so far (a power of two)
+
     int stage = 0;
     for (int st = st0; st < st1; ++st) {
       cp_async_wait<L::kStages - 2>();
@@ -272,210 +312,226 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(DecodeParams p)
       }
       const uint8_t* k = ring + stage * L::kStage;
       const uint8_t* v = k + L::kTile;
-      const float* ms = reinterpret_cast<const float*>(meta + stage * 32);
-      const float ks[2] = {ms[0], ms[1]}, vs[2] = {ms[2], ms[3]};
-      const bool grp[2] = {reinterpret_cast<const int*>(ms)[4] != 0,
-                           reinterpret_cast<const int*>(ms)[5] != 0};
+      const float4 sc = *reinterpret_cast<const float4*>(meta + stage * 32);
+      const int2 there = *reinterpret_cast<const int2*>(meta + stage * 32 + 16);
+      const float ks[2] = {sc.x, sc.y}, vs[2] = {sc.z, sc.w};
       stage = stage + 1 == L::kStages ? 0 : stage + 1;
 
-      // ---- S = Q K^T: four 8-row tiles of cached rows
-      float s[MT][4][4];
+      // ---- S^T = K Q^T: two tiles of 16 cached rows (rows key_of(g), + 8)
+      float s[NT][2][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m) s[m][i][0] = s[m][i][1] = s[m][i][2] = s[m][i][3] = 0.0f;
-        const int row = 8 * i + key_of(g);
+        for (int u = 0; u < NT; ++u) s[u][i][0] = s[u][i][1] = s[u][i][2] = s[u][i][3] = 0.0f;
+        const int row = 16 * i + key_of(g);
 #pragma unroll
-        for (int f = 0; f < D / 64; ++f) {
-          const uint4 w = *reinterpret_cast<const uint4*>(k + chunk_at<D>(row, 4 * f + t));
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        for (int f = 0; f < kHalf; ++f) {
+          const uint4 wa = *reinterpret_cast<const uint4*>(k + chunk_at<D>(row, 4 * f + t));
+          const uint4 wb = *reinterpret_cast<const uint4*>(k + chunk_at<D>(row + 8, 4 * f + t));
+          const uint32_t xa[4] = {wa.x, wa.y, wa.z, wa.w}, xb[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            uint32_t b0, b1;
-            kv8_to_f16<FMT>(ww[q], b0, b1);
+            uint32_t a[4];
+            kv8_to_f16<FMT>(xa[q], a[0], a[2]);
+            kv8_to_f16<FMT>(xb[q], a[1], a[3]);
 #pragma unroll
-            for (int m = 0; m < MT; ++m) mma16816(s[m][i], qf[m][4 * f + q], b0, b1);
+            for (int u = 0; u < NT; ++u) mma16816(s[u][i], a, qf[u][4 * f + q][0], qf[u][4 * f + q][1]);
           }
         }
       }
 
-      // ---- online softmax; P in f16 times 2^15 and the V scale's share
-      const float vnew = fmaxf(vref, fmaxf(vs[0], vs[1]));
-      const float vdown = vnew > vref ? vref * kv8_inverse(vnew) : 1.0f;
-      const float vinv = kv8_inverse(vnew);
-      const float vr[2] = {vs[0] * vinv * 32768.0f, vs[1] * vinv * 32768.0f};
-      vref = vnew;
+      // ---- logits (base 2): s[u][i][2 r + e] is cached row 16 i + 8 r + key_of(g),
+      // query row 8 u + 2 t + e
       const int pos = st * kKv8Step + warp * kSub;
-      uint32_t pf[MT][2][4];
+      bool raise = false;
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        float alpha[2];
+      for (int u = 0; u < NT; ++u)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float top = mx[m][r];
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int j = pos + 8 * i + key_of(2 * t + e);
-              float y = s[m][i][2 * r + e] * (mul[m][r] * ks[i >> 1]);
-              if (j >= lim[m][r] || !grp[i >> 1]) y = -INFINITY;
-              s[m][i][2 * r + e] = y;
-              top = fmaxf(top, y);
-            }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const float use = top == -INFINITY ? 0.0f : top;
-          alpha[r] = kv8_exp2(mx[m][r] - use);
-          mx[m][r] = top;
-          float sum = 0.0f;
+            for (int r = 0; r < 2; ++r) s[u][i][2 * r + e] *= mul[u][e] * ks[i];
+      if (pos + kSub > full || !(there.x & there.y)) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+        for (int u = 0; u < NT; ++u)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float w = kv8_exp2(s[m][i][2 * r + e] - use);
-              sum += w;
-              s[m][i][2 * r + e] = w * vr[i >> 1];
-            }
-          ls[m][r] = ls[m][r] * alpha[r] + sum;
-          alpha[r] *= vdown;
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+                if (pos + 16 * i + 8 * r + key_of(g) >= min(lim[u][e], n) ||
+                    !(i ? there.y : there.x))
+                  s[u][i][2 * r + e] = -INFINITY;
+      }
+      float tops[NT][2];
+#pragma unroll
+      for (int u = 0; u < NT; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          tops[u][e] = fmaxf(fmaxf(s[u][0][e], s[u][0][2 + e]), fmaxf(s[u][1][e], s[u][1][2 + e]));
+          raise |= tops[u][e] > mx[u][e] + 8.0f;
         }
+      const float vnew = fmaxf(vref, fmaxf(vs[0], vs[1]));
+      if (__any_sync(0xffffffffu, raise) || vnew > vref) {
+        // raise the maxima and the V reference; O and the sums follow
+        const float vdown = vnew > vref ? vref * kv8_inverse(vnew) : 1.0f;
+        vref = vnew;
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
+        for (int u = 0; u < NT; ++u) {
+          float alpha[2];
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
+          for (int e = 0; e < 2; ++e) {
+            float top = tops[u][e];
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            top = fmaxf(top, mx[u][e]);
+            alpha[e] = top == -INFINITY ? 1.0f : kv8_exp2(mx[u][e] - top);
+            mx[u][e] = top;
+            ls[u][e] *= alpha[e];
+            alpha[e] *= vdown;
+          }
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-              pf[m][kk][2 * u + r] =
-                  pack16(s[m][2 * kk + u][2 * r], s[m][2 * kk + u][2 * r + 1], CSA2_F16);
-        if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
-#pragma unroll
-          for (int j = 0; j < kNT; ++j) {
-            o[m][j][0] *= alpha[0];
-            o[m][j][1] *= alpha[0];
-            o[m][j][2] *= alpha[1];
-            o[m][j][3] *= alpha[1];
+          for (int j = 0; j < kMT; ++j) {
+            o[u][j][0] *= alpha[0];
+            o[u][j][1] *= alpha[1];
+            o[u][j][2] *= alpha[0];
+            o[u][j][3] *= alpha[1];
           }
         }
       }
-
-      // ---- O += P V: column n of output tile j is channel (D/8) n + j
+      // ---- P^T in f16, transposed into the B fragments of the P V product
+      const float vinv = kv8_inverse(vref);
+      const float vr[2] = {vs[0] * vinv * 128.0f, vs[1] * vinv * 128.0f};
+      uint32_t pf[NT][2][2];
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
+      for (int u = 0; u < NT; ++u) {
+        const float use[2] = {mx[u][0] == -INFINITY ? 0.0f : mx[u][0],
+                              mx[u][1] == -INFINITY ? 0.0f : mx[u][1]};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float wa = kv8_exp2(s[u][i][2 * r] - use[0]);
+            const float wb = kv8_exp2(s[u][i][2 * r + 1] - use[1]);
+            ls[u][0] += wa;
+            ls[u][1] += wb;
+            pf[u][i][r] = transpose8x8(pack16(wa * vr[i], wb * vr[i], CSA2_F16));
+          }
+      }
+
+      // ---- O^T += V^T P^T: rows g, g + 8 of output tile j are the channels
+      // (D/8) g + 2 j and + 1, its columns the query rows
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
         uint32_t w[4][D / 32];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int row = 16 * kk + 8 * (u >> 1) + key_of(2 * t + (u & 1));
+        for (int y = 0; y < 4; ++y) {
+          const int row = 16 * i + 8 * (y >> 1) + key_of(2 * t + (y & 1));
           if (D == 128) {
-            const uint4 y = *reinterpret_cast<const uint4*>(v + chunk_at<D>(row, g));
-            w[u][0] = y.x; w[u][1] = y.y; w[u][D / 32 - 2] = y.z; w[u][D / 32 - 1] = y.w;
+            const uint4 z = *reinterpret_cast<const uint4*>(v + chunk_at<D>(row, g));
+            w[y][0] = z.x; w[y][1] = z.y; w[y][D / 32 - 2] = z.z; w[y][D / 32 - 1] = z.w;
           } else {
-            const uint2 y =
+            const uint2 z =
                 *reinterpret_cast<const uint2*>(v + chunk_at<D>(row, g >> 1) + 8 * (g & 1));
-            w[u][0] = y.x; w[u][1] = y.y;
+            w[y][0] = z.x; w[y][1] = z.y;
           }
         }
 #pragma unroll
         for (int q = 0; q < D / 32; ++q) {
-          uint32_t b0[4], b1[4];
-          kv8_to_f16<FMT>(__byte_perm(w[0][q], w[1][q], 0x5140), b0[0], b0[1]);
-          kv8_to_f16<FMT>(__byte_perm(w[0][q], w[1][q], 0x7362), b0[2], b0[3]);
-          kv8_to_f16<FMT>(__byte_perm(w[2][q], w[3][q], 0x5140), b1[0], b1[1]);
-          kv8_to_f16<FMT>(__byte_perm(w[2][q], w[3][q], 0x7362), b1[2], b1[3]);
+          uint32_t a[4], d[4];
+          kv8_to_f16<FMT>(__byte_perm(w[0][q], w[1][q], 0x5140), a[0], a[1]);
+          kv8_to_f16<FMT>(__byte_perm(w[2][q], w[3][q], 0x5140), a[2], a[3]);
+          kv8_to_f16<FMT>(__byte_perm(w[0][q], w[1][q], 0x7362), d[0], d[1]);
+          kv8_to_f16<FMT>(__byte_perm(w[2][q], w[3][q], 0x7362), d[2], d[3]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int m = 0; m < MT; ++m) mma16816(o[m][4 * q + j], pf[m][kk], b0[j], b1[j]);
+          for (int u = 0; u < NT; ++u) {
+            mma16816(o[u][2 * q], a, pf[u][i][0], pf[u][i][1]);
+            mma16816(o[u][2 * q + 1], d, pf[u][i][0], pf[u][i][1]);
+          }
         }
       }
       __syncwarp();
     }
     cp_async_wait<0>();
 
-    // ---- merge the warps, then write the rows or a partial result
+    // ---- merge the warps (over the ring), then write the rows or a partial result
     const bool whole = st0 == 0 && st1 == steps;
     float* part = p.a.part + (2 * (int64_t)blockIdx.x + (st0 > 0 ? 0 : 1)) * slot_floats(D);
+    float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int u = 0; u < NT; ++u)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        ls[m][r] += __shfl_xor_sync(0xffffffffu, ls[m][r], 1);
-        ls[m][r] += __shfl_xor_sync(0xffffffffu, ls[m][r], 2);
-        if (t == 0) {
-          sm[warp * 32 + 16 * m + 8 * r + g] = mx[m][r];
-          sl[warp * 32 + 16 * m + 8 * r + g] = ls[m][r];
+      for (int e = 0; e < 2; ++e) {
+        ls[u][e] += __shfl_xor_sync(0xffffffffu, ls[u][e], 4);
+        ls[u][e] += __shfl_xor_sync(0xffffffffu, ls[u][e], 8);
+        ls[u][e] += __shfl_xor_sync(0xffffffffu, ls[u][e], 16);
+        if (g == 0) {
+          sm[warp * 32 + 8 * u + 2 * t + e] = mx[u][e];
+          sl[warp * 32 + 8 * u + 2 * t + e] = ls[u][e];
         }
       }
     __syncthreads();
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int u = 0; u < NT; ++u)
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (warp == w) {
+      for (int e = 0; e < 2; ++e) {
+        const int row = 8 * u + 2 * t + e;
+        float top = sm[row];
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int row = 16 * m + 8 * r + g;
-            float top = sm[row];
+        for (int i = 1; i < kWarps; ++i) top = fmaxf(top, sm[i * 32 + row]);
+        // a sum of 0: no row was visible; of NaN: the query holds one
+        const float f = ls[u][e] == 0.0f ? 0.0f : kv8_exp2(mx[u][e] - top) * (vref * 0x1p-7f);
+        float* to = red + (warp * 8 * NT + row) * L::kRedRow + (D / 8) * g;
 #pragma unroll
-            for (int u = 1; u < kWarps; ++u) top = fmaxf(top, sm[u * 32 + row]);
-            // a sum of 0: no row was visible; of NaN: the query holds one
-            const float f =
-                ls[m][r] == 0.0f ? 0.0f : kv8_exp2(mx[m][r] - top) * (vref * 0x1p-15f);
-            float* to = red + (8 * r + g) * (D + 4);
-#pragma unroll
-            for (int j = 0; j < kNT; ++j)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int ch = kNT * (2 * t + e) + j;
-                const float y = o[m][j][2 * r + e] * f;
-                to[ch] = w == 0 ? y : to[ch] + y;
-              }
-          }
-        }
-        __syncthreads();
+        for (int j = 0; j < kMT; j += 2)
+          *reinterpret_cast<float4*>(to + 2 * j) =
+              make_float4(o[u][j][e] * f, o[u][j][2 + e] * f, o[u][j + 1][e] * f,
+                          o[u][j + 1][2 + e] * f);
       }
-      // 8 threads per row, D / 8 channels each
-      const int row = 16 * m + (tid >> 3), ch0 = (tid & 7) * (D / 8);
-      float top = sm[row];
+    __syncthreads();
+    // 8 channels a thread
+    for (int id = tid; id < 8 * NT * (D / 8); id += kThreads) {
+      const int row = id / (D / 8), ch = 8 * (id % (D / 8));
+      float top = sm[row], l = 0.0f;
 #pragma unroll
-      for (int u = 1; u < kWarps; ++u) top = fmaxf(top, sm[u * 32 + row]);
-      float l = 0.0f;
+      for (int i = 1; i < kWarps; ++i) top = fmaxf(top, sm[i * 32 + row]);
+      float y[8] = {};
 #pragma unroll
-      for (int u = 0; u < kWarps; ++u)
-        l += sl[u * 32 + row] == 0.0f ? 0.0f : sl[u * 32 + row] * kv8_exp2(sm[u * 32 + row] - top);
-      const float* from = red + (tid >> 3) * (D + 4) + ch0;
+      for (int i = 0; i < kWarps; ++i) {
+        const float wl = sl[i * 32 + row];
+        l += wl == 0.0f ? 0.0f : wl * kv8_exp2(sm[i * 32 + row] - top);
+        const float4* from =
+            reinterpret_cast<const float4*>(red + (i * 8 * NT + row) * L::kRedRow + ch);
+        const float4 ya = from[0], yb = from[1];
+        y[0] += ya.x; y[1] += ya.y; y[2] += ya.z; y[3] += ya.w;
+        y[4] += yb.x; y[5] += yb.y; y[6] += yb.z; y[7] += yb.w;
+      }
+      const int gr = row0 + row, tok = gr / p.a.G, hd = h * p.a.G + gr % p.a.G;
+      if (gr >= p.rows || tok >= ql) continue;
       if (whole) {
-        const int gr = row0 + row, tok = gr / p.a.G, hd = h * p.a.G + gr % p.a.G;
-        if (gr < p.rows && tok < ql) {
-          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-          uint16_t* out = static_cast<uint16_t*>(const_cast<void*>(p.a.out.data)) +
-                          b * p.a.out.sb + tok * p.a.out.st + hd * p.a.out.sh + ch0;
-#pragma unroll
-          for (int i = 0; i < D / 8; i += 8) {
-            uint4 y;
-            y.x = pack16(from[i] * inv, from[i + 1] * inv, p.a.out.type);
-            y.y = pack16(from[i + 2] * inv, from[i + 3] * inv, p.a.out.type);
-            y.z = pack16(from[i + 4] * inv, from[i + 5] * inv, p.a.out.type);
-            y.w = pack16(from[i + 6] * inv, from[i + 7] * inv, p.a.out.type);
-            *reinterpret_cast<uint4*>(out + i) = y;
-          }
-          if (p.a.lse && ch0 == 0)
-            p.a.lse[((int64_t)b * p.a.T + tok) * p.a.H + hd] =
-                l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
-        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        uint16_t* out = static_cast<uint16_t*>(const_cast<void*>(p.a.out.data)) + b * p.a.out.sb +
+                        tok * p.a.out.st + hd * p.a.out.sh + ch;
+        *reinterpret_cast<uint4*>(out) = make_uint4(
+            pack16(y[0] * inv, y[1] * inv, p.a.out.type), pack16(y[2] * inv, y[3] * inv, p.a.out.type),
+            pack16(y[4] * inv, y[5] * inv, p.a.out.type), pack16(y[6] * inv, y[7] * inv, p.a.out.type));
+        if (p.a.lse && ch == 0)
+          p.a.lse[((int64_t)b * p.a.T + tok) * p.a.H + hd] =
+              l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
       } else {
-        float* po = part + row * D + ch0;
-#pragma unroll
-        for (int i = 0; i < D / 8; i += 4)
-          *reinterpret_cast<float4*>(po + i) =
-              make_float4(from[i], from[i + 1], from[i + 2], from[i + 3]);
-        if (ch0 == 0) {
+        float4* po = reinterpret_cast<float4*>(part + row * D + ch);
+        po[0] = make_float4(y[0], y[1], y[2], y[3]);
+        po[1] = make_float4(y[4], y[5], y[6], y[7]);
+        if (ch == 0) {
           part[kKv8SlotRows * D + row] = top;
           part[kKv8SlotRows * (D + 1) + row] = l;
         }
       }
-      __syncthreads();
     }
+    __syncthreads();   // the ring takes the next unit's rows
 
     // ---- next unit
     x += st1 - st0;
@@ -551,12 +607,18 @@ __global__ void __launch_bounds__(D) kv8_combine_kernel(DecodeParams p, int tile
 }
 
 // ---------------------------------------------------------------------- mass
-// mass_j = decay mass_j + sum over the query rows of 2^(c q k_j - lse).  A warp
-// holds 32 cached rows' codes as f16 B fragments and walks the query rows 16 at
-// a time; a cached row belongs to one warp, so nothing is added atomically and
-// the order of the sum is fixed.
-template <int D, int FMT>
-__global__ void __launch_bounds__(kThreads) kv8_mass_kernel(DecodeParams p) {
+// mass_j = decay mass_j + sum over the query rows of 2^(c q k_j - lse), for up to
+// 8 NT query rows: their fragments stay in registers while a warp streams its
+// cached rows, the next tile's codes loaded while this one is worked on.  A
+// cached row belongs to one warp, so nothing is added atomically and the order
+// of the sum is fixed.
+//
+// The exponent is x = s f - lse2 with f = c log2(e) 2^e s_K and lse2 = lse log2(e).
+// Both constants are held in two fp32 parts: at logits of 20 to 30 the rounding
+// of one part alone would be 1e-6 of the weight.
+template <int D, int NT, int FMT>
+__global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kv8_mass_kernel(DecodeParams p) {
+  constexpr int kHalf = D / 64;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const Kv8& c = p.a.c;
   griddep_wait();
@@ -569,139 +631,146 @@ __global__ void __launch_bounds__(kThreads) kv8_mass_kernel(DecodeParams p) {
   int64_t first;
   int b = kv8_find(c, lane, c.heads, x, first);
   int n = kv8_len(c, b), steps = kv8_steps(c, b);
-  int h = (int)((x - first) / steps), st = (int)((x - first) % steps);
-  for (; x < x1; ++x) {
-    const int pos = st * kKv8Step + warp * kSub;
-    if (pos < n) {
-      int ql = p.a.q_len ? p.a.q_len[b] : p.a.T;
-      ql = ql < 0 ? 0 : (ql > p.a.T ? p.a.T : ql);
-      uint32_t kf[4][D / 16][2];
-      int64_t grow[2];
-      float ks[2];
+  int h = (int)((x - first) / steps), st0 = (int)((x - first) % steps);
+  while (x < x1) {
+    const int st1 = (int)min((int64_t)steps, st0 + (x1 - x));
+    int ql = p.a.q_len ? p.a.q_len[b] : p.a.T;
+    ql = ql < 0 ? 0 : (ql > p.a.T ? p.a.T : ql);
+
+    Groups at;
+    uint4 raw[2][kHalf][2];     // rows 16 i + 8 r + g, 16-byte chunk 4 f + t
+    float ks[2];
+    auto load = [&](int st) {
+      const int pos = st * kKv8Step + warp * kSub;
+      at = resolve_groups(c, b, h, pos, st < st1 ? n : 0, p.a.status, lane);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        grow[u] = -1;
-        ks[u] = 0.0f;
-        if (pos + 16 * u < n) {
-          int in_page;
-          const int page = kv8_page(c, b, pos + 16 * u, in_page);
-          if (page >= 0) {
-            grow[u] = kv8_row(c, page, h, in_page);
-            ks[u] = c.scales[0][kv8_block(c, page, h, in_page)];
-          } else if (lane == 0) {
-            set_status(p.a.status, CSA2_DEV_BAD_PAGE);
+      for (int i = 0; i < 2; ++i) {
+        ks[i] = at.row[i] >= 0 ? c.scales[0][at.blk[i]] : 0.0f;
+#pragma unroll
+        for (int f = 0; f < kHalf; ++f)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            raw[i][f][r] = make_uint4(0, 0, 0, 0);
+            if (at.row[i] >= 0 && pos + 16 * i + 8 * r + g < n)
+              raw[i][f][r] = *reinterpret_cast<const uint4*>(
+                  c.codes[0] + (at.row[i] + 8 * r + g) * D + (4 * f + t) * 16);
+          }
+      }
+    };
+    load(st0);
+
+    uint32_t qf[NT][D / 16][2];
+    float mul[NT][2], ml[NT][2], l2[NT][2], ll[NT][2];
+    int lim[NT][2], full = 0x7FFFFFFF;
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      const int row = 8 * u + g, tok = row / p.a.G, hd = h * p.a.G + row % p.a.G;
+      const bool ok = row < p.rows && tok < ql;
+      const float f = load_query<D>(p.a.q, b * p.a.q.sb + tok * p.a.q.st + hd * p.a.q.sh, ok, t,
+                                    1.0f, qf[u]);
+      float y = ok ? p.a.lse[((int64_t)b * p.a.T + tok) * p.a.H + hd] : -INFINITY;
+      const int see = ok && y != -INFINITY ? min(n, n - ql + tok + 1) : 0;
+      if (y == -INFINITY) y = 0.0f;
+      // a row without weight: a constant so large that every weight is 0
+      const float hi = see ? y * 1.44269502f : INFINITY;
+      const float lo = see ? fmaf(y, 1.44269502f, -hi) + y * 1.92596299e-8f : 0.0f;
+      if (see) full = min(full, see);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int from = 4 * (2 * t + e);
+        const float fe = __shfl_sync(0xffffffffu, f, from);
+        mul[u][e] = p.a.scale_log2 * fe;
+        ml[u][e] = p.a.scale_low * fe;
+        l2[u][e] = __shfl_sync(0xffffffffu, hi, from);
+        ll[u][e] = __shfl_sync(0xffffffffu, lo, from);
+        lim[u][e] = __shfl_sync(0xffffffffu, see, from);
+      }
+    }
+    full = __reduce_min_sync(0xffffffffu, full);
+
+    for (int st = st0; st < st1; ++st) {
+      const int pos = st * kKv8Step + warp * kSub;
+      const Groups here = at;
+      const float kscale[2] = {ks[0], ks[1]};
+      float s[NT][2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int u = 0; u < NT; ++u) s[u][i][0] = s[u][i][1] = s[u][i][2] = s[u][i][3] = 0.0f;
+#pragma unroll
+        for (int f = 0; f < kHalf; ++f) {
+          const uint32_t* xa = reinterpret_cast<const uint32_t*>(&raw[i][f][0]);
+          const uint32_t* xb = reinterpret_cast<const uint32_t*>(&raw[i][f][1]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t a[4];
+            kv8_to_f16<FMT>(xa[q], a[0], a[2]);
+            kv8_to_f16<FMT>(xb[q], a[1], a[3]);
+#pragma unroll
+            for (int u = 0; u < NT; ++u) mma16816(s[u][i], a, qf[u][4 * f + q][0], qf[u][4 * f + q][1]);
           }
         }
       }
+      load(st + 1);
+      const bool some = pos + kSub > full;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + g;
-        const bool ok = grow[i >> 1] >= 0 && pos + r < n;
-#pragma unroll
-        for (int f = 0; f < D / 64; ++f) {
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (ok)
-            w = *reinterpret_cast<const uint4*>(c.codes[0] + (grow[i >> 1] + (r & 15)) * D +
-                                                (4 * f + t) * 16);
-          kv8_to_f16<FMT>(w.x, kf[i][4 * f][0], kf[i][4 * f][1]);
-          kv8_to_f16<FMT>(w.y, kf[i][4 * f + 1][0], kf[i][4 * f + 1][1]);
-          kv8_to_f16<FMT>(w.z, kf[i][4 * f + 2][0], kf[i][4 * f + 2][1]);
-          kv8_to_f16<FMT>(w.w, kf[i][4 * f + 3][0], kf[i][4 * f + 3][1]);
-        }
-      }
-      float sum[4][2] = {};
-      const int rows = ql * p.a.G;
-      // the first query token that sees row `pos`
-      const int tok0 = max(0, pos - (n - ql));
-      for (int r0 = tok0 * p.a.G / 16 * 16; r0 < rows; r0 += 16) {
-        uint32_t qf[D / 16][4];
-        float mul[2], lse2[2];
-        int lim[2];
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int row = r0 + 8 * r + g;
-          const int tok = row / p.a.G, hd = h * p.a.G + row % p.a.G;
-          const bool ok = row < rows;
-          uint32_t fr[D / 16][2];
-          mul[r] = load_query<D>(p.a.q, b * p.a.q.sb + tok * p.a.q.st + hd * p.a.q.sh, ok, t,
-                                 p.a.scale_log2, fr);
+          const int row = 16 * i + 8 * r + g;
+          float sum = 0.0f;
 #pragma unroll
-          for (int s = 0; s < D / 16; ++s) {
-            qf[s][r] = fr[s][0];
-            qf[s][2 + r] = fr[s][1];
-          }
-          lim[r] = 0;
-          lse2[r] = 0.0f;
-          if (ok) {
-            const float y = p.a.lse[((int64_t)b * p.a.T + tok) * p.a.H + hd];
-            if (y != -INFINITY) {
-              lse2[r] = y * 1.4426950408889634f;
-              lim[r] = min(n, n - ql + tok + 1);
+          for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float z = s[u][i][2 * r + e] * kscale[i];       // exact: a power of two
+              float w = kv8_exp2(fmaf(z, mul[u][e], -l2[u][e]) + fmaf(z, ml[u][e], -ll[u][e]));
+              if (some && pos + row >= lim[u][e]) w = 0.0f;
+              sum += w;
             }
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float s[4] = {};
-#pragma unroll
-          for (int q = 0; q < D / 16; ++q) mma16816(s, qf[q], kf[i][q][0], kf[i][q][1]);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int j = pos + 8 * i + 2 * t + e;
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-              if (j < lim[r])
-                sum[i][e] += kv8_exp2(s[2 * r + e] * (mul[r] * ks[i >> 1]) - lse2[r]);
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float y = sum[i][e];
-          y += __shfl_xor_sync(0xffffffffu, y, 4);
-          y += __shfl_xor_sync(0xffffffffu, y, 8);
-          y += __shfl_xor_sync(0xffffffffu, y, 16);
-          const int r = 8 * i + 2 * t + e;
-          if (g == 0 && grow[i >> 1] >= 0 && pos + r < n) {
-            float* m = c.mass + grow[i >> 1] + (r & 15);
-            *m = p.a.decay == 0.0f ? y : *m * p.a.decay + y;
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          if (t == 0 && here.row[i] >= 0 && pos + row < n) {
+            float* m = c.mass + here.row[i] + 8 * r + g;
+            *m = p.a.decay == 0.0f ? sum : *m * p.a.decay + sum;
           }
         }
     }
-    if (++st == steps) {
-      st = 0;
-      if (++h == c.heads && x + 1 < x1) {
-        h = 0;
-        ++b;
-        n = kv8_len(c, b);
-        steps = kv8_steps(c, b);
-      }
+    x += st1 - st0;
+    st0 = 0;
+    if (st1 == steps && ++h == c.heads && x < x1) {
+      h = 0;
+      ++b;
+      n = kv8_len(c, b);
+      steps = kv8_steps(c, b);
     }
   }
 }
 
-template <int D, int MT, int FMT>
+template <int D, int NT, int FMT>
 cudaError_t decode_as(const DecodeParams& p, cudaStream_t s) {
-  auto kern = kv8_decode_kernel<D, MT, FMT>;
+  auto kern = kv8_decode_kernel<D, NT, FMT>;
   static std::atomic<uint64_t> seen;
   cudaError_t e = kv8_prepare(kern, DecodeSmem<D>::kBytes, seen);
   if (e != cudaSuccess) return e;
   e = kv8_launch(kern, dim3(p.ctas), kThreads, DecodeSmem<D>::kBytes, s, p);
   if (e != cudaSuccess) return e;
-  return kv8_launch(kv8_combine_kernel<D>, dim3(p.a.c.batch * p.a.c.heads * p.tiles, 16 * MT), D, 0, s, p,
-                16 * MT);
+  return kv8_launch(kv8_combine_kernel<D>, dim3(p.a.c.batch * p.a.c.heads * p.tiles, 8 * NT), D, 0,
+                    s, p, 8 * NT);
 }
 template <int D, int FMT>
 cudaError_t decode_of(DecodeParams p, cudaStream_t s) {
-  const int mt = p.rows <= 16 ? 1 : 2;
-  p.tiles = (p.rows + 16 * mt - 1) / (16 * mt);
-  return mt == 1 ? decode_as<D, 1, FMT>(p, s) : decode_as<D, 2, FMT>(p, s);
+  const int nt = p.rows <= 8 ? 1 : (p.rows <= 16 ? 2 : 4);
+  p.tiles = (p.rows + 8 * nt - 1) / (8 * nt);
+  return nt == 1   ? decode_as<D, 1, FMT>(p, s)
+         : nt == 2 ? decode_as<D, 2, FMT>(p, s)
+                   : decode_as<D, 4, FMT>(p, s);
 }
 template <int D, int FMT>
-cudaError_t mass_as(const DecodeParams& p, cudaStream_t s) {
-  return kv8_launch(kv8_mass_kernel<D, FMT>, dim3(p.ctas), kThreads, 0, s, p);
+cudaError_t mass_of(const DecodeParams& p, cudaStream_t s) {
+  return p.rows <= 8    ? kv8_launch(kv8_mass_kernel<D, 1, FMT>, dim3(p.ctas), kThreads, 0, s, p)
+         : p.rows <= 16 ? kv8_launch(kv8_mass_kernel<D, 2, FMT>, dim3(p.ctas), kThreads, 0, s, p)
+                        : kv8_launch(kv8_mass_kernel<D, 4, FMT>, dim3(p.ctas), kThreads, 0, s, p);
 }
 
 }  // namespace
@@ -715,11 +784,11 @@ cudaError_t launch_kv8_attn(const Kv8Attn& a, int num_sms, cudaStream_t s) {
   return a.D == 64 ? decode_of<64, CSA2_KV8_INT8>(p, s) : decode_of<128, CSA2_KV8_INT8>(p, s);
 }
 
-cudaError_t launch_kv8_mass(const Kv8Attn& a, int num_sms, cudaStream_t s) {
+cudaError_t launch_kv8_mass_few(const Kv8Attn& a, int num_sms, cudaStream_t s) {
   DecodeParams p{a, a.T * a.G, 1, 3 * num_sms < kKv8Ctas ? 3 * num_sms : kKv8Ctas};
   if (a.c.format == CSA2_KV8_E4M3)
-    return a.D == 64 ? mass_as<64, CSA2_KV8_E4M3>(p, s) : mass_as<128, CSA2_KV8_E4M3>(p, s);
-  return a.D == 64 ? mass_as<64, CSA2_KV8_INT8>(p, s) : mass_as<128, CSA2_KV8_INT8>(p, s);
+    return a.D == 64 ? mass_of<64, CSA2_KV8_E4M3>(p, s) : mass_of<128, CSA2_KV8_E4M3>(p, s);
+  return a.D == 64 ? mass_of<64, CSA2_KV8_INT8>(p, s) : mass_of<128, CSA2_KV8_INT8>(p, s);
 }
 
 }  // namespace csa2

@@ -56,7 +56,8 @@ inline int max_active_clusters(Kernel kern, int cluster, int threads, int smem) 
 cudaError_t set_wait_limit_indexer(unsigned long long ns);
 cudaError_t set_wait_limit_attention(unsigned long long ns);
 cudaError_t set_wait_limit_quant(unsigned long long ns);
-cudaError_t set_wait_limit_kv8(unsigned long long ns);
+cudaError_t set_wait_limit_kv8_prefill(unsigned long long ns);
+cudaError_t set_wait_limit_kv8_mass(unsigned long long ns);
 
 // Benchmark instrumentation (api.cu): records the family's begin/end events
 // on stream s when they are set.

@@ -106,10 +106,9 @@ def attention_bounds(q, p, b, h, G, ql, scale, out_half):
     rounded to f16 once, 2^-11.  The output is off by that times A = sum p |v|,
     by the fp32 additions of n terms and of the normaliser's, 2 n 2^-23 A, and
     by its own rounding: half a step, which is out_half of it and, for f16 below
-    2^-14, where the steps are 2^-24 throughout, 2^-25.  Weights far below the largest lose bits: with T G <= 64
-    a weight is held in steps of at least 2^-39 of the largest, else 2^-31 (f16's
-    smallest step 2^-24 over the factor 2^15 or 2^7), an error of half that times
-    max |v| each; and a code times its block's share of the largest scale is held
+    2^-14, where the steps are 2^-24 throughout, 2^-25.  Weights far below the largest lose bits: a weight
+    is held in steps of 2^-31 of the running maximum's (f16's smallest step 2^-24
+    over the factor 2^7), an error of half that times max |v| each; and a code times its block's share of the largest scale is held
     in steps of 2^-24 of that scale, at most max |v| / 63: 2^-25 / 63 < 2^-30 of it.
     """
     n = p.len[b]
@@ -118,7 +117,7 @@ def attention_bounds(q, p, b, h, G, ql, scale, out_half):
     ds = (p.D + 2) * 2.0 ** -23 * big
     rel = 2 * ds + 2.0 ** -20 + 2.0 ** -11 + 2 * n * 2.0 ** -23
     vmax = np.abs(v).max() if n else 0.0
-    tol = a * rel[..., None] + (n * 2.0 ** (-40 if ql * G <= 64 else -32) + 2.0 ** -30) * vmax
+    tol = a * rel[..., None] + (n * 2.0 ** -32 + 2.0 ** -30) * vmax
     tol = tol + out_half * (np.abs(o) + tol) + (2.0 ** -25 if out_half == 2.0 ** -11 else 1e-30)
     ltol = ds + 2.0 ** -20 + n * 2.0 ** -23 + 2.0 ** -22 * np.abs(np.where(np.isfinite(lse), lse, 0))
     return o, lse, tol, ltol
