@@ -38,8 +38,8 @@ struct MassSmem {
   static constexpr int kQSlab = kCols * 128;
   static constexpr int kK = 0;
   static constexpr int kQ = kSlabs * kKSlab;          // 2 stages
-  static constexpr int kConst = kQ + 2 * kSlabs * kQSlab;   // [2 stages][-hi, 2^-lo][256]
-  static constexpr int kSum = kConst + 2 * 2 * kCols * 4;   // [2][128]
+  static constexpr int kConst = kQ + 2 * kSlabs * kQSlab;   // [4][-hi, 2^-lo][256]
+  static constexpr int kSum = kConst + 4 * 2 * kCols * 4;   // [2][128]
   static constexpr int kBars = kSum + 2 * kKeys * 4;
   static constexpr int kFlags = kBars + 128;          // abort, tmem, K's reference scale [4]
   // tensor memory holds one CTA, so a second is kept off the SM
@@ -149,7 +149,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
     for (int64_t id = blockIdx.x; id < total; id += gridDim.x, ++round) {
       const Item it = item_of(p, lane, id);
       uint64_t acc[2] = {0, 0};
-      const float* cst = reinterpret_cast<const float*>(smem + L::kConst) + 2 * kCols * wg;
       // query rows below this one do not see the thread's cached row
       const int64_t see = (int64_t)(it.key0 + key - (it.n - it.ql)) * p.a.G;
       bool got = false;
@@ -166,16 +165,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
           f = p.a.scale_log2 * refs[k & 3];
           fl = p.a.scale_low * refs[k & 3];
         }
+        const float* cst = reinterpret_cast<const float*>(smem + L::kConst) + 2 * kCols * (q & 3);
         const uint64_t f2 = pack2(f, f), fl2 = pack2(fl, fl);
         const int64_t hid64 = see - (int64_t)(it.first + i) * kCols;
         const int hidden = hid64 < 0 ? 0 : (hid64 > kCols ? kCols : (int)hid64);
         const bool masked = __any_sync(0xffffffffu, hidden > 0);
-#pragma unroll 1
-        for (int u = 0; u < kCols / 32; ++u) {
-          uint32_t s[32];
-          tmem_ld32(tS + 32 * u, s);
-          tmem_ld_wait();
-          reg_fence32(s);
+        auto add = [&](const uint32_t (&s)[32], int u) {
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
             const float4 h = *reinterpret_cast<const float4*>(cst + 32 * u + j);
@@ -196,6 +191,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
               acc[e] = fma2(pack2(x, y), gg[e], acc[e]);
             }
           }
+        };
+        // the next columns are on their way while these are worked on
+        uint32_t sa[32], sb[32];
+        tmem_ld32(tS, sa);
+        tmem_ld_wait();
+        reg_fence32(sa);
+#pragma unroll 1
+        for (int u = 0; u < kCols / 32; u += 2) {
+          tmem_ld32(tS + 32 * (u + 1), sb);
+          add(sa, u);
+          tmem_ld_wait();
+          reg_fence32(sb);
+          if (u + 2 < kCols / 32) tmem_ld32(tS + 32 * (u + 2), sa);
+          add(sb, u + 1);
+          tmem_ld_wait();
+          reg_fence32(sa);
         }
         tc_fence_before();
         __syncwarp();
@@ -291,68 +302,78 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
         if (lane == 0) mbar_arrive(k_full);
         ++k;
       }
-      // ---- queries: tile i is copied while tile i - 1 lands
-      auto land = [&](uint32_t t) {      // every copy of tile t is in: hand it over
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full + (t & 1));
+      // ---- queries.  A stage is free once its MMA is done; the constants' four
+      // slots are: the MMA of tile q - 2 waited for the sums of tile q - 4.
+      // Query row r is token r / G, head r % G of the group: each thread keeps
+      // the place of its next row of queries (they go up by 16) and of its next
+      // row of constants (by 128).
+      const int G = p.a.G, r0 = it.first * kCols, g16 = 16 % G, g128 = 128 % G;
+      struct Place {
+        int r, g;
+        int64_t off;
       };
+      auto place = [&](int r, int64_t per_tok, int64_t per_head) {
+        return Place{r, r % G, r / G * per_tok + r % G * per_head};
+      };
+      const int64_t st_ = p.a.q.st, sh_ = p.a.q.sh;
+      auto step = [&](Place& x, int by, int by_head, int64_t by_off, int64_t wrap) {
+        x.r += by;
+        x.g += by_head;
+        x.off += by_off;
+        if (x.g >= G) {
+          x.g -= G;
+          x.off += wrap;
+        }
+      };
+      Place pq = place(r0 + (ct >> 3), st_, sh_), pl = place(r0 + ct, p.a.H, 1);
+      const int64_t q_by = 16 / G * st_ + 16 % G * sh_, q_wrap = st_ - G * sh_;
+      const int64_t l_by = 128 / G * (int64_t)p.a.H + 128 % G, l_wrap = p.a.H - G;
+      const char* qsrc = static_cast<const char*>(p.a.q.data) +
+                         2 * (it.b * p.a.q.sb + (int64_t)it.h * G * sh_ + 8 * (ct & 7));
+      const float* lsrc = p.a.lse + (int64_t)it.b * p.a.T * p.a.H + it.h * G;
+      const int dst = (ct >> 3) * 128 + (((ct & 7) ^ ((ct >> 3) & 7)) << 4);
       for (int i = 0; i < it.nt; ++i, ++q) {
         const int st = q & 1;
-        if (q >= 2) {
-          wait(q_empty + st, ((q >> 1) - 1) & 1);
-          wait(s_empty + st, ((q >> 1) - 1) & 1);
-        }
+        if (q >= 2) wait(q_empty + st, ((q >> 1) - 1) & 1);
         if (!ok) break;
-        const int r0 = (it.first + i) * kCols;
-        uint8_t* stage = smem + L::kQ + st * L::kSlabs * L::kQSlab;
+        const uint32_t stage = smem_u32(smem + L::kQ + st * L::kSlabs * L::kQSlab) + dst;
 #pragma unroll 4
         for (int v = 0; v < kCols / 16; ++v) {
-          const int row = (ct >> 3) + 16 * v, gr = r0 + row;
-          const bool in = gr < it.rows;
-          const int tok = gr / p.a.G;
-          const char* from = static_cast<const char*>(p.a.q.data);
-          if (in)
-            from += 2 * (it.b * p.a.q.sb + tok * p.a.q.st +
-                         (it.h * p.a.G + gr - tok * p.a.G) * p.a.q.sh + 8 * (ct & 7));
+          const bool in = pq.r < it.rows;
+          const char* from = qsrc + (in ? 2 * pq.off : 0);
+          const uint32_t size = in ? 16u : 0u;
 #pragma unroll
-          for (int s = 0; s < L::kSlabs; ++s) {
-            uint8_t* to = stage + s * L::kQSlab + row * 128 + (((ct & 7) ^ (row & 7)) << 4);
-            const uint32_t size = in ? 16u : 0u;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)),
-                         "l"(from + (in ? 128 * s : 0)), "r"(size)
+          for (int s = 0; s < L::kSlabs; ++s)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             stage + s * L::kQSlab + v * 2048),
+                         "l"(from + 128 * s), "r"(size)
                          : "memory");
-          }
+          step(pq, 16, g16, q_by, q_wrap);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        float* cst = reinterpret_cast<float*>(smem + L::kConst) + 2 * kCols * st;
+        float* cst = reinterpret_cast<float*>(smem + L::kConst) + 2 * kCols * (q & 3);
 #pragma unroll
         for (int v = 0; v < kCols / 128; ++v) {
-          const int row = ct + 128 * v, gr = r0 + row;
           float nh = -INFINITY, g = 1.0f;       // no weight
-          if (gr < it.rows) {
-            const int tok = gr / p.a.G;
-            const float y = p.a.lse[((int64_t)it.b * p.a.T + tok) * p.a.H + it.h * p.a.G + gr -
-                                    tok * p.a.G];
+          if (pl.r < it.rows) {
+            const float y = lsrc[pl.off];
             if (y != -INFINITY) {
               const float hi = y * 1.44269502f;
               nh = -hi;
               g = exp2f(-(fmaf(y, 1.44269502f, -hi) + y * 1.92596299e-8f));
             }
           }
-          cst[row] = nh;
-          cst[kCols + row] = g;
+          cst[ct + 128 * v] = nh;
+          cst[kCols + ct + 128 * v] = g;
+          step(pl, 128, g128, l_by, l_wrap);
         }
-        if (i > 0) {
-          asm volatile("cp.async.wait_group 1;" ::: "memory");
-          land(q - 1);
-        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full + st);
       }
       if (!ok) break;
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      land(q - 1);
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else {
     // ================================================================== MMA warp
     const uint32_t fmt = p.a.q.type == CSA2_BF16 ? 1u : 0u;

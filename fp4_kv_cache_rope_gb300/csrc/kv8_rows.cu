@@ -33,31 +33,33 @@ __device__ __forceinline__ Span append_span(const AppendParams& p, int b) {
   return s;
 }
 
+// Largest of the NT threads' values (a warp's or a CTA's).
 template <int NT>
-__device__ __forceinline__ float group_max(float x, float* red, int tid) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  if (NT == 32) {
-    __syncwarp();
-    return x;
-  }
+__device__ __forceinline__ uint32_t group_max(uint32_t x, uint32_t* red, int tid) {
+  x = __reduce_max_sync(0xffffffffu, x);
+  if (NT == 32) return x;
   __syncthreads();         // red may still be read from an earlier call
   if ((tid & 31) == 0) red[tid >> 5] = x;
   __syncthreads();
   x = red[0];
 #pragma unroll
-  for (int i = 1; i < NT / 32; ++i) x = fmaxf(x, red[i]);
+  for (int i = 1; i < NT / 32; ++i) x = max(x, red[i]);
   return x;
 }
 
 // The new rows of one block, head and side (0 K, 1 V), by NT threads (a warp
-// or a CTA).  The rows are held in registers between the block's maximum and
-// their codes, so they are read once.
-template <int D, int ES, int FMT, int NT, int PASSES>
+// or a CTA), 16 bytes a thread and access.  The rows are held in registers
+// between the block's maximum and their codes, so they are read once.  The
+// maximum is taken over the bits of the magnitudes (two 16-bit values at a
+// time), which also shows whether there is an infinity or a NaN.
+// EL: elements per 16 bytes (4 fp32, 8 of 16 bits).
+template <int D, int EL, int FMT, int NT, int PASSES>
 __device__ __forceinline__ void append_block(const AppendParams& p, const Span& sp, int b, int h,
-                                             int side, int blk, float* red, int tid) {
-  constexpr int kLanes = D / 8;            // threads per row, 8 channels each
+                                             int side, int blk, uint32_t* red, int tid) {
+  constexpr int kLanes = D / EL;           // threads per row
   constexpr int kRows = NT / kLanes;
+  constexpr int ES = 16 / EL;
+  static_assert(kRows >= 1, "a row per pass");
   const Kv8& c = p.c;
   const int block = 1 << c.block_shift;
   const int b0 = blk << c.block_shift;
@@ -70,87 +72,97 @@ __device__ __forceinline__ void append_block(const AppendParams& p, const Span& 
     return;
   }
   const Kv8Rows& in = p.in[side];
-  const int sub = tid / kLanes, ch = (tid % kLanes) * 8;
+  const int sub = tid / kLanes, ch = (tid % kLanes) * EL;
   const char* src = static_cast<const char*>(in.data) +
-                    (b * in.sb + (int64_t)(lo - sp.start) * in.st + h * in.sh + ch) * ES;
+                    (b * in.sb + (int64_t)(lo - sp.start + sub) * in.st + h * in.sh + ch) * ES;
+  const int64_t step = (int64_t)kRows * in.st * ES;
   const bool had = sp.start > b0;
   float* scale = c.scales[side] + kv8_block(c, page, h, in_page);
   const float s0 = had ? *scale : 0.0f;
 
-  uint4 raw[PASSES][ES / 2];
+  uint4 raw[PASSES];
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
-    const int r = i * kRows + sub;
-#pragma unroll
-    for (int u = 0; u < ES / 2; ++u) {
-      raw[i][u] = make_uint4(0, 0, 0, 0);
-      if (lo + r < hi)
-        raw[i][u] = reinterpret_cast<const uint4*>(src + (int64_t)r * in.st * ES)[u];
-    }
+    raw[i] = make_uint4(0, 0, 0, 0);
+    if (lo + i * kRows + sub < hi) raw[i] = *reinterpret_cast<const uint4*>(src + i * step);
   }
-  auto values = [&](int i, float (&v)[8]) {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(raw[i]);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (ES == 4) {
-        v[2 * j] = __uint_as_float(w[2 * j]);
-        v[2 * j + 1] = __uint_as_float(w[2 * j + 1]);
-      } else if (in.type == CSA2_BF16) {
-        bf16x2_to_f32(w[j], v[2 * j], v[2 * j + 1]);
-      } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-        v[2 * j] = f.x;
-        v[2 * j + 1] = f.y;
-      }
-    }
-  };
-  float amax = 0.0f;
-  bool odd = false;                        // an infinity or a NaN
+  const uint32_t inf = EL == 4 ? 0x7F800000u : (in.type == CSA2_BF16 ? 0x7F80u : 0x7C00u);
+  uint32_t bits = 0;
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
-    float v[8];
-    values(i, v);
+    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float a = fabsf(v[j]);
-      const bool fin = a <= 3.402823466e38f;
-      odd |= !fin;
-      amax = fmaxf(amax, fin ? a : 0.0f);
-    }
+    for (int j = 0; j < 4; ++j)
+      bits = EL == 4 ? max(bits, w[j] & 0x7FFFFFFFu) : __vmaxu2(bits, w[j] & 0x7FFF7FFFu);
   }
-  if (odd) set_status(p.status, CSA2_DEV_NONFINITE);
-  amax = group_max<NT>(amax, red, tid);    // also: every thread has read s0
+  if (EL == 8) bits = max(bits & 0xFFFFu, bits >> 16);
+  bits = group_max<NT>(bits, red, tid);
+  const bool odd = bits >= inf;            // uniform over the group
+  if (odd) {                               // the maximum of the finite values then
+    if (tid == 0) set_status(p.status, CSA2_DEV_NONFINITE);
+    bits = 0;
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < (EL == 4 ? 1 : 2); ++e) {
+          const uint32_t m = EL == 4 ? w[j] & 0x7FFFFFFFu : (w[j] >> (16 * e)) & 0x7FFFu;
+          if (m < inf) bits = max(bits, m);
+        }
+    }
+    bits = group_max<NT>(bits, red, tid);
+  }
+  __syncwarp();                            // every thread of the group has read s0
+  const float amax = EL == 4 ? __uint_as_float(bits)
+                     : in.type == CSA2_BF16 ? __uint_as_float(bits << 16)
+                                            : __half2float(__ushort_as_half((unsigned short)bits));
   const float s1 = fmaxf(s0, kv8_scale_of<FMT>(amax));
   const float inv = kv8_inverse(s1);
   const int64_t row0 = kv8_row(c, page, h, in_page);
-  uint8_t* dst = c.codes[side] + (row0 + (lo - b0)) * D + ch;
+  uint8_t* dst = c.codes[side] + (row0 + (lo - b0) + sub) * D + ch;
+  const float big = s1 > 0.0f ? (FMT == CSA2_KV8_E4M3 ? 448.0f : 127.0f) : 0.0f;
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
-    const int r = i * kRows + sub;
-    if (lo + r >= hi) continue;
-    float v[8];
-    values(i, v);
+    if (lo + i * kRows + sub >= hi) continue;
+    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+    float v[EL];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = v[j] != v[j] ? 0.0f : v[j] * inv;
-    if (odd) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = v[j] != v[j] ? 0.0f : v[j];   // inf * 0
-    }
-    uint2 w;
-    w.x = kv8_encode4<FMT>(v[0], v[1], v[2], v[3]);
-    w.y = kv8_encode4<FMT>(v[4], v[5], v[6], v[7]);
-    *reinterpret_cast<uint2*>(dst + (int64_t)r * D) = w;
-  }
-  if (s1 > s0) {
-    if (s0 > 0.0f) {                       // the block's earlier rows under the larger scale
-      const float ratio = s0 * inv;
-      uint8_t* old = c.codes[side] + row0 * D + ch;
-      for (int r = sub; r < lo - b0; r += kRows) {
-        uint2 w = *reinterpret_cast<uint2*>(old + (int64_t)r * D);
-        w.x = kv8_recode<FMT>(w.x, ratio);
-        w.y = kv8_recode<FMT>(w.y, ratio);
-        *reinterpret_cast<uint2*>(old + (int64_t)r * D) = w;
+    for (int j = 0; j < 4; ++j) {
+      if (EL == 4) {
+        v[j] = __uint_as_float(w[j]);
+      } else if (in.type == CSA2_BF16) {
+        bf16x2_to_f32(w[j], v[2 * j % EL], v[(2 * j + 1) % EL]);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+        v[2 * j % EL] = f.x;
+        v[(2 * j + 1) % EL] = f.y;
       }
+    }
+#pragma unroll
+    for (int j = 0; j < EL; ++j) {
+      const float x = v[j];
+      v[j] = x * inv;
+      if (odd && !(fabsf(x) <= 3.402823466e38f)) v[j] = x != x ? 0.0f : copysignf(big, x);
+    }
+    uint8_t* to = dst + (int64_t)i * kRows * D;
+    if (EL == 4) {
+      *reinterpret_cast<uint32_t*>(to) = kv8_encode4<FMT>(v[0], v[1], v[2], v[3]);
+    } else {
+      *reinterpret_cast<uint2*>(to) =
+          make_uint2(kv8_encode4<FMT>(v[0], v[1], v[2], v[3]),
+                     kv8_encode4<FMT>(v[4 % EL], v[5 % EL], v[6 % EL], v[7 % EL]));
+    }
+  }
+  if (s1 > s0 && s0 > 0.0f) {              // the block's earlier rows under the larger scale
+    const float ratio = s0 * inv;
+    uint8_t* old = c.codes[side] + row0 * D;
+    for (int i = tid; i < (lo - b0) * D / 8; i += NT) {
+      uint2 w = *reinterpret_cast<uint2*>(old + 8 * i);
+      w.x = kv8_recode<FMT>(w.x, ratio);
+      w.y = kv8_recode<FMT>(w.y, ratio);
+      *reinterpret_cast<uint2*>(old + 8 * i) = w;
     }
   }
   if (tid == 0 && (s1 > s0 || !had)) *scale = s1;
@@ -163,8 +175,8 @@ __device__ __forceinline__ void append_block(const AppendParams& p, const Span& 
 // Appends of a few rows: one CTA per sequence, a warp per (head, side), so that
 // one launch also advances seq_len (every warp reads it before the barrier).
 constexpr int kFewRows = 8;
-template <int D, int ES, int FMT>
-__global__ void __launch_bounds__(1024) kv8_append_few_kernel(AppendParams p) {
+template <int D, int EL, int FMT>
+__global__ void __launch_bounds__(512) kv8_append_few_kernel(AppendParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const int b = blockIdx.x, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -178,14 +190,16 @@ __global__ void __launch_bounds__(1024) kv8_append_few_kernel(AppendParams p) {
   const int first = sp.start >> p.c.block_shift, last = (sp.start + sp.t - 1) >> p.c.block_shift;
   for (int i = threadIdx.x >> 5; i < 2 * p.c.heads; i += warps)
     for (int blk = first; blk <= last; ++blk)
-      append_block<D, ES, FMT, 32, kFewRows * D / 256>(p, sp, b, i >> 1, i & 1, blk, nullptr, lane);
+      append_block<D, EL, FMT, 32, kFewRows * D / EL / 32>(p, sp, b, i >> 1, i & 1, blk, nullptr,
+                                                           lane);
 }
 
-// Longer appends: one CTA per (block, head, side, sequence).
+// Longer appends: one CTA per (block, head, side, sequence).  PASSES: 16-byte
+// accesses of a thread that hold a whole block.
 constexpr int kAppendThreads = 256;
-template <int D, int ES, int FMT>
+template <int D, int EL, int FMT, int PASSES>
 __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendParams p) {
-  __shared__ float red[kAppendThreads / 32];
+  __shared__ uint32_t red[kAppendThreads / 32];
   griddep_wait();
   griddep_launch_dependents();
   const int b = blockIdx.z;
@@ -195,7 +209,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendParams
     if (p.own_len) p.c.seq_len[b] = sp.start + sp.t;
   }
   if (sp.t == 0) return;
-  append_block<D, ES, FMT, kAppendThreads, D / 16>(p, sp, b, blockIdx.y >> 1, blockIdx.y & 1,
+  append_block<D, EL, FMT, kAppendThreads, PASSES>(p, sp, b, blockIdx.y >> 1, blockIdx.y & 1,
                                                    (sp.start >> p.c.block_shift) + blockIdx.x, red,
                                                    threadIdx.x);
 }
@@ -208,19 +222,25 @@ __global__ void kv8_advance_kernel(AppendParams p) {
   p.c.seq_len[b] = sp.start + sp.t;
 }
 
-template <int D, int ES, int FMT>
+template <int D, int EL, int FMT>
 cudaError_t append_as(const AppendParams& p0, cudaStream_t s) {
   AppendParams p = p0;
   if (p.T <= kFewRows) {
-    const int warps = 2 * p.c.heads < 32 ? 2 * p.c.heads : 32;
-    return kv8_launch(kv8_append_few_kernel<D, ES, FMT>, dim3(p.c.batch), 32 * warps, 0, s, p);
+    const int warps = 2 * p.c.heads < 16 ? 2 * p.c.heads : 16;
+    return kv8_launch(kv8_append_few_kernel<D, EL, FMT>, dim3(p.c.batch), 32 * warps, 0, s, p);
   }
   const int block = 1 << p.c.block_shift;
+  const dim3 grid((p.T + block - 2) / block + 1, 2 * p.c.heads, p.c.batch);
   // with `start` given nothing in the launch reads seq_len, so it may write it
   p.own_len = p.start != nullptr;
-  cudaError_t e = kv8_launch(kv8_append_kernel<D, ES, FMT>,
-                         dim3((p.T + block - 2) / block + 1, 2 * p.c.heads, p.c.batch),
-                         kAppendThreads, 0, s, p);
+  constexpr int kMost = 128 * D / EL / kAppendThreads;   // passes of 128 rows
+  cudaError_t e;
+  if (block == 128)
+    e = kv8_launch(kv8_append_kernel<D, EL, FMT, kMost>, grid, kAppendThreads, 0, s, p);
+  else if (block == 64)
+    e = kv8_launch(kv8_append_kernel<D, EL, FMT, kMost / 2>, grid, kAppendThreads, 0, s, p);
+  else
+    e = kv8_launch(kv8_append_kernel<D, EL, FMT, kMost / 4>, grid, kAppendThreads, 0, s, p);
   if (e != cudaSuccess || p.own_len) return e;
   return kv8_launch(kv8_advance_kernel, dim3((p.c.batch + 127) / 128), 128, 0, s, p);
 }
@@ -228,8 +248,8 @@ template <int D>
 cudaError_t append_of(const AppendParams& p, cudaStream_t s) {
   const bool wide = p.in[0].type == CSA2_F32;
   if (p.c.format == CSA2_KV8_E4M3)
-    return wide ? append_as<D, 4, CSA2_KV8_E4M3>(p, s) : append_as<D, 2, CSA2_KV8_E4M3>(p, s);
-  return wide ? append_as<D, 4, CSA2_KV8_INT8>(p, s) : append_as<D, 2, CSA2_KV8_INT8>(p, s);
+    return wide ? append_as<D, 4, CSA2_KV8_E4M3>(p, s) : append_as<D, 8, CSA2_KV8_E4M3>(p, s);
+  return wide ? append_as<D, 4, CSA2_KV8_INT8>(p, s) : append_as<D, 8, CSA2_KV8_INT8>(p, s);
 }
 
 // ------------------------------------------------------------------- eviction
@@ -250,26 +270,38 @@ __device__ __forceinline__ uint32_t rank_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Which rows stay, one CTA per (head, sequence): the threshold among the rows
-// between the sink and the recent ones by a radix select over the order keys of
-// their mass (8 bits a pass), then the kept rows in order by a running count.
+// Which rows stay.  A cluster of CTAs per (head, sequence); each warp has a run
+// of consecutive rows.  The need-th largest key is found 8 bits a pass: every
+// CTA counts its rows' digits, the counts are added up over the cluster, and all
+// CTAs walk the sum alike.  Rows above that key stay, and of those at it the
+// first ones in order; both are counted per warp first, so that every warp knows
+// its rows' places in `kept`.  Bound by latency (one round of the cluster's
+// barrier per pass), not by the 4 bytes per row that it reads.
 constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelHeld = 16;       // keys that a thread keeps in registers
 __global__ void __launch_bounds__(kSelThreads) kv8_evict_select_kernel(EvictParams p) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t sh_prefix, sh_need;
-  __shared__ int wsum[2][32];
+  __shared__ uint32_t hist[2][256];                // this CTA's counts, by pass parity
+  __shared__ uint32_t sum[256];
+  __shared__ uint32_t sh_digit, sh_need;
+  __shared__ int cnt[2][kSelWarps];                // rows above / at the threshold, per warp
+  __shared__ int total[2];
+  const Kv8& c = p.src;
+  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = cluster_rank(), size = cluster_size();
   griddep_wait();
   griddep_launch_dependents();
-  const Kv8& c = p.src;
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = kv8_len(c, b);
-  if (h == 0 && tid == 0) p.old_len[b] = n;
+  if (h == 0 && rank == 0 && tid == 0) p.old_len[b] = n;
   int32_t* kept = p.kept + ((int64_t)b * c.heads + h) * p.keep;
-  if (n <= p.keep) {
-    for (int i = tid; i < p.keep; i += kSelThreads) kept[i] = i < n ? i : -1;
+  if (n <= p.keep) {                               // uniform over the cluster
+    for (int i = rank * kSelThreads + tid; i < p.keep; i += size * kSelThreads)
+      kept[i] = i < n ? i : -1;
     return;
   }
-  const int lo = p.sink, hi = n - p.recent;      // the ranked rows
+  const int lo = p.sink, hi = n - p.recent;        // the ranked rows
+  const int per = (n + size * kSelWarps * 32 - 1) / (size * kSelWarps * 32);   // rows a thread
+  const int row0 = (rank * kSelWarps + warp) * per * 32 + lane;
   auto key_at = [&](int j) -> uint32_t {
     int in_page;
     const int page = kv8_page(c, b, j, in_page);
@@ -279,112 +311,141 @@ __global__ void __launch_bounds__(kSelThreads) kv8_evict_select_kernel(EvictPara
     }
     return rank_key(c.mass[kv8_row(c, page, h, in_page)]);
   };
-  if (tid == 0) {
-    sh_prefix = 0;
-    sh_need = (uint32_t)(p.keep - p.sink - p.recent);
+  uint32_t held[kSelHeld];
+#pragma unroll
+  for (int e = 0; e < kSelHeld; ++e) {
+    const int j = row0 + 32 * e;
+    held[e] = 0;
+    if (e < per && j >= lo && j < hi) held[e] = key_at(j);
+  }
+  // f(row, key) for each ranked row of the thread, in order
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int e = 0; e < kSelHeld; ++e) {
+      const int j = row0 + 32 * e;
+      if (e < per) f(j, j >= lo && j < hi, held[e]);
+    }
+    for (int e = kSelHeld; e < per; ++e) {
+      const int j = row0 + 32 * e;
+      const bool in = j >= lo && j < hi;
+      f(j, in, in ? key_at(j) : 0u);
+    }
+  };
+  uint32_t prefix = 0;
+  uint32_t need = (uint32_t)(p.keep - p.sink - p.recent);
+  const bool any = need > 0;
+  for (int shift = 24; any && shift >= 0; shift -= 8) {
+    uint32_t* mine = hist[(shift >> 3) & 1];
+    if (tid < 256) mine[tid] = 0;
+    __syncthreads();
+    const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
+    each([&](int, bool in, uint32_t k) {
+      if (in && (k & mask) == prefix) atomicAdd(&mine[(k >> shift) & 255u], 1u);
+    });
+    cluster_sync();
+    if (tid < 256) {
+      uint32_t s = 0;
+      for (int r = 0; r < size; ++r) s += peer_u32(&mine[tid], r);
+      sum[tid] = s;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      // lane l: digits 255 - 8 l downwards; how many rows lie above them
+      uint32_t own = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) own += sum[255 - 8 * lane - i];
+      uint32_t above = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, above, o);
+        if (lane >= o) above += y;
+      }
+      above -= own;
+      if (above < need && above + own >= need) {
+        uint32_t left = need - above;
+        int d = 255 - 8 * lane;
+        for (; sum[d] < left; --d) left -= sum[d];
+        sh_digit = (uint32_t)d;
+        sh_need = left;
+      }
+    }
+    __syncthreads();
+    prefix |= sh_digit << shift;
+    need = sh_need;                                // rows at the threshold that stay
+  }
+  // ---- counts per warp, then the number of kept rows in front of it
+  int above = 0, at = 0;
+  each([&](int j, bool in, uint32_t k) {
+    const bool up = j < n && (!in || (any && k > prefix));
+    above += __popc(__ballot_sync(0xffffffffu, up));
+    at += __popc(__ballot_sync(0xffffffffu, in && any && k == prefix));
+  });
+  if (lane == 0) {
+    cnt[0][warp] = above;
+    cnt[1][warp] = at;
   }
   __syncthreads();
-  // after pass i: the top 8 (i+1) bits of the need-th largest key
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    const uint32_t prefix = sh_prefix;
-    const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-    for (int j = lo + tid; j < hi; j += kSelThreads) {
-      const uint32_t k = key_at(j);
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
-    }
-    __syncthreads();
-    if (tid == 0) {
-      uint32_t need = sh_need;
-      int d = 255;
-      for (; d > 0 && hist[d] < need; --d) need -= hist[d];
-      sh_prefix = prefix | ((uint32_t)d << shift);
-      sh_need = need;                            // how many of the rows at the threshold stay
-    }
-    __syncthreads();
+  if (tid < 2) {
+    int t = 0;
+    for (int w = 0; w < kSelWarps; ++w) t += cnt[tid][w];
+    total[tid] = t;
   }
-  const uint32_t thr = sh_prefix;
-  const uint32_t ties = p.keep - p.sink - p.recent == 0 ? 0u : sh_need;
-  // in order: rows above the threshold, and the first `ties` rows at it
-  int out = 0;
-  uint32_t tied = 0;
-  for (int base = 0; base < n; base += kSelThreads) {
-    const int j = base + tid;
-    bool always = j < n && (j < lo || j >= hi), above = false, at = false;
-    if (j >= lo && j < hi && p.keep > p.sink + p.recent) {
-      const uint32_t k = key_at(j);
-      above = k > thr;
-      at = k == thr;
-    }
-    const uint32_t bt = __ballot_sync(0xffffffffu, at);
-    if (lane == 0) wsum[0][warp] = __popc(bt);
-    __syncthreads();
-    int before = 0, all = 0;
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      before += w < warp ? wsum[0][w] : 0;
-      all += wsum[0][w];
-    }
-    const uint32_t rank = tied + before + __popc(bt & ((1u << lane) - 1u));
-    const bool keep = always || above || (at && rank < ties);
-    tied += all;
-    const uint32_t bk = __ballot_sync(0xffffffffu, keep);
-    if (lane == 0) wsum[1][warp] = __popc(bk);
-    __syncthreads();
-    before = 0;
-    all = 0;
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      before += w < warp ? wsum[1][w] : 0;
-      all += wsum[1][w];
-    }
-    const int at_out = out + before + __popc(bk & ((1u << lane) - 1u));
-    if (keep && at_out < p.keep) kept[at_out] = j;
-    out += all;
+  cluster_sync();
+  int before_up = 0, before_at = 0;
+  for (int r = 0; r < rank; ++r) {
+    before_up += (int)peer_u32(&total[0], r);
+    before_at += (int)peer_u32(&total[1], r);
   }
+  for (int w = 0; w < warp; ++w) {
+    before_up += cnt[0][w];
+    before_at += cnt[1][w];
+  }
+  const uint32_t under = (1u << lane) - 1u;
+  each([&](int j, bool in, uint32_t k) {
+    const bool up = j < n && (!in || (any && k > prefix)), eq = in && any && k == prefix;
+    const uint32_t bu = __ballot_sync(0xffffffffu, up), be = __ballot_sync(0xffffffffu, eq);
+    const int r = before_at + __popc(be & under);  // place among the rows at the threshold
+    const bool stay = up || (eq && r < (int)need);
+    const int to = before_up + __popc(bu & under) + min(r, (int)need);
+    if (stay && to < p.keep) kept[to] = j;
+    before_up += __popc(bu);
+    before_at += __popc(be);
+  });
+  cluster_sync();                                  // peers may still read this CTA's counts
 }
 
-// One block of the result, by a CTA: the kept rows' codes in registers, their
-// largest value, the new scale, the codes re-expressed.  Every read of the
-// source comes before the first write.
+// A block of the result: its rows' codes (one side) in the registers of a CTA,
+// 16 codes a thread and pass.
 constexpr int kMoveThreads = 256;
-template <int D, int FMT>
-__device__ void move_block(const EvictParams& p, int b, int h, int blk, int m, const int32_t* kept,
-                           float* red) {
-  constexpr int kLanes = D / 16;              // threads per row, 16 codes each
-  constexpr int kRows = kMoveThreads / kLanes;
-  constexpr int kPasses = 128 / kRows;
-  const Kv8 &s = p.src, &d = p.dst;
-  const int block = 1 << d.block_shift, b0 = blk << d.block_shift;
-  const int rows = min(block, m - b0);
-  const int tid = threadIdx.x, sub = tid / kLanes, ch = (tid % kLanes) * 16;
-  int from[kPasses];
-  bool moved = false;
+constexpr int kMoveCluster = 8;
+template <int D, int FMT, int PASSES>
+struct MovedBlock {
+  static constexpr int kLanes = D / 16, kRows = kMoveThreads / kLanes;
+  uint4 code[PASSES];
+  float scale[PASSES], mass[PASSES];
+  float amax;
+  int rows;
+  bool moved;
+
+  // reads the rows; every thread of the CTA gets the block's largest value
+  __device__ __forceinline__ void read(const EvictParams& p, int b, int h, int side, int blk, int m,
+                                       const int32_t* kept, uint32_t* red) {
+    const Kv8& s = p.src;
+    const int b0 = blk << p.dst.block_shift;
+    rows = min(1 << p.dst.block_shift, m - b0);
+    const int sub = threadIdx.x / kLanes, ch = (threadIdx.x % kLanes) * 16;
+    bool other = false;
+    float big = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int r = i * kRows + sub;
-    from[i] = r < rows ? kept[b0 + r] : -1;
-    moved |= r < rows && from[i] != b0 + r;
-  }
-  moved = __syncthreads_or(moved);
-  if (p.in_place && !moved) return;
-  int din;
-  const int dpage = kv8_page(d, b, b0, din);
-  if (dpage < 0 && tid == 0) set_status(p.status, CSA2_DEV_BAD_PAGE);
-  const int64_t drow = kv8_row(d, dpage < 0 ? 0 : dpage, h, din);
-  float mass[kPasses];
-#pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    uint4 code[kPasses];
-    float scale[kPasses];
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
+    for (int i = 0; i < PASSES; ++i) {
+      const int r = i * kRows + sub;
       code[i] = make_uint4(0, 0, 0, 0);
-      scale[i] = 0.0f;
-      if (side == 0) mass[i] = 0.0f;
-      if (from[i] < 0) continue;
+      scale[i] = mass[i] = 0.0f;
+      if (r >= rows) continue;
+      const int from = kept[b0 + r];
+      other |= from != b0 + r;
       int in_page;
-      const int page = kv8_page(s, b, from[i], in_page);
+      const int page = kv8_page(s, b, from, in_page);
       if (page < 0) {
         set_status(p.status, CSA2_DEV_BAD_PAGE);
         continue;
@@ -392,20 +453,31 @@ __device__ void move_block(const EvictParams& p, int b, int h, int blk, int m, c
       const int64_t row = kv8_row(s, page, h, in_page);
       code[i] = *reinterpret_cast<const uint4*>(s.codes[side] + row * D + ch);
       scale[i] = s.scales[side][kv8_block(s, page, h, in_page)];
-      if (side == 0 && s.mass) mass[i] = s.mass[row];
+      if (side == 0) mass[i] = s.mass[row];
     }
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
+    for (int i = 0; i < PASSES; ++i) {
       const uint32_t mx = max(max(kv8_max4<FMT>(code[i].x), kv8_max4<FMT>(code[i].y)),
                               max(kv8_max4<FMT>(code[i].z), kv8_max4<FMT>(code[i].w)));
-      amax = fmaxf(amax, kv8_mag<FMT>(mx) * scale[i]);
+      big = fmaxf(big, kv8_mag<FMT>(mx) * scale[i]);
     }
-    amax = group_max<kMoveThreads>(amax, red, tid);   // every read is behind this
-    const float s1 = kv8_scale_of<FMT>(amax);
-    const float inv = kv8_inverse(s1);
-    if (dpage < 0) continue;
+    moved = __syncthreads_or(other);
+    // magnitudes compare as their bits do
+    amax = __uint_as_float(group_max<kMoveThreads>(__float_as_uint(big), red, threadIdx.x));
+  }
+  __device__ __forceinline__ void write(const EvictParams& p, int b, int h, int side, int blk) {
+    const Kv8& d = p.dst;
+    int din;
+    const int page = kv8_page(d, b, blk << d.block_shift, din);
+    if (page < 0) {
+      if (threadIdx.x == 0) set_status(p.status, CSA2_DEV_BAD_PAGE);
+      return;
+    }
+    const int64_t drow = kv8_row(d, page, h, din);
+    const int sub = threadIdx.x / kLanes, ch = (threadIdx.x % kLanes) * 16;
+    const float s1 = kv8_scale_of<FMT>(amax), inv = kv8_inverse(s1);
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
+    for (int i = 0; i < PASSES; ++i) {
       const int r = i * kRows + sub;
       if (r >= rows) continue;
       uint4 w = code[i];
@@ -418,35 +490,77 @@ __device__ void move_block(const EvictParams& p, int b, int h, int blk, int m, c
       }
       *reinterpret_cast<uint4*>(d.codes[side] + (drow + r) * D + ch) = w;
       if (side == 0 && ch == 0 && d.mass) d.mass[drow + r] = mass[i];
-      if (r == 0 && ch == 0) d.scales[side][kv8_block(d, dpage, h, din)] = moved ? s1 : scale[i];
+      if (r == 0 && ch == 0) d.scales[side][kv8_block(d, page, h, din)] = moved ? s1 : scale[i];
     }
+  }
+};
+
+// Into another cache: one CTA per (block, side, head, sequence).  In place: a
+// cluster per (side, head, sequence) walks the blocks upwards, one block a CTA
+// and round; it reads a round's rows, meets at the cluster's barrier, and writes
+// them.  A kept row never moves to a later place, so the sources of the rounds
+// still to come lie behind the rows being written.
+template <int D, int FMT, int PASSES, bool PLACE>
+__global__ void __launch_bounds__(kMoveThreads) kv8_evict_move_kernel(EvictParams p) {
+  __shared__ uint32_t red[kMoveThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int h = blockIdx.y >> 1, side = blockIdx.y & 1, b = blockIdx.z;
+  const int n = p.old_len[b], m = min(n, p.keep);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.dst.seq_len[b] = m;
+  const int32_t* kept = p.kept + ((int64_t)b * p.src.heads + h) * p.keep;
+  const int blocks = (m + (1 << p.dst.block_shift) - 1) >> p.dst.block_shift;
+  MovedBlock<D, FMT, PASSES> x;
+  if (!PLACE) {
+    if ((int)blockIdx.x >= blocks) return;
+    x.read(p, b, h, side, blockIdx.x, m, kept, red);
+    x.write(p, b, h, side, blockIdx.x);
+    return;
+  }
+  if (n == m) return;                              // uniform over the cluster
+  for (int first = 0; first < blocks; first += kMoveCluster) {
+    const int blk = first + (int)blockIdx.x;       // the cluster is the grid's x
+    const bool mine = blk < blocks;
+    if (mine) x.read(p, b, h, side, blk, m, kept, red);
+    cluster_sync();
+    if (mine && x.moved) x.write(p, b, h, side, blk);
   }
 }
 
-// Into another cache: one CTA per (block, head, sequence).  In place: one CTA
-// per (head, sequence) walks the blocks upwards.  A kept row never moves to a
-// later place, so the sources of the blocks still to come lie behind the block
-// being written.
-template <int D, int FMT>
-__global__ void __launch_bounds__(kMoveThreads) kv8_evict_move_kernel(EvictParams p) {
-  __shared__ float red[kMoveThreads / 32];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int h = blockIdx.y, b = blockIdx.z;
-  const int n = p.old_len[b], m = min(n, p.keep);
-  if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) p.dst.seq_len[b] = m;
-  if (p.in_place && n == m) return;
-  const int32_t* kept = p.kept + ((int64_t)b * p.src.heads + h) * p.keep;
-  const int blocks = (m + (1 << p.dst.block_shift) - 1) >> p.dst.block_shift;
-  for (int blk = blockIdx.x; blk < blocks; blk += gridDim.x)
-    move_block<D, FMT>(p, b, h, blk, m, kept, red);
+template <typename... A>
+cudaError_t launch_cluster(void (*kern)(A...), dim3 grid, int threads, int cluster, cudaStream_t s,
+                           A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2] = {pdl_attribute()};
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int D, int FMT>
+template <int D, int FMT, int PASSES>
 cudaError_t move_as(const EvictParams& p, cudaStream_t s) {
   const int blocks = (p.keep + (1 << p.dst.block_shift) - 1) >> p.dst.block_shift;
-  return kv8_launch(kv8_evict_move_kernel<D, FMT>,
-                dim3(p.in_place ? 1 : blocks, p.src.heads, p.src.batch), kMoveThreads, 0, s, p);
+  const dim3 grid(p.in_place ? kMoveCluster : blocks, 2 * p.src.heads, p.src.batch);
+  return p.in_place ? launch_cluster(kv8_evict_move_kernel<D, FMT, PASSES, true>, grid, kMoveThreads,
+                                     kMoveCluster, s, p)
+                    : kv8_launch(kv8_evict_move_kernel<D, FMT, PASSES, false>, grid, kMoveThreads, 0,
+                                 s, p);
+}
+template <int D, int FMT>
+cudaError_t move_of(const EvictParams& p, cudaStream_t s) {
+  constexpr int kMost = 128 * (D / 16) / kMoveThreads;   // passes of 128 rows
+  switch (p.dst.block_shift) {
+    case 7: return move_as<D, FMT, kMost>(p, s);
+    case 6: return move_as<D, FMT, kMost / 2>(p, s);
+    default: return move_as<D, FMT, (kMost > 3 ? kMost / 4 : 1)>(p, s);
+  }
 }
 
 }  // namespace
@@ -462,12 +576,14 @@ cudaError_t launch_kv8_evict(const Kv8& src, const Kv8& dst, bool in_place, int 
                              int sink, int recent, int32_t* kept, int32_t* old_len,
                              uint32_t* status, int num_sms, cudaStream_t s) {
   EvictParams p{src, dst, keep, sink, recent, kept, old_len, status, in_place ? 1 : 0};
-  cudaError_t e = kv8_launch(kv8_evict_select_kernel, dim3(src.heads, src.batch), kSelThreads, 0,
-                         s, p);
+  // one CTA holds 16 K rows in registers; longer caches are spread over eight
+  const int cluster = src.max_len <= 8192 ? 1 : 8;
+  cudaError_t e = launch_cluster(kv8_evict_select_kernel, dim3(cluster, src.heads, src.batch),
+                                 kSelThreads, cluster, s, p);
   if (e != cudaSuccess) return e;
   if (src.format == CSA2_KV8_E4M3)
-    return D == 64 ? move_as<64, CSA2_KV8_E4M3>(p, s) : move_as<128, CSA2_KV8_E4M3>(p, s);
-  return D == 64 ? move_as<64, CSA2_KV8_INT8>(p, s) : move_as<128, CSA2_KV8_INT8>(p, s);
+    return D == 64 ? move_of<64, CSA2_KV8_E4M3>(p, s) : move_of<128, CSA2_KV8_E4M3>(p, s);
+  return D == 64 ? move_of<64, CSA2_KV8_INT8>(p, s) : move_of<128, CSA2_KV8_INT8>(p, s);
 }
 
 }  // namespace csa2

@@ -360,7 +360,7 @@ def weights(p, kind):
 
 
 @pytest.mark.parametrize("into", ["place", "cache", "pool"])
-@pytest.mark.parametrize("i,fmt", [(i, f) for i in range(8) for f in (O.E4M3, O.INT8)])
+@pytest.mark.parametrize("i,fmt", [(i, f) for i in range(10) for f in (O.E4M3, O.INT8)])
 def test_evict(i, fmt, into):
     B, Hkv, D, lens, block, page, keep, sink, recent, kind = [
         (2, 2, 64, [300, 50], 16, 16, 100, 4, 20, "plain"),
@@ -370,7 +370,9 @@ def test_evict(i, fmt, into):
         (2, 1, 64, [400, 0], 16, 48, 1, 0, 0, "odd"),
         (2, 2, 128, [400, 399], 16, 16, 130, 130, 0, "ties"),
         (1, 2, 64, [2300], 32, 64, 1999, 3, 10, "odd"),
-        (2, 2, 64, [600, 555], 64, 0, 200, 4, 32, "equal")][i]
+        (2, 2, 64, [600, 555], 64, 0, 200, 4, 32, "equal"),
+        (2, 1, 64, [9000, 8999], 64, 64, 3000, 7, 100, "ties"),      # spread over eight CTAs
+        (1, 1, 64, [140000], 128, 128, 20001, 0, 1, "ties")][i]      # keys beyond the registers
     p = filled(B, Hkv, D, lens, block, page, fmt, seed=200 + i, cap=max(lens) + 7)
     # a few tokens one by one: blocks whose scale is larger than their rows need
     ws = p.c.workspace(1, Hkv)
