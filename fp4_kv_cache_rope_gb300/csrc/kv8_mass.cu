@@ -15,12 +15,14 @@
 // part of f = c log2(e) in a second fma; lo enters as the factor 2^-lo of the
 // sum's fma.  With one part each the weights would be off by 1e-6.
 //
-// Each cached row is written by one thread; its sum is that of the even query
-// tiles (warps 0-3) plus that of the odd ones (warps 4-7), in a fixed order.
+// A cached row is one thread's in each of four warp groups: even and odd query
+// tiles, left and right half of their columns.  Their four sums are added in a
+// fixed order and written by the first group.
 //
-// Warps (416 threads): 0-3 and 4-7 exponentials of even and odd query tiles;
-// 8-11 load (K into its tile, queries by 16-byte asynchronous copies into a
-// two-stage ring); 12 issues the MMAs.
+// Warps (672 threads): 0-15 exponentials; 16-19 load (K into its tile, queries
+// by 16-byte asynchronous copies into a two-stage ring); 20 issues the MMAs.
+#include <type_traits>
+
 #include "kv8_mma.cuh"
 
 namespace csa2 {
@@ -29,7 +31,8 @@ namespace {
 constexpr int kKeys = 128;
 static_assert(kKeys == kKv8Step, "the items are the steps of the split");
 constexpr int kCols = 256;
-constexpr int kThreads = 416;
+constexpr int kThreads = 672;
+constexpr int kExpWarps = 16;
 
 template <int D>
 struct MassSmem {
@@ -39,8 +42,8 @@ struct MassSmem {
   static constexpr int kK = 0;
   static constexpr int kQ = kSlabs * kKSlab;          // 2 stages
   static constexpr int kConst = kQ + 2 * kSlabs * kQSlab;   // [4][-hi, 2^-lo][256]
-  static constexpr int kSum = kConst + 4 * 2 * kCols * 4;   // [2][128]
-  static constexpr int kBars = kSum + 2 * kKeys * 4;
+  static constexpr int kSum = kConst + 4 * 2 * kCols * 4;   // [2][3][128]
+  static constexpr int kBars = kSum + 2 * 3 * kKeys * 4;
   static constexpr int kFlags = kBars + 128;          // abort, tmem, K's reference scale [4]
   // tensor memory holds one CTA, so a second is kept off the SM
   static constexpr int kBytes = kFlags + 64 < 120 * 1024 ? 120 * 1024 : kFlags + 64;
@@ -103,8 +106,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
   uint64_t* q_full = bars + 2;    // [2] 4 warps
   uint64_t* q_empty = bars + 4;   // [2] commit
   uint64_t* s_full = bars + 6;    // [2] commit
-  uint64_t* s_empty = bars + 8;   // [2] 4 warps
-  uint64_t* x_full = bars + 10;   // [2] 4 warps: the odd tiles' sums of a round are there
+  uint64_t* s_empty = bars + 8;   // [2] 8 warps
+  uint64_t* x_full = bars + 10;   // [2] 12 warps: the other groups' sums of a round are there
   uint64_t* x_empty = bars + 12;  // [2] 4 warps: ... were read
   uint64_t* drain = bars + 14;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kFlags);
@@ -117,15 +120,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
       mbar_init(q_full + i, 4);
       mbar_init(q_empty + i, 1);
       mbar_init(s_full + i, 1);
-      mbar_init(s_empty + i, 4);
-      mbar_init(x_full + i, 4);
+      mbar_init(s_empty + i, 8);
+      mbar_init(x_full + i, 12);
       mbar_init(x_empty + i, 4);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 12) tmem_alloc(tmem_slot, 512);
+  if (warp == kExpWarps + 4) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   griddep_wait();
   griddep_launch_dependents();
@@ -139,14 +142,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
   };
   const int64_t total = kv8_total(c, lane) * c.heads;
 
+  // Items go out in rounds, forwards and backwards in turn: the first tiles of a
+  // sequence are seen by the most queries, so long and short ones pair up.  -1: no
+  // more (a round that a CTA misses is its last).
+  auto item_id = [&](uint32_t round) -> int64_t {
+    const int64_t id = (int64_t)round * gridDim.x +
+                       (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    return id < total ? id : -1;
+  };
   // q counts the CTA's query tiles over all items, k its items with queries
   uint32_t q = 0, k = 0, round = 0;
-  if (warp < 8) {
+  if (warp < kExpWarps) {
     // ======================================================== exponential warps
-    const int wg = warp >> 2, key = 32 * (warp & 3) + lane;
-    const uint32_t tS = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kCols * wg;
+    const int wg = warp >> 2, buf = wg >> 1, half = wg & 1, key = 32 * (warp & 3) + lane;
+    const uint32_t tS =
+        tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kCols * buf + kCols / 2 * half;
     float* sums = reinterpret_cast<float*>(smem + L::kSum);
-    for (int64_t id = blockIdx.x; id < total; id += gridDim.x, ++round) {
+    for (int64_t id; (id = item_id(round)) >= 0; ++round) {
       const Item it = item_of(p, lane, id);
       uint64_t acc[2] = {0, 0};
       // query rows below this one do not see the thread's cached row
@@ -154,8 +166,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
       bool got = false;
       float f = 0.0f, fl = 0.0f;
       for (int i = 0; i < it.nt; ++i, ++q) {
-        if ((q & 1) != (uint32_t)wg) continue;
-        wait(s_full + wg, (q >> 1) & 1);
+        if ((q & 1) != (uint32_t)buf) continue;
+        wait(s_full + buf, (q >> 1) & 1);
         tc_fence_after();
         if (!ok) break;
         if (!got) {
@@ -165,12 +177,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
           f = p.a.scale_log2 * refs[k & 3];
           fl = p.a.scale_low * refs[k & 3];
         }
-        const float* cst = reinterpret_cast<const float*>(smem + L::kConst) + 2 * kCols * (q & 3);
+        const float* cst = reinterpret_cast<const float*>(smem + L::kConst) + 2 * kCols * (q & 3) +
+                           kCols / 2 * half;
         const uint64_t f2 = pack2(f, f), fl2 = pack2(fl, fl);
-        const int64_t hid64 = see - (int64_t)(it.first + i) * kCols;
+        const int64_t hid64 = see - (int64_t)(it.first + i) * kCols - kCols / 2 * half;
         const int hidden = hid64 < 0 ? 0 : (hid64 > kCols ? kCols : (int)hid64);
-        const bool masked = __any_sync(0xffffffffu, hidden > 0);
-        auto add = [&](const uint32_t (&s)[32], int u) {
+        auto add = [&](auto masked, int u) {
+          uint32_t s[32];
+          tmem_ld32(tS + 32 * u, s);
+          tmem_ld_wait();
+          reg_fence32(s);
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
             const float4 h = *reinterpret_cast<const float4*>(cst + 32 * u + j);
@@ -184,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
               unpack2(fma2(s2, fl2, fma2(s2, f2, hh[e])), x, y);
               x = kv8_exp2(x);
               y = kv8_exp2(y);
-              if (masked) {
+              if (decltype(masked)::value) {
                 if (32 * u + j + 2 * e < hidden) x = 0.0f;
                 if (32 * u + j + 2 * e + 1 < hidden) y = 0.0f;
               }
@@ -192,25 +208,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
             }
           }
         };
-        // the next columns are on their way while these are worked on
-        uint32_t sa[32], sb[32];
-        tmem_ld32(tS, sa);
-        tmem_ld_wait();
-        reg_fence32(sa);
+        if (__any_sync(0xffffffffu, hidden > 0)) {
 #pragma unroll 1
-        for (int u = 0; u < kCols / 32; u += 2) {
-          tmem_ld32(tS + 32 * (u + 1), sb);
-          add(sa, u);
-          tmem_ld_wait();
-          reg_fence32(sb);
-          if (u + 2 < kCols / 32) tmem_ld32(tS + 32 * (u + 2), sa);
-          add(sb, u + 1);
-          tmem_ld_wait();
-          reg_fence32(sa);
+          for (int u = 0; u < kCols / 64; ++u) add(std::true_type{}, u);
+        } else {
+#pragma unroll 1
+          for (int u = 0; u < kCols / 64; ++u) add(std::false_type{}, u);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(s_empty + wg);
+        if (lane == 0) mbar_arrive(s_empty + buf);
       }
       if (!ok) break;
       k += it.nt > 0;
@@ -219,17 +226,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
       unpack2(acc[1], a2, a3);
       const float sum = (a0 + a1) + (a2 + a3);
       // (waits with a limit, not a named barrier: a warp may have given up)
-      if (wg == 1) {
+      float* slot = sums + (round & 1) * 3 * kKeys + key;
+      if (wg > 0) {
         if (round >= 2) wait(x_empty + (round & 1), ((round >> 1) - 1) & 1);
         if (!ok) break;
-        sums[(round & 1) * kKeys + key] = sum;
+        slot[(wg - 1) * kKeys] = sum;
         __syncwarp();
         if (lane == 0) mbar_arrive(x_full + (round & 1));
         continue;
       }
       wait(x_full + (round & 1), (round >> 1) & 1);
       if (!ok) break;
-      const float other = sums[(round & 1) * kKeys + key];
+      const float other = (slot[0] + slot[kKeys]) + slot[2 * kKeys];
       __syncwarp();
       if (lane == 0) mbar_arrive(x_empty + (round & 1));
       if (it.key0 + key < it.n) {
@@ -244,11 +252,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
         }
       }
     }
-  } else if (warp < 12) {
+  } else if (warp < kExpWarps + 4) {
     // ============================================================ loading warps
-    const int ct = tid - 256;
+    const int ct = tid - 32 * kExpWarps;
     const bool bf16 = p.a.q.type == CSA2_BF16;
-    for (int64_t id = blockIdx.x; id < total; id += gridDim.x, ++round) {
+    for (int64_t id; (id = item_id(round)) >= 0; ++round) {
       const Item it = item_of(p, lane, id);
       if (it.nt == 0) continue;
       // ---- K: 16-byte chunk cc (of a 64-channel half) of rows r4 + 32 v
@@ -381,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
     const uint64_t kd = smem_desc(smem_u32(smem + L::kK), 16, 1024, 2);
     const uint64_t qd = smem_desc(smem_u32(smem + L::kQ), 16, 1024, 2);
     bool issued = false;
-    for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
+    for (int64_t id; (id = item_id(round)) >= 0; ++round) {
       const Item it = item_of(p, lane, id);
       if (it.nt == 0) continue;
       wait(k_full, k & 1);
@@ -417,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
   if (!ok) set_status(p.a.status, CSA2_DEV_TIMEOUT);
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kExpWarps + 4) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
