@@ -545,14 +545,17 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(DecodeParams p)
   }
 }
 
-// Joins the partial results of the units that several CTAs shared: one CTA of
-// D threads per query row of a unit.  The order is that of the cached rows.
+// Joins the partial results of the units that several CTAs shared: one CTA per
+// query row of a unit, four channels a thread, its threads' groups taking every
+// kCombine-th part.  The order of the sums is fixed by the split.
+constexpr int kCombine = 4;
 template <int D>
-__global__ void __launch_bounds__(D) kv8_combine_kernel(DecodeParams p, int tile_rows) {
+__global__ void __launch_bounds__(D / 4 * kCombine) kv8_combine_kernel(DecodeParams p, int tile_rows) {
+  constexpr int kThreadsC = D / 4 * kCombine;
   griddep_wait();
   griddep_launch_dependents();
   const Kv8& c = p.a.c;
-  const int lane = threadIdx.x & 31;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int units = c.heads * p.tiles;
   const int b = blockIdx.x / units, unit = blockIdx.x % units, row = blockIdx.y;
   const int h = unit / p.tiles, gr = (unit % p.tiles) * tile_rows + row;
@@ -567,41 +570,62 @@ __global__ void __launch_bounds__(D) kv8_combine_kernel(DecodeParams p, int tile
   const int c0 = (int)(((x0 + 1) * ctas - 1) / total), c1 = (int)((x1 * ctas - 1) / total);
   if (c0 == c1) return;
   // the unit began in CTA c0's second slot and went on in the others' first
-  __shared__ float w[kKv8Ctas], red[2][D / 32];
+  __shared__ float w[kKv8Ctas], red[2][kThreadsC / 32];
+  __shared__ float4 sum[kCombine][D / 4];
   const int parts = c1 - c0 + 1;
   auto slot = [&](int i) { return p.a.part + (2 * (int64_t)(c0 + i) + (i == 0)) * slot_floats(D); };
   float top = -INFINITY;
-  for (int i = threadIdx.x; i < parts; i += D) {
+  for (int i = tid; i < parts; i += kThreadsC) {
     w[i] = slot(i)[kKv8SlotRows * D + row];
     top = fmaxf(top, w[i]);
   }
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-  if (lane == 0) red[0][threadIdx.x >> 5] = top;
+  if (lane == 0) red[0][warp] = top;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < D / 32; ++k) top = fmaxf(top, red[0][k]);
+  for (int k = 0; k < kThreadsC / 32; ++k) top = fmaxf(top, red[0][k]);
   float l = 0.0f;
-  for (int i = threadIdx.x; i < parts; i += D) {
+  for (int i = tid; i < parts; i += kThreadsC) {
     const float pl = slot(i)[kKv8SlotRows * (D + 1) + row];
     w[i] = pl == 0.0f ? 0.0f : kv8_exp2(w[i] - top);   // NaN sums stay NaN
     l += pl == 0.0f ? 0.0f : pl * w[i];
   }
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-  if (lane == 0) red[1][threadIdx.x >> 5] = l;
+  if (lane == 0) red[1][warp] = l;
   __syncthreads();
+  const int grp = tid / (D / 4), ch = tid % (D / 4);
+  float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+  for (int i = grp; i < parts; i += kCombine) {
+    const float4 y = reinterpret_cast<const float4*>(slot(i) + row * D)[ch];
+    const float f = w[i];
+    o.x = fmaf(y.x, f, o.x);
+    o.y = fmaf(y.y, f, o.y);
+    o.z = fmaf(y.z, f, o.z);
+    o.w = fmaf(y.w, f, o.w);
+  }
+  sum[grp][ch] = o;
+  __syncthreads();
+  if (grp > 0) return;
   l = 0.0f;
 #pragma unroll
-  for (int k = 0; k < D / 32; ++k) l += red[1][k];
-  float o = 0.0f;
-#pragma unroll 4
-  for (int i = 0; i < parts; ++i) o = fmaf(slot(i)[row * D + threadIdx.x], w[i], o);
-  const float y = l == 0.0f ? 0.0f : o / l;
+  for (int k = 0; k < kThreadsC / 32; ++k) l += red[1][k];
+#pragma unroll
+  for (int k = 1; k < kCombine; ++k) {
+    const float4 y = sum[k][ch];
+    o.x += y.x;
+    o.y += y.y;
+    o.z += y.z;
+    o.w += y.w;
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint16_t* out = static_cast<uint16_t*>(const_cast<void*>(p.a.out.data)) + b * p.a.out.sb +
-                  tok * p.a.out.st + hd * p.a.out.sh + threadIdx.x;
-  *out = (uint16_t)(pack16(y, 0.0f, p.a.out.type) & 0xFFFFu);
-  if (p.a.lse && threadIdx.x == 0)
+                  tok * p.a.out.st + hd * p.a.out.sh + 4 * ch;
+  *reinterpret_cast<uint2*>(out) = make_uint2(pack16(o.x * inv, o.y * inv, p.a.out.type),
+                                              pack16(o.z * inv, o.w * inv, p.a.out.type));
+  if (p.a.lse && tid == 0)
     p.a.lse[((int64_t)b * p.a.T + tok) * p.a.H + hd] =
         l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
 }
@@ -755,15 +779,16 @@ cudaError_t decode_as(const DecodeParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = kv8_launch(kern, dim3(p.ctas), kThreads, DecodeSmem<D>::kBytes, s, p);
   if (e != cudaSuccess) return e;
-  return kv8_launch(kv8_combine_kernel<D>, dim3(p.a.c.batch * p.a.c.heads * p.tiles, 8 * NT), D, 0,
-                    s, p, 8 * NT);
+  return kv8_launch(kv8_combine_kernel<D>, dim3(p.a.c.batch * p.a.c.heads * p.tiles, 8 * NT),
+                    D / 4 * kCombine, 0, s, p, 8 * NT);
 }
 template <int D, int FMT>
 cudaError_t decode_of(DecodeParams p, cudaStream_t s) {
-  const int nt = p.rows <= 8 ? 1 : (p.rows <= 16 ? 2 : 4);
+  const int nt = p.rows <= 8 ? 1 : p.rows <= 16 ? 2 : p.rows <= 24 ? 3 : 4;
   p.tiles = (p.rows + 8 * nt - 1) / (8 * nt);
   return nt == 1   ? decode_as<D, 1, FMT>(p, s)
          : nt == 2 ? decode_as<D, 2, FMT>(p, s)
+         : nt == 3 ? decode_as<D, 3, FMT>(p, s)
                    : decode_as<D, 4, FMT>(p, s);
 }
 template <int D, int FMT>

@@ -76,20 +76,6 @@ __device__ __forceinline__ Item item_of(const MassParams& p, int lane, int64_t i
   return it;
 }
 
-__device__ __forceinline__ uint64_t pack2(float x, float y) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
-}
-
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p) {
   using L = MassSmem<D>;

@@ -26,9 +26,12 @@
 // 2^15, with f16's full precision down to 2^-21.  l is summed in fp32 from the
 // unrounded weights.
 //
-// Warps (416 threads): 0-3 and 4-7 softmax of query tile 0 and 1; 8-11 turn the
-// cache's codes into f16 tiles, from registers loaded one tile ahead (no raw
-// copy in shared memory, whose bandwidth the MMAs need); 12 issues the MMAs.
+// Warps (512 threads): 0-3 and 4-7 softmax of query tile 0 and 1, a row's 128
+// logits in registers at once (one pass over tensor memory; the registers come
+// from the other warps); 8-11 turn the cache's codes into f16 tiles, from
+// registers loaded one tile ahead (no raw copy in shared memory, whose bandwidth
+// the MMAs need); 12 issues the MMAs.  P is handed over in two halves, so that
+// P V starts while the second half's exponentials are taken.
 #include "kv8_mma.cuh"
 
 namespace csa2 {
@@ -36,7 +39,10 @@ namespace {
 
 constexpr int kTileKeys = 128;
 constexpr int kTileRows = 256;
-constexpr int kThreads = 416;
+constexpr int kThreads = 512;
+// Registers a thread at launch, and after the split among the warp groups.
+constexpr int kRegs = 128, kRegsSoftmax = 168, kRegsConvert = 120, kRegsMma = 56;
+static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsMma <= 4 * kRegs, "register split");
 
 template <int D>
 struct PreSmem {
@@ -76,7 +82,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
   uint64_t* s_full = bars + 9;       // [2 query tiles] commit
   uint64_t* p_full = bars + 11;      // [2] 4 warps
   uint64_t* pv_done = bars + 13;     // [2] commit
-  uint64_t* drain = bars + 15;
+  uint64_t* p_half = bars + 15;      // [2] 4 warps: the first 64 columns of P
+  uint64_t* drain = bars + 17;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kFlags);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kFlags + 4);
   volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + L::kFlags + 8);
@@ -91,6 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
       mbar_init(v_empty + i, 1);
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 4);
+      mbar_init(p_half + i, 4);
       mbar_init(pv_done + i, 1);
     }
     mbar_init(drain, 1);
@@ -159,6 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
 
   if (warp < 8) {
     // ============================================================ softmax warps
+    regs_inc<kRegsSoftmax>();
     const int mt = warp >> 2;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + lanes + 128 * mt, tO = tmem + lanes + 256 + D * mt;
@@ -220,7 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
       if (lane == 0) mbar_arrive(q_ready);
     }
 
-    float m = -INFINITY, l = 0.0f;
+    float m = -INFINITY;
+    uint64_t l2[2] = {0, 0};                   // the sum, as four partial ones
     for (int i = 0; mt < mts && i < nt; ++i) {
       wait(s_full + mt, i & 1);
       tc_fence_after();
@@ -230,42 +240,50 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
       const uint32_t groups = masks[i & 3];
       const int key0 = (t0 + i) * kTileKeys;
       const bool masked = groups != 0xFFu || __any_sync(0xffffffffu, lim < key0 + kTileKeys);
-      uint32_t s[32];
-      // whether column j of 32-column part u is hidden
-      auto hide = [&](int u) {
+      uint32_t s[4][32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (key0 + 32 * u + j >= lim || !((groups >> (2 * u + (j >> 4))) & 1u))
-            s[j] = 0xFF800000u;
-      };
-      float top = -INFINITY;
+      for (int u = 0; u < 4; ++u) tmem_ld32(tS + 32 * u, s[u]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int u = 0; u < 4; ++u) reg_fence32(s[u]);
+      if (masked) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (key0 + 32 * u + j >= lim || !((groups >> (2 * u + (j >> 4))) & 1u))
+              s[u][j] = 0xFF800000u;
+      }
+      float tops[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        tmem_ld32(tS + 32 * u, s);
-        tmem_ld_wait();
-        reg_fence32(s);
-        if (masked) hide(u);
+        tops[u] = __uint_as_float(s[u][0]);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(s[j]));
+        for (int j = 1; j < 31; j += 2)
+          tops[u] = fmaxf(tops[u], fmaxf(__uint_as_float(s[u][j]), __uint_as_float(s[u][j + 1])));
+        tops[u] = fmaxf(tops[u], __uint_as_float(s[u][31]));
       }
-      top *= mul;
+      const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * mul;
       if (__any_sync(0xffffffffu, top > m + 8.0f)) {
         const float up = fmaxf(m, top);
         const float alpha = m == -INFINITY ? 0.0f : kv8_exp2(m - up);
-        l *= alpha;
+        const uint64_t a2 = pack2(alpha, alpha);
+        l2[0] = mul2(l2[0], a2);
+        l2[1] = mul2(l2[1], a2);
         m = up;
         if (i > 0) {
           wait(pv_done + mt, (i - 1) & 1);
           tc_fence_after();
           if (!ok) break;
 #pragma unroll 1
-          for (int u = 0; u < D / 32; ++u) {
-            tmem_ld32(tO + 32 * u, s);
+          for (int u = 0; u < D / 16; ++u) {
+            uint32_t o[16];
+            tmem_ld16(tO + 16 * u, o);
             tmem_ld_wait();
-            reg_fence32(s);
+            reg_fence(o);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) * alpha);
-            tmem_st32(tO + 32 * u, s);
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+            tmem_st16(tO + 16 * u, o);
           }
           tmem_st_wait();
         }
@@ -275,37 +293,50 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
       // it would carry P out of range (ulp(2^16) = 2^-7), the logits are rounded
       // like m, which makes the largest difference 0 again.
       const bool plain = !masked && !__any_sync(0xffffffffu, fabsf(m) > 65536.0f);
-      const float mm = m == -INFINITY ? 0.0f : m, use = mm - 7.0f;
+      const float mm = m == -INFINITY ? 0.0f : m;
+      if (plain) {
+        const uint64_t f2 = pack2(mul, mul), u2 = pack2(7.0f - mm, 7.0f - mm);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            float x, y;
+            unpack2(fma2(pack2(__uint_as_float(s[u][j]), __uint_as_float(s[u][j + 1])), f2, u2), x, y);
+            s[u][j] = __float_as_uint(x);
+            s[u][j + 1] = __float_as_uint(y);
+          }
+      } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            s[u][j] = __float_as_uint((__fmul_rn(__uint_as_float(s[u][j]), mul) - mm) + 7.0f);
+      }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        tmem_ld32(tS + 32 * u, s);
-        tmem_ld_wait();
-        reg_fence32(s);
-        if (plain) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            s[j] = __float_as_uint(fmaf(__uint_as_float(s[j]), mul, -use));
-        } else {
-          hide(u);
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            s[j] = __float_as_uint((__fmul_rn(__uint_as_float(s[j]), mul) - mm) + 7.0f);
-        }
         uint32_t w[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const float x = kv8_exp2(__uint_as_float(s[2 * j]));
-          const float y = kv8_exp2(__uint_as_float(s[2 * j + 1]));
-          l += x;
-          l += y;
+          const float x = kv8_exp2(__uint_as_float(s[u][2 * j]));
+          const float y = kv8_exp2(__uint_as_float(s[u][2 * j + 1]));
+          l2[j & 1] = add2(l2[j & 1], pack2(x, y));
           w[j] = pack16(x, y, CSA2_F16);
         }
         tmem_st16(tS + 16 * u, w);
+        if (u & 1) {
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive((u == 1 ? p_half : p_full) + mt);
+        }
       }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full + mt);
+    }
+    float l = 0.0f;
+    {
+      float a, b2, c2, d;
+      unpack2(l2[0], a, b2);
+      unpack2(l2[1], c2, d);
+      l = (a + b2) + (c2 + d);
     }
     // ---- the row's result
     if (nt > 0 && mt < mts) wait(pv_done + mt, (nt - 1) & 1);
@@ -365,6 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
     }
   } else if (warp < 12) {
     // ========================================================== converter warps
+    regs_dec<kRegsConvert>();
     // Thread: 16-byte chunk cc (of a 64-channel half) of rows r4 + 32 v.  Eight
     // neighbouring lanes then store to two rows' chunks of all eight positions.
     const int ct = tid - 256, cc = ct & 3, r4 = ct >> 2;
@@ -464,27 +496,34 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
       }
       good = good_next;
     }
-  } else if (lane == 0 && nt > 0) {
+  } else {
     // ================================================================ MMA thread
+    regs_dec<kRegsMma>();
+    if (warp == 12 && lane == 0 && nt > 0) {
     constexpr uint32_t idesc_qk = instr_desc(0, 0, false, false, 128, 128);
     constexpr uint32_t idesc_pv = instr_desc(0, 0, false, true, 128, D);
-    const uint64_t qd = smem_desc(smem_u32(smem + L::kQ), 16, 1024, 2);
-    const uint64_t kd = smem_desc(smem_u32(smem + L::kK), 16, 1024, 2);
-    const uint64_t vd = smem_desc(smem_u32(smem + L::kV), L::kSlab, 1024, 2);
-    constexpr uint64_t kTileDesc = L::kSlabs * L::kSlab / 16;
+    const uint64_t kmajor = smem_desc(smem_u32(smem), 16, 1024, 2);
+    const uint64_t vmajor = smem_desc(smem_u32(smem), L::kSlab, 1024, 2);
+    const uint32_t k_hi = (uint32_t)(kmajor >> 32), v_hi = (uint32_t)(vmajor >> 32);
+    const uint32_t qd = (uint32_t)kmajor + L::kQ / 16, kd = (uint32_t)kmajor + L::kK / 16;
+    const uint32_t vd = (uint32_t)vmajor + L::kV / 16;
+    constexpr uint32_t kTileDesc = L::kSlabs * L::kSlab / 16;
     auto qk = [&](int mt, int st) {
+      const uint32_t a = qd + mt * kTileDesc, b2 = kd + st * kTileDesc, d = tmem + 128 * mt;
 #pragma unroll
       for (int s = 0; s < L::kSlabs; ++s)
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_f16(tmem + 128 * mt, qd + mt * kTileDesc + (s * L::kSlab + kk * 32) / 16,
-                  kd + st * kTileDesc + (s * L::kSlab + kk * 32) / 16, idesc_qk, (s | kk) ? 1u : 0u);
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint32_t o = (s * L::kSlab + kk * 32) / 16;
+          mma_ss(d, a + o, k_hi, b2 + o, k_hi, idesc_qk, (s | kk) ? 1u : 0u);
+        }
     };
     bool issued = false;
     ok = mbar_wait(q_ready, 0, abort_flag) && mbar_wait(k_full, 0, abort_flag);
     if (ok) {
       tc_fence_after();
       issued = true;
+#pragma unroll 1
       for (int mt = 0; mt < mts; ++mt) {
         qk(mt, 0);
         mma_commit(s_full + mt);
@@ -493,15 +532,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
     }
     for (int i = 0; ok && i < nt; ++i) {
       const int st = i & 1, sn = st ^ 1;
+#pragma unroll 1
       for (int mt = 0; ok && mt < mts; ++mt) {
-        ok = mbar_wait(p_full + mt, i & 1, abort_flag) &&
-             mbar_wait(v_full + st, (i >> 1) & 1, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
+        ok = mbar_wait(v_full + st, (i >> 1) & 1, abort_flag);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_f16_ts(tmem + 256 + D * mt, tmem + 128 * mt + 8 * kk,
-                     vd + st * kTileDesc + kk * 2048 / 16, idesc_pv, (i | kk) ? 1u : 0u);
+        for (int half = 0; half < 2; ++half) {
+          if (ok) ok = mbar_wait((half ? p_full : p_half) + mt, i & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+            mma_ts(tmem + 256 + D * mt, tmem + 128 * mt + 8 * kk,
+                   vd + st * kTileDesc + kk * 2048 / 16, v_hi, idesc_pv, (i | kk) ? 1u : 0u);
+        }
+        if (!ok) break;
         mma_commit(pv_done + mt);
         if (mt == mts - 1) mma_commit(v_empty + st);
         if (i + 1 < nt) {
@@ -517,6 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
     if (issued) {   // let every issued MMA land before tensor memory is freed
       mma_commit(drain);
       mbar_wait_drain(drain, 0);
+    }
     }
   }
   __syncwarp();

@@ -47,23 +47,130 @@ __device__ __forceinline__ uint32_t group_max(uint32_t x, uint32_t* red, int tid
   return x;
 }
 
-// The new rows of one block, head and side (0 K, 1 V), by NT threads (a warp
-// or a CTA), 16 bytes a thread and access.  The rows are held in registers
-// between the block's maximum and their codes, so they are read once.  The
-// maximum is taken over the bits of the magnitudes (two 16-bit values at a
-// time), which also shows whether there is an infinity or a NaN.
+// The new rows of one block and head, K and V, by NT threads (a warp or a CTA),
+// 16 bytes a thread and access.  The rows are held in registers between the
+// block's maximum and their codes, so they are read once; where the registers
+// allow it both sides are read before either is worked on.  The maximum is taken
+// over the bits of the magnitudes (two 16-bit values at a time), which also
+// shows whether there is an infinity or a NaN.
 // EL: elements per 16 bytes (4 fp32, 8 of 16 bits).
-template <int D, int EL, int FMT, int NT, int PASSES>
+template <int D, int EL, int NT, int PASSES>
+struct NewRows {
+  static constexpr int kLanes = D / EL;    // threads per row
+  static constexpr int kRows = NT / kLanes;
+  static constexpr int ES = 16 / EL;
+  uint4 raw[PASSES];
+  float s0;                                // the block's scale so far
+
+  __device__ __forceinline__ void read(const Kv8Rows& in, const Span& sp, int b, int h, int lo,
+                                       int hi, bool had, const float* scale, int tid) {
+    const int sub = tid / kLanes, ch = (tid % kLanes) * EL;
+    const char* src = static_cast<const char*>(in.data) +
+                      (b * in.sb + (int64_t)(lo - sp.start + sub) * in.st + h * in.sh + ch) * ES;
+    const int64_t step = (int64_t)kRows * in.st * ES;
+    s0 = had ? *scale : 0.0f;
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (lo + i * kRows + sub < hi) raw[i] = *reinterpret_cast<const uint4*>(src + i * step);
+    }
+  }
+
+  // row0: index of the block's first row; lo, hi: the new rows' positions
+  template <int FMT>
+  __device__ __forceinline__ void write(const AppendParams& p, int type, uint8_t* codes,
+                                        float* scale, int64_t row0, int b0, int lo, int hi,
+                                        uint32_t* red, int tid) {
+    const int sub = tid / kLanes, ch = (tid % kLanes) * EL;
+    const uint32_t inf = EL == 4 ? 0x7F800000u : (type == CSA2_BF16 ? 0x7F80u : 0x7C00u);
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        bits = EL == 4 ? max(bits, w[j] & 0x7FFFFFFFu) : __vmaxu2(bits, w[j] & 0x7FFF7FFFu);
+    }
+    if (EL == 8) bits = max(bits & 0xFFFFu, bits >> 16);
+    bits = group_max<NT>(bits, red, tid);
+    const bool odd = bits >= inf;          // uniform over the group
+    if (odd) {                             // the maximum of the finite values then
+      if (tid == 0) set_status(p.status, CSA2_DEV_NONFINITE);
+      bits = 0;
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < (EL == 4 ? 1 : 2); ++e) {
+            const uint32_t m = EL == 4 ? w[j] & 0x7FFFFFFFu : (w[j] >> (16 * e)) & 0x7FFFu;
+            if (m < inf) bits = max(bits, m);
+          }
+      }
+      bits = group_max<NT>(bits, red, tid);
+    }
+    __syncwarp();                          // every thread of the group has read s0
+    const float amax = EL == 4 ? __uint_as_float(bits)
+                       : type == CSA2_BF16
+                           ? __uint_as_float(bits << 16)
+                           : __half2float(__ushort_as_half((unsigned short)bits));
+    const float s1 = fmaxf(s0, kv8_scale_of<FMT>(amax));
+    const float inv = kv8_inverse(s1);
+    const float big = s1 > 0.0f ? (FMT == CSA2_KV8_E4M3 ? 448.0f : 127.0f) : 0.0f;
+    uint8_t* dst = codes + (row0 + (lo - b0) + sub) * D + ch;
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      if (lo + i * kRows + sub >= hi) continue;
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      float v[EL];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (EL == 4) {
+          v[j] = __uint_as_float(w[j]);
+        } else if (type == CSA2_BF16) {
+          bf16x2_to_f32(w[j], v[2 * j % EL], v[(2 * j + 1) % EL]);
+        } else {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+          v[2 * j % EL] = f.x;
+          v[(2 * j + 1) % EL] = f.y;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < EL; ++j) {
+        const float x = v[j];
+        v[j] = x * inv;
+        if (odd && !(fabsf(x) <= 3.402823466e38f)) v[j] = x != x ? 0.0f : copysignf(big, x);
+      }
+      uint8_t* to = dst + (int64_t)i * kRows * D;
+      if (EL == 4) {
+        *reinterpret_cast<uint32_t*>(to) = kv8_encode4<FMT>(v[0], v[1], v[2], v[3]);
+      } else {
+        *reinterpret_cast<uint2*>(to) =
+            make_uint2(kv8_encode4<FMT>(v[0], v[1], v[2], v[3]),
+                       kv8_encode4<FMT>(v[4 % EL], v[5 % EL], v[6 % EL], v[7 % EL]));
+      }
+    }
+    if (s1 > s0 && s0 > 0.0f) {            // the block's earlier rows under the larger scale
+      const float ratio = s0 * inv;
+      uint8_t* old = codes + row0 * D;
+      for (int i = tid; i < (lo - b0) * D / 8; i += NT) {
+        uint2 w = *reinterpret_cast<uint2*>(old + 8 * i);
+        w.x = kv8_recode<FMT>(w.x, ratio);
+        w.y = kv8_recode<FMT>(w.y, ratio);
+        *reinterpret_cast<uint2*>(old + 8 * i) = w;
+      }
+    }
+    if (tid == 0 && (s1 > s0 || lo == b0)) *scale = s1;
+  }
+};
+
+template <int D, int EL, int FMT, int NT, int PASSES, int SIDES>
 __device__ __forceinline__ void append_block(const AppendParams& p, const Span& sp, int b, int h,
                                              int side, int blk, uint32_t* red, int tid) {
-  constexpr int kLanes = D / EL;           // threads per row
-  constexpr int kRows = NT / kLanes;
-  constexpr int ES = 16 / EL;
-  static_assert(kRows >= 1, "a row per pass");
   const Kv8& c = p.c;
-  const int block = 1 << c.block_shift;
   const int b0 = blk << c.block_shift;
-  const int lo = max(sp.start, b0), hi = min(sp.start + sp.t, b0 + block);
+  const int lo = max(sp.start, b0), hi = min(sp.start + sp.t, b0 + (1 << c.block_shift));
   if (lo >= hi) return;                    // uniform over the group
   int in_page;
   const int page = kv8_page(c, b, b0, in_page);
@@ -71,105 +178,22 @@ __device__ __forceinline__ void append_block(const AppendParams& p, const Span& 
     if (tid == 0) set_status(p.status, CSA2_DEV_BAD_PAGE);
     return;
   }
-  const Kv8Rows& in = p.in[side];
-  const int sub = tid / kLanes, ch = (tid % kLanes) * EL;
-  const char* src = static_cast<const char*>(in.data) +
-                    (b * in.sb + (int64_t)(lo - sp.start + sub) * in.st + h * in.sh + ch) * ES;
-  const int64_t step = (int64_t)kRows * in.st * ES;
+  const int64_t row0 = kv8_row(c, page, h, in_page), at = kv8_block(c, page, h, in_page);
   const bool had = sp.start > b0;
-  float* scale = c.scales[side] + kv8_block(c, page, h, in_page);
-  const float s0 = had ? *scale : 0.0f;
-
-  uint4 raw[PASSES];
-#pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    raw[i] = make_uint4(0, 0, 0, 0);
-    if (lo + i * kRows + sub < hi) raw[i] = *reinterpret_cast<const uint4*>(src + i * step);
+  if (SIDES == 2) {
+    NewRows<D, EL, NT, PASSES> k, v;
+    k.read(p.in[0], sp, b, h, lo, hi, had, c.scales[0] + at, tid);
+    v.read(p.in[1], sp, b, h, lo, hi, had, c.scales[1] + at, tid);
+    k.template write<FMT>(p, p.in[0].type, c.codes[0], c.scales[0] + at, row0, b0, lo, hi, red, tid);
+    v.template write<FMT>(p, p.in[0].type, c.codes[1], c.scales[1] + at, row0, b0, lo, hi, red, tid);
+  } else {
+    NewRows<D, EL, NT, PASSES> x;
+    x.read(p.in[side], sp, b, h, lo, hi, had, c.scales[side] + at, tid);
+    x.template write<FMT>(p, p.in[0].type, c.codes[side], c.scales[side] + at, row0, b0, lo, hi, red,
+                          tid);
   }
-  const uint32_t inf = EL == 4 ? 0x7F800000u : (in.type == CSA2_BF16 ? 0x7F80u : 0x7C00u);
-  uint32_t bits = 0;
-#pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      bits = EL == 4 ? max(bits, w[j] & 0x7FFFFFFFu) : __vmaxu2(bits, w[j] & 0x7FFF7FFFu);
-  }
-  if (EL == 8) bits = max(bits & 0xFFFFu, bits >> 16);
-  bits = group_max<NT>(bits, red, tid);
-  const bool odd = bits >= inf;            // uniform over the group
-  if (odd) {                               // the maximum of the finite values then
-    if (tid == 0) set_status(p.status, CSA2_DEV_NONFINITE);
-    bits = 0;
-#pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int e = 0; e < (EL == 4 ? 1 : 2); ++e) {
-          const uint32_t m = EL == 4 ? w[j] & 0x7FFFFFFFu : (w[j] >> (16 * e)) & 0x7FFFu;
-          if (m < inf) bits = max(bits, m);
-        }
-    }
-    bits = group_max<NT>(bits, red, tid);
-  }
-  __syncwarp();                            // every thread of the group has read s0
-  const float amax = EL == 4 ? __uint_as_float(bits)
-                     : in.type == CSA2_BF16 ? __uint_as_float(bits << 16)
-                                            : __half2float(__ushort_as_half((unsigned short)bits));
-  const float s1 = fmaxf(s0, kv8_scale_of<FMT>(amax));
-  const float inv = kv8_inverse(s1);
-  const int64_t row0 = kv8_row(c, page, h, in_page);
-  uint8_t* dst = c.codes[side] + (row0 + (lo - b0) + sub) * D + ch;
-  const float big = s1 > 0.0f ? (FMT == CSA2_KV8_E4M3 ? 448.0f : 127.0f) : 0.0f;
-#pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    if (lo + i * kRows + sub >= hi) continue;
-    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-    float v[EL];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (EL == 4) {
-        v[j] = __uint_as_float(w[j]);
-      } else if (in.type == CSA2_BF16) {
-        bf16x2_to_f32(w[j], v[2 * j % EL], v[(2 * j + 1) % EL]);
-      } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-        v[2 * j % EL] = f.x;
-        v[(2 * j + 1) % EL] = f.y;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < EL; ++j) {
-      const float x = v[j];
-      v[j] = x * inv;
-      if (odd && !(fabsf(x) <= 3.402823466e38f)) v[j] = x != x ? 0.0f : copysignf(big, x);
-    }
-    uint8_t* to = dst + (int64_t)i * kRows * D;
-    if (EL == 4) {
-      *reinterpret_cast<uint32_t*>(to) = kv8_encode4<FMT>(v[0], v[1], v[2], v[3]);
-    } else {
-      *reinterpret_cast<uint2*>(to) =
-          make_uint2(kv8_encode4<FMT>(v[0], v[1], v[2], v[3]),
-                     kv8_encode4<FMT>(v[4 % EL], v[5 % EL], v[6 % EL], v[7 % EL]));
-    }
-  }
-  if (s1 > s0 && s0 > 0.0f) {              // the block's earlier rows under the larger scale
-    const float ratio = s0 * inv;
-    uint8_t* old = c.codes[side] + row0 * D;
-    for (int i = tid; i < (lo - b0) * D / 8; i += NT) {
-      uint2 w = *reinterpret_cast<uint2*>(old + 8 * i);
-      w.x = kv8_recode<FMT>(w.x, ratio);
-      w.y = kv8_recode<FMT>(w.y, ratio);
-      *reinterpret_cast<uint2*>(old + 8 * i) = w;
-    }
-  }
-  if (tid == 0 && (s1 > s0 || !had)) *scale = s1;
-  if (side == 0 && c.mass) {
-    float* m = c.mass + row0 + (lo - b0);
-    for (int r = tid; r < hi - lo; r += NT) m[r] = 0.0f;
-  }
+  if (side == 0 && c.mass)
+    for (int r = tid; r < hi - lo; r += NT) c.mass[row0 + (lo - b0) + r] = 0.0f;
 }
 
 // Appends of a few rows: one CTA per sequence, a warp per (head, side), so that
@@ -190,13 +214,14 @@ __global__ void __launch_bounds__(512) kv8_append_few_kernel(AppendParams p) {
   const int first = sp.start >> p.c.block_shift, last = (sp.start + sp.t - 1) >> p.c.block_shift;
   for (int i = threadIdx.x >> 5; i < 2 * p.c.heads; i += warps)
     for (int blk = first; blk <= last; ++blk)
-      append_block<D, EL, FMT, 32, kFewRows * D / EL / 32>(p, sp, b, i >> 1, i & 1, blk, nullptr,
-                                                           lane);
+      append_block<D, EL, FMT, 32, kFewRows * D / EL / 32, 1>(p, sp, b, i >> 1, i & 1, blk,
+                                                              nullptr, lane);
 }
 
-// Longer appends: one CTA per (block, head, side, sequence).  PASSES: 16-byte
-// accesses of a thread that hold a whole block.
+// Longer appends: one CTA per (block, head, sequence), or side of it.  PASSES:
+// 16-byte accesses of a thread that hold a side of a block.
 constexpr int kAppendThreads = 256;
+constexpr int append_sides(int passes) { return passes <= 8 ? 2 : 1; }
 template <int D, int EL, int FMT, int PASSES>
 __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendParams p) {
   __shared__ uint32_t red[kAppendThreads / 32];
@@ -209,9 +234,10 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendParams
     if (p.own_len) p.c.seq_len[b] = sp.start + sp.t;
   }
   if (sp.t == 0) return;
-  append_block<D, EL, FMT, kAppendThreads, PASSES>(p, sp, b, blockIdx.y >> 1, blockIdx.y & 1,
-                                                   (sp.start >> p.c.block_shift) + blockIdx.x, red,
-                                                   threadIdx.x);
+  constexpr int kSides = append_sides(PASSES);
+  append_block<D, EL, FMT, kAppendThreads, PASSES, kSides>(
+      p, sp, b, kSides == 2 ? blockIdx.y : blockIdx.y >> 1, kSides == 2 ? 0 : blockIdx.y & 1,
+      (sp.start >> p.c.block_shift) + blockIdx.x, red, threadIdx.x);
 }
 __global__ void kv8_advance_kernel(AppendParams p) {
   griddep_wait();
@@ -230,17 +256,17 @@ cudaError_t append_as(const AppendParams& p0, cudaStream_t s) {
     return kv8_launch(kv8_append_few_kernel<D, EL, FMT>, dim3(p.c.batch), 32 * warps, 0, s, p);
   }
   const int block = 1 << p.c.block_shift;
-  const dim3 grid((p.T + block - 2) / block + 1, 2 * p.c.heads, p.c.batch);
   // with `start` given nothing in the launch reads seq_len, so it may write it
   p.own_len = p.start != nullptr;
+  auto run = [&](auto kern, int passes) {
+    const dim3 grid((p.T + block - 2) / block + 1, p.c.heads * (append_sides(passes) == 2 ? 1 : 2),
+                    p.c.batch);
+    return kv8_launch(kern, grid, kAppendThreads, 0, s, p);
+  };
   constexpr int kMost = 128 * D / EL / kAppendThreads;   // passes of 128 rows
-  cudaError_t e;
-  if (block == 128)
-    e = kv8_launch(kv8_append_kernel<D, EL, FMT, kMost>, grid, kAppendThreads, 0, s, p);
-  else if (block == 64)
-    e = kv8_launch(kv8_append_kernel<D, EL, FMT, kMost / 2>, grid, kAppendThreads, 0, s, p);
-  else
-    e = kv8_launch(kv8_append_kernel<D, EL, FMT, kMost / 4>, grid, kAppendThreads, 0, s, p);
+  const cudaError_t e = block == 128 ? run(kv8_append_kernel<D, EL, FMT, kMost>, kMost)
+                        : block == 64 ? run(kv8_append_kernel<D, EL, FMT, kMost / 2>, kMost / 2)
+                                      : run(kv8_append_kernel<D, EL, FMT, kMost / 4>, kMost / 4);
   if (e != cudaSuccess || p.own_len) return e;
   return kv8_launch(kv8_advance_kernel, dim3((p.c.batch + 127) / 128), 128, 0, s, p);
 }
@@ -340,7 +366,11 @@ __global__ void __launch_bounds__(kSelThreads) kv8_evict_select_kernel(EvictPara
     __syncthreads();
     const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
     each([&](int, bool in, uint32_t k) {
-      if (in && (k & mask) == prefix) atomicAdd(&mine[(k >> shift) & 255u], 1u);
+      // (weights share their leading bits: the lanes with one digit add once)
+      const bool hit = in && (k & mask) == prefix;
+      const uint32_t d = hit ? (k >> shift) & 255u : 256u;
+      const uint32_t same = __match_any_sync(0xffffffffu, d);
+      if (hit && lane == __ffs(same) - 1) atomicAdd(&mine[d], (uint32_t)__popc(same));
     });
     cluster_sync();
     if (tid < 256) {
@@ -576,8 +606,12 @@ cudaError_t launch_kv8_evict(const Kv8& src, const Kv8& dst, bool in_place, int 
                              int sink, int recent, int32_t* kept, int32_t* old_len,
                              uint32_t* status, int num_sms, cudaStream_t s) {
   EvictParams p{src, dst, keep, sink, recent, kept, old_len, status, in_place ? 1 : 0};
-  // one CTA holds 16 K rows in registers; longer caches are spread over eight
-  const int cluster = src.max_len <= 8192 ? 1 : 8;
+  // CTAs per (head, sequence): as many as the SMs hold at once, up to eight and
+  // one for each 2048 rows of the capacity
+  int cluster = 8;
+  while (cluster > 1 && ((int64_t)cluster * src.heads * src.batch > num_sms ||
+                         src.max_len < 2048 * cluster))
+    cluster /= 2;
   cudaError_t e = launch_cluster(kv8_evict_select_kernel, dim3(cluster, src.heads, src.batch),
                                  kSelThreads, cluster, s, p);
   if (e != cudaSuccess) return e;
