@@ -34,12 +34,11 @@ struct Kv8 {
   int32_t paged, page_shift;       // page_shift: log2(page_rows) or -1
 };
 
-// Page (physical) and row in the page of position t of sequence b; page -1
-// when the table's entry is out of range.
-__device__ __forceinline__ int kv8_page(const Kv8& c, int b, int t, int& in_page) {
+// Column of the page table and row in the page of position t (contiguous: 0, t).
+__device__ __forceinline__ int kv8_in_page(const Kv8& c, int t, int& in_page) {
   if (!c.paged) {
     in_page = t;
-    return b;
+    return 0;
   }
   const uint32_t ut = (uint32_t)t;
   uint32_t pg;
@@ -50,8 +49,23 @@ __device__ __forceinline__ int kv8_page(const Kv8& c, int b, int t, int& in_page
     pg = ut / (uint32_t)c.page_rows;
     in_page = (int)(ut - pg * (uint32_t)c.page_rows);
   }
-  const int32_t phys = c.page_table[(int64_t)b * c.max_pages + pg];
-  return phys < 0 || phys >= c.num_pages ? -1 : phys;
+  return (int)pg;
+}
+// The page table's entry for position t, unchecked (contiguous: the sequence).
+__device__ __forceinline__ int kv8_page_id(const Kv8& c, int b, int t) {
+  int in_page;
+  const int pg = kv8_in_page(c, t, in_page);
+  return c.paged ? c.page_table[(int64_t)b * c.max_pages + pg] : b;
+}
+// The page, or -1 when its id is out of range.
+__device__ __forceinline__ int kv8_check(const Kv8& c, int id) {
+  return id < 0 || id >= c.num_pages ? -1 : id;
+}
+// Page (physical) and row in the page of position t of sequence b; page -1
+// when the table's entry is out of range.
+__device__ __forceinline__ int kv8_page(const Kv8& c, int b, int t, int& in_page) {
+  const int pg = kv8_in_page(c, t, in_page);
+  return kv8_check(c, c.paged ? c.page_table[(int64_t)b * c.max_pages + pg] : b);
 }
 // Row index over [pages, kv_heads, page rows]; times D for codes, as is for mass.
 __device__ __forceinline__ int64_t kv8_row(const Kv8& c, int page, int h, int in_page) {

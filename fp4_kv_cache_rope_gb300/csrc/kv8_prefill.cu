@@ -26,23 +26,27 @@
 // 2^15, with f16's full precision down to 2^-21.  l is summed in fp32 from the
 // unrounded weights.
 //
-// Warps (512 threads): 0-3 and 4-7 softmax of query tile 0 and 1, a row's 128
-// logits in registers at once (one pass over tensor memory; the registers come
-// from the other warps); 8-11 turn the cache's codes into f16 tiles, from
-// registers loaded one tile ahead (no raw copy in shared memory, whose bandwidth
-// the MMAs need); 12 issues the MMAs.  P is handed over in two halves, so that
-// P V starts while the second half's exponentials are taken.
+// Warps (640 threads): 0-3 and 4-7 softmax of query tile 0 and 1; 8-11 turn K's
+// codes into f16 tiles and 12-15 V's, from registers loaded one tile ahead (no
+// raw copy in shared memory, whose bandwidth the MMAs need); 16 issues the MMAs.
+//
+// A softmax thread reads its row's 128 logits from tensor memory twice, 16 at a
+// time with the next ones on their way: once for the maximum, once for the
+// exponentials, whose P goes back in two halves, each handed over at once.  That
+// keeps every role within its registers: a spilled register is read back from
+// L2, because L1 is left little beside the tiles.
 #include "kv8_mma.cuh"
 
 namespace csa2 {
 namespace {
 
 constexpr int kTileKeys = 128;
+constexpr int kNone = -0x7FFFFFFF - 1;   // no page id
 constexpr int kTileRows = 256;
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 // Registers a thread at launch, and after the split among the warp groups.
-constexpr int kRegs = 128, kRegsSoftmax = 168, kRegsConvert = 120, kRegsMma = 56;
-static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsMma <= 4 * kRegs, "register split");
+constexpr int kRegs = 96, kRegsSoftmax = 104, kRegsConvert = 96, kRegsMma = 80;
+static_assert(2 * kRegsSoftmax + 2 * kRegsConvert + kRegsMma <= 5 * kRegs, "register split");
 
 template <int D>
 struct PreSmem {
@@ -75,15 +79,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
   }
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
   uint64_t* q_ready = bars;          // 8 warps
-  uint64_t* k_full = bars + 1;       // [2] 4 warps
-  uint64_t* k_empty = bars + 3;      // [2] commit
-  uint64_t* v_full = bars + 5;       // [2] 4 warps
-  uint64_t* v_empty = bars + 7;      // [2] commit
-  uint64_t* s_full = bars + 9;       // [2 query tiles] commit
-  uint64_t* p_full = bars + 11;      // [2] 4 warps
-  uint64_t* pv_done = bars + 13;     // [2] commit
-  uint64_t* p_half = bars + 15;      // [2] 4 warps: the first 64 columns of P
-  uint64_t* drain = bars + 17;
+  uint64_t* k_full = bars + 1;       // [2 stages] 4 warps
+  uint64_t* v_full = bars + 3;       // [2 stages] 4 warps
+  uint64_t* s_full = bars + 5;       // [2 query tiles][2: tile parity] commit
+  uint64_t* p_full = bars + 9;       // [2 query tiles] 4 warps
+  uint64_t* p_half = bars + 11;      // [2] 4 warps: the first 64 columns of P
+  uint64_t* o_done = bars + 13;      // commit after the last MMA
+  uint64_t* drain = bars + 14;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kFlags);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kFlags + 4);
   volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + L::kFlags + 8);
@@ -93,19 +95,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
     mbar_init(q_ready, 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full + i, 4);
-      mbar_init(k_empty + i, 1);
       mbar_init(v_full + i, 4);
-      mbar_init(v_empty + i, 1);
       mbar_init(s_full + i, 1);
+      mbar_init(s_full + 2 + i, 1);
       mbar_init(p_full + i, 4);
       mbar_init(p_half + i, 4);
-      mbar_init(pv_done + i, 1);
     }
+    mbar_init(o_done, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 12) tmem_alloc(tmem_slot, 512);
+  if (warp == 16) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   griddep_wait();
   griddep_launch_dependents();
@@ -176,54 +177,50 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
     const bool real = r < rows;
     const int lim = real ? min(n, n - ql + tok + 1) : 0;
     float mul = 0.0f;
+    constexpr int kPer = D / 8;                            // 16-byte chunks of a row
+    constexpr int kAt = 32 / kPer;                         // rows of a warp's access
+    const int chunk = lane % kPer;
     if (nt > 0) {
-      // the row as f16 in the swizzled tile
-      const uint4* src = reinterpret_cast<const uint4*>(
-          static_cast<const char*>(p.a.q.data) +
-          2 * (b * p.a.q.sb + tok * p.a.q.st + hd * p.a.q.sh));
-      float amax = 0.0f;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const uint4 w = real ? src[i] : make_uint4(0, 0, 0, 0);
+      // the warp's 32 rows as f16 in the swizzled tile, kAt rows an access
+      const int64_t off = b * p.a.q.sb + tok * p.a.q.st + hd * p.a.q.sh;
+      uint8_t* tile = smem + L::kQ + mt * L::kSlabs * L::kSlab + (chunk >> 3) * L::kSlab;
+      float up = 1.0f;
+#pragma unroll 8
+      for (int i = 0; i < 32 / kAt; ++i) {
+        const int row = i * kAt + lane / kPer;             // of the warp's 32
+        const int64_t from = __shfl_sync(0xffffffffu, off, row);
+        const bool in = __shfl_sync(0xffffffffu, (int)real, row) != 0;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (in)
+          w = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.a.q.data) + 2 * from +
+                                              16 * chunk);
         const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        float x[8], amax = 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float x, y;
           if (p.a.q.type == CSA2_BF16) {
-            bf16x2_to_f32(ww[j], x, y);
+            bf16x2_to_f32(ww[j], x[2 * j], x[2 * j + 1]);
           } else {
             const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&ww[j]));
-            x = f.x;
-            y = f.y;
+            x[2 * j] = f.x;
+            x[2 * j + 1] = f.y;
           }
-          amax = fmaxf(amax, fmaxf(fabsf(x), fabsf(y)));
+          amax = fmaxf(amax, fmaxf(fabsf(x[2 * j]), fabsf(x[2 * j + 1])));
         }
+#pragma unroll
+        for (int o = kPer / 2; o > 0; o >>= 1)
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const int e = (int)(__float_as_uint(amax) >> 23);
+        const int shift = e == 0 || e == 255 ? 0 : 134 - e;
+        const float f = __uint_as_float((uint32_t)(127 + (shift > 127 ? 127 : shift)) << 23);
+        const float mine = __shfl_sync(0xffffffffu, f, lane % kAt * kPer);
+        if (lane / kAt == i) up = mine;
+        st_swizzled(tile, 32 * (warp & 3) + row, chunk & 7,
+                    make_uint4(pack16(x[0] * f, x[1] * f, CSA2_F16), pack16(x[2] * f, x[3] * f, CSA2_F16),
+                               pack16(x[4] * f, x[5] * f, CSA2_F16), pack16(x[6] * f, x[7] * f, CSA2_F16)));
       }
-      const int e = (int)(__float_as_uint(amax) >> 23);
-      const int shift = e == 0 || e == 255 ? 0 : 134 - e;
-      const float up = __uint_as_float((uint32_t)(127 + (shift > 127 ? 127 : shift)) << 23);
       // (kept above zero: hidden columns are -inf times it)
       mul = fmaxf(p.a.scale_log2 / up * (kref > 0.0f ? kref : 1.0f), 1.2e-38f);
-      uint8_t* tile = smem + L::kQ + mt * L::kSlabs * L::kSlab;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const uint4 w = real ? src[i] : make_uint4(0, 0, 0, 0);
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-        uint32_t o[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float x, y;
-          if (p.a.q.type == CSA2_BF16) {
-            bf16x2_to_f32(ww[j], x, y);
-          } else {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&ww[j]));
-            x = f.x;
-            y = f.y;
-          }
-          o[j] = pack16(x * up, y * up, CSA2_F16);
-        }
-        st_swizzled(tile + (i >> 3) * L::kSlab, r & 127, i & 7, make_uint4(o[0], o[1], o[2], o[3]));
-      }
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_ready);
@@ -232,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
     float m = -INFINITY;
     uint64_t l2[2] = {0, 0};                   // the sum, as four partial ones
     for (int i = 0; mt < mts && i < nt; ++i) {
-      wait(s_full + mt, i & 1);
+      wait(s_full + 2 * mt + (i & 1), (i >> 1) & 1);
       tc_fence_after();
       if (!ok) break;
       // written before the tile's K was handed over, and not written again
@@ -240,41 +237,59 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
       const uint32_t groups = masks[i & 3];
       const int key0 = (t0 + i) * kTileKeys;
       const bool masked = groups != 0xFFu || __any_sync(0xffffffffu, lim < key0 + kTileKeys);
-      uint32_t s[4][32];
+      auto hide = [&](uint32_t (&s)[16], int u) {          // columns 16 u ..
+        const bool gone = !((groups >> u) & 1u);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) tmem_ld32(tS + 32 * u, s[u]);
-      tmem_ld_wait();
+        for (int j = 0; j < 16; ++j)
+          if (gone || key0 + 16 * u + j >= lim) s[j] = 0xFF800000u;
+      };
+      // f(columns 16 u .., u) for u = 0 .. 7, the next ones on their way meanwhile
+      auto each = [&](auto f) {
+        uint32_t sa[16], sb[16];
+        tmem_ld16(tS, sa);
+        tmem_ld_wait();
+        reg_fence(sa);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) reg_fence32(s[u]);
+        for (int u = 0; u < 8; u += 2) {
+          tmem_ld16(tS + 16 * (u + 1), sb);
+          f(sa, u);
+          tmem_ld_wait();
+          reg_fence(sb);
+          if (u + 2 < 8) tmem_ld16(tS + 16 * (u + 2), sa);
+          f(sb, u + 1);
+          tmem_ld_wait();
+          reg_fence(sa);
+        }
+      };
+      float tops[2] = {-INFINITY, -INFINITY};
+      auto largest = [&](uint32_t (&s)[16], int) {
+#pragma unroll
+        for (int j = 0; j < 16; j += 2)
+          tops[(j >> 1) & 1] =
+              fmaxf(tops[(j >> 1) & 1], fmaxf(__uint_as_float(s[j]), __uint_as_float(s[j + 1])));
+      };
       if (masked) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (key0 + 32 * u + j >= lim || !((groups >> (2 * u + (j >> 4))) & 1u))
-              s[u][j] = 0xFF800000u;
+        each([&](uint32_t (&s)[16], int u) {
+          hide(s, u);
+          largest(s, u);
+        });
+      } else {
+        each(largest);
       }
-      float tops[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        tops[u] = __uint_as_float(s[u][0]);
-#pragma unroll
-        for (int j = 1; j < 31; j += 2)
-          tops[u] = fmaxf(tops[u], fmaxf(__uint_as_float(s[u][j]), __uint_as_float(s[u][j + 1])));
-        tops[u] = fmaxf(tops[u], __uint_as_float(s[u][31]));
-      }
-      const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * mul;
-      if (__any_sync(0xffffffffu, top > m + 8.0f)) {
-        const float up = fmaxf(m, top);
+      const float top = fmaxf(tops[0], tops[1]) * mul;
+      // (a row without a visible key so far waits for one; no row's result
+      // depends on another's)
+      const bool raise = top > m + 8.0f;
+      if (__any_sync(0xffffffffu, raise)) {
+        const float up = raise ? top : m;
         const float alpha = m == -INFINITY ? 0.0f : kv8_exp2(m - up);
         const uint64_t a2 = pack2(alpha, alpha);
         l2[0] = mul2(l2[0], a2);
         l2[1] = mul2(l2[1], a2);
         m = up;
         if (i > 0) {
-          wait(pv_done + mt, (i - 1) & 1);
-          tc_fence_after();
-          if (!ok) break;
+          // (P V of the tile before was issued ahead of this tile's Q K^T, so O
+          // is complete with S)
 #pragma unroll 1
           for (int u = 0; u < D / 16; ++u) {
             uint32_t o[16];
@@ -292,43 +307,43 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
       // same for the whole row and cancels in P / l.  Where m is so large that
       // it would carry P out of range (ulp(2^16) = 2^-7), the logits are rounded
       // like m, which makes the largest difference 0 again.
-      const bool plain = !masked && !__any_sync(0xffffffffu, fabsf(m) > 65536.0f);
       const float mm = m == -INFINITY ? 0.0f : m;
-      if (plain) {
-        const uint64_t f2 = pack2(mul, mul), u2 = pack2(7.0f - mm, 7.0f - mm);
+      const uint64_t f2 = pack2(mul, mul), u2 = pack2(7.0f - mm, 7.0f - mm);
+      auto weights = [&](uint32_t (&s)[16], int u) {        // exponents -> P
+        uint32_t w[8];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            float x, y;
-            unpack2(fma2(pack2(__uint_as_float(s[u][j]), __uint_as_float(s[u][j + 1])), f2, u2), x, y);
-            s[u][j] = __float_as_uint(x);
-            s[u][j + 1] = __float_as_uint(y);
-          }
-      } else {
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            s[u][j] = __float_as_uint((__fmul_rn(__uint_as_float(s[u][j]), mul) - mm) + 7.0f);
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        uint32_t w[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float x = kv8_exp2(__uint_as_float(s[u][2 * j]));
-          const float y = kv8_exp2(__uint_as_float(s[u][2 * j + 1]));
+        for (int j = 0; j < 8; ++j) {
+          const float x = kv8_exp2(__uint_as_float(s[2 * j])), y = kv8_exp2(__uint_as_float(s[2 * j + 1]));
           l2[j & 1] = add2(l2[j & 1], pack2(x, y));
           w[j] = pack16(x, y, CSA2_F16);
         }
-        tmem_st16(tS + 16 * u, w);
-        if (u & 1) {
+        tmem_st8(tS + 8 * u, w);
+        if ((u & 3) == 3) {
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive((u == 1 ? p_half : p_full) + mt);
+          if (lane == 0) mbar_arrive((u == 3 ? p_half : p_full) + mt);
         }
+      };
+      if (!masked && !__any_sync(0xffffffffu, fabsf(mm) > 65536.0f)) {
+        each([&](uint32_t (&s)[16], int u) {
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            float x, y;
+            unpack2(fma2(pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), f2, u2), x, y);
+            s[j] = __float_as_uint(x);
+            s[j + 1] = __float_as_uint(y);
+          }
+          weights(s, u);
+        });
+      } else {
+        each([&](uint32_t (&s)[16], int u) {
+          hide(s, u);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            s[j] = __float_as_uint((__fmul_rn(__uint_as_float(s[j]), mul) - mm) + 7.0f);
+          weights(s, u);
+        });
       }
     }
     float l = 0.0f;
@@ -339,33 +354,46 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
       l = (a + b2) + (c2 + d);
     }
     // ---- the row's result
-    if (nt > 0 && mt < mts) wait(pv_done + mt, (nt - 1) & 1);
+    if (nt > 0 && mt < mts) wait(o_done, 0);
     tc_fence_after();
     const bool empty = l == 0.0f;
     const float base2 = empty ? -INFINITY : m + log2f(l) - 7.0f;
     if (p.splits == 1) {
+      // through shared memory (the query tile, done with), so that a row's
+      // stores go out together: 16-byte chunks, swizzled by the row
       const float f = empty ? 0.0f : vref / l;
-      uint16_t* out = static_cast<uint16_t*>(const_cast<void*>(p.a.out.data)) + b * p.a.out.sb +
-                      tok * p.a.out.st + hd * p.a.out.sh;
+      uint8_t* stage = smem + L::kQ + warp * 32 * 2 * D;
 #pragma unroll
-      for (int u = 0; u < D / 32; ++u) {
-        uint32_t s[32];
+      for (int u = 0; u < D / 16; ++u) {
+        uint32_t s[16];
         if (nt > 0 && mt < mts && ok) {
-          tmem_ld32(tO + 32 * u, s);
+          tmem_ld16(tO + 16 * u, s);
           tmem_ld_wait();
-          reg_fence32(s);
+          reg_fence(s);
         }
-        if (!real || !ok) continue;
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
+        for (int j = 0; j < 16; j += 8) {
           uint32_t w[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             w[q] = empty ? 0u
                          : pack16(__uint_as_float(s[j + 2 * q]) * f,
                                   __uint_as_float(s[j + 2 * q + 1]) * f, p.a.out.type);
-          *reinterpret_cast<uint4*>(out + 32 * u + j) = make_uint4(w[0], w[1], w[2], w[3]);
+          const int at = (2 * u + (j >> 3)) ^ (lane & 7);
+          *reinterpret_cast<uint4*>(stage + lane * 2 * D + 16 * at) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+      }
+      __syncwarp();
+      const int64_t off = b * p.a.out.sb + tok * p.a.out.st + hd * p.a.out.sh;
+#pragma unroll 4
+      for (int i = 0; i < 32 / kAt; ++i) {
+        const int row = i * kAt + lane / kPer;
+        const int64_t to = __shfl_sync(0xffffffffu, off, row);
+        const bool in = __shfl_sync(0xffffffffu, (int)(real && ok), row) != 0;
+        if (in)
+          *reinterpret_cast<uint4*>(static_cast<char*>(const_cast<void*>(p.a.out.data)) + 2 * to +
+                                    16 * chunk) =
+              *reinterpret_cast<const uint4*>(stage + row * 2 * D + 16 * (chunk ^ (row & 7)));
       }
       if (real && ok && p.a.lse)
         p.a.lse[((int64_t)b * p.a.T + tok) * p.a.H + hd] =
@@ -394,59 +422,68 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
         part[kTileRows * (D + 1) + r] = ok ? l : 0.0f;
       }
     }
-  } else if (warp < 12) {
+  } else if (warp < 16) {
     // ========================================================== converter warps
-    regs_dec<kRegsConvert>();
     // Thread: 16-byte chunk cc (of a 64-channel half) of rows r4 + 32 v.  Eight
     // neighbouring lanes then store to two rows' chunks of all eight positions.
-    const int ct = tid - 256, cc = ct & 3, r4 = ct >> 2;
+    regs_dec<kRegsConvert>();
+    const int side = warp >= 12, ct = tid & 127, cc = ct & 3, r4 = ct >> 2;
     constexpr int kPer = L::kSlabs * 4;
-    const float kinv = kv8_inverse(kref), vinv = kv8_inverse(vref);
-    // lanes 0..7: the tile's eight 16-row groups
-    int64_t grow = -1;
-    float gk = 0.0f, gv = 0.0f;
-    auto resolve = [&](int i) {
-      grow = -1;
-      gk = gv = 0.0f;
+    const float inv = kv8_inverse(side ? vref : kref);
+    uint64_t* full = side ? v_full : k_full;
+    uint8_t* tiles = smem + (side ? L::kV : L::kK);
+    const uint8_t* codes = c.codes[side] + 16 * cc;
+    const float* scales = c.scales[side];
+    // Lanes 0..7 look after the tile's eight 16-row groups.  A warp stops at the
+    // first use of a value that is still on its way, so each lookup is a tile
+    // apart from the next: page ids three tiles ahead, rows and scales two, codes
+    // one.
+    int in_page = 0;
+    auto fetch = [&](int i) -> int {         // page id; kNone: no row of this group counts
       const int pos = (t0 + i) * kTileKeys + 16 * (lane & 7);
-      if (i < nt && pos < keys) {
-        int in_page;
-        const int page = kv8_page(c, b, pos, in_page);
-        if (page >= 0) {
-          grow = kv8_row(c, page, h, in_page);
-          const int64_t at = kv8_block(c, page, h, in_page);
-          gk = c.scales[0][at] * kinv;
-          gv = c.scales[1][at] * vinv;
-        } else if (lane < 8) {
-          set_status(p.a.status, CSA2_DEV_BAD_PAGE);
-        }
+      if (i >= nt || pos >= keys) return kNone;
+      return kv8_page_id(c, b, pos);
+    };
+    int64_t grow = -1;
+    float gs = 0.0f;
+    auto place = [&](int i, int id) {
+      grow = -1;
+      gs = 0.0f;
+      if (id == kNone) return;
+      const int page = kv8_check(c, id);
+      if (page >= 0) {
+        kv8_in_page(c, (t0 + i) * kTileKeys + 16 * (lane & 7), in_page);
+        grow = kv8_row(c, page, h, in_page);
+        gs = scales[kv8_block(c, page, h, in_page)];
+      } else if (lane < 8) {
+        set_status(p.a.status, CSA2_DEV_BAD_PAGE);
       }
     };
-    uint4 raw[2][kPer];
-    float fac[2][4];
-    auto load = [&](int side, int i) {
+    uint4 raw[kPer];
+    float fac[4];
+    auto load = [&](int i) {
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const int row = r4 + 32 * v;
         const int64_t g = __shfl_sync(0xffffffffu, grow, row >> 4);
-        fac[side][v] = __shfl_sync(0xffffffffu, side ? gv : gk, row >> 4);
+        fac[v] = __shfl_sync(0xffffffffu, gs, row >> 4) * inv;
         // rows the CTA does not see stay 0: their scales are not in the range
         const bool in = g >= 0 && (t0 + i) * kTileKeys + row < keys;
-        const uint8_t* from = c.codes[side] + (g + (row & 15)) * D + 16 * cc;
+        const uint8_t* from = codes + (g + (row & 15)) * D;
 #pragma unroll
         for (int s = 0; s < L::kSlabs; ++s) {
-          raw[side][s * 4 + v] = make_uint4(0, 0, 0, 0);
-          if (in) raw[side][s * 4 + v] = *reinterpret_cast<const uint4*>(from + 64 * s);
+          raw[s * 4 + v] = make_uint4(0, 0, 0, 0);
+          if (in) raw[s * 4 + v] = load_once(from + 64 * s);
         }
       }
     };
-    auto convert = [&](int side, uint8_t* tile) {
+    auto convert = [&](uint8_t* tile) {
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const __half2 f = __float2half2_rn(fac[side][v]);
+        const __half2 f = __float2half2_rn(fac[v]);
 #pragma unroll
         for (int s = 0; s < L::kSlabs; ++s) {
-          const uint4 w = raw[side][s * 4 + v];
+          const uint4 w = raw[s * 4 + v];
           const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
           uint32_t o[8];
 #pragma unroll
@@ -466,40 +503,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
       fence_async_smem();
       __syncwarp();
     };
-    // K and V of the next tile are loaded as soon as this tile's registers are
-    // free, their pages and scales one tile earlier still
-    uint32_t good = 0, good_next = 0;
+    uint32_t good = 0;
+    int id = kNone;
     if (nt > 0) {
-      resolve(0);
-      load(0, 0);
-      load(1, 0);
+      place(0, fetch(0));
+      load(0);
       good = __ballot_sync(0xffffffffu, grow >= 0) & 0xFFu;
-      resolve(1);
+      place(1, fetch(1));
+      id = fetch(2);
     }
     for (int i = 0; i < nt; ++i) {
       const int st = i & 1;
-      if (i >= 2) wait(k_empty + st, ((i >> 1) - 1) & 1);
+      // K's stage is free once Q K^T of tile i - 2 is done with all query tiles;
+      // V's once P V of tile i - 2 is, which Q K^T of tile i - 1 came after
+      const int after = i - 2 + side;
+      if (i >= 2) wait(s_full + 2 * (mts - 1) + (after & 1), (after >> 1) & 1);
       if (!ok) break;
-      convert(0, smem + L::kK + st * L::kSlabs * L::kSlab);
+      convert(tiles + st * L::kSlabs * L::kSlab);
       if (warp == 8 && lane == 0) masks[i & 3] = good;
       __syncwarp();
-      if (lane == 0) mbar_arrive(k_full + st);
-      if (i + 1 < nt) load(0, i + 1);
-      if (i >= 2) wait(v_empty + st, ((i >> 1) - 1) & 1);
-      if (!ok) break;
-      convert(1, smem + L::kV + st * L::kSlabs * L::kSlab);
-      if (lane == 0) mbar_arrive(v_full + st);
+      if (lane == 0) mbar_arrive(full + st);
       if (i + 1 < nt) {
-        load(1, i + 1);
-        good_next = __ballot_sync(0xffffffffu, grow >= 0) & 0xFFu;
-        resolve(i + 2);
+        load(i + 1);
+        good = __ballot_sync(0xffffffffu, grow >= 0) & 0xFFu;
+        place(i + 2, id);
+        id = fetch(i + 3);
       }
-      good = good_next;
     }
   } else {
     // ================================================================ MMA thread
     regs_dec<kRegsMma>();
-    if (warp == 12 && lane == 0 && nt > 0) {
+    if (warp == 16 && lane == 0 && nt > 0) {
     constexpr uint32_t idesc_qk = instr_desc(0, 0, false, false, 128, 128);
     constexpr uint32_t idesc_pv = instr_desc(0, 0, false, true, 128, D);
     const uint64_t kmajor = smem_desc(smem_u32(smem), 16, 1024, 2);
@@ -518,6 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
           mma_ss(d, a + o, k_hi, b2 + o, k_hi, idesc_qk, (s | kk) ? 1u : 0u);
         }
     };
+    // A commit takes the issuing thread some 200 cycles and the tensor cores queue
+    // few MMAs, so there are two a tile: S of either query tile.  MMAs run in
+    // order, so S of tile i + 1 also says that P V of tile i is done.
     bool issued = false;
     ok = mbar_wait(q_ready, 0, abort_flag) && mbar_wait(k_full, 0, abort_flag);
     if (ok) {
@@ -526,15 +563,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
 #pragma unroll 1
       for (int mt = 0; mt < mts; ++mt) {
         qk(mt, 0);
-        mma_commit(s_full + mt);
+        mma_commit(s_full + 2 * mt);
       }
-      mma_commit(k_empty);
     }
     for (int i = 0; ok && i < nt; ++i) {
       const int st = i & 1, sn = st ^ 1;
+      const bool more = i + 1 < nt;
+      ok = mbar_wait(v_full + st, (i >> 1) & 1, abort_flag);
 #pragma unroll 1
       for (int mt = 0; ok && mt < mts; ++mt) {
-        ok = mbar_wait(v_full + st, (i >> 1) & 1, abort_flag);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (ok) ok = mbar_wait((half ? p_full : p_half) + mt, i & 1, abort_flag);
@@ -545,19 +582,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
             mma_ts(tmem + 256 + D * mt, tmem + 128 * mt + 8 * kk,
                    vd + st * kTileDesc + kk * 2048 / 16, v_hi, idesc_pv, (i | kk) ? 1u : 0u);
         }
-        if (!ok) break;
-        mma_commit(pv_done + mt);
-        if (mt == mts - 1) mma_commit(v_empty + st);
-        if (i + 1 < nt) {
+        if (!ok || !more) continue;
+        if (mt == 0) {
           ok = mbar_wait(k_full + sn, ((i + 1) >> 1) & 1, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          qk(mt, sn);
-          mma_commit(s_full + mt);
-          if (mt == mts - 1) mma_commit(k_empty + sn);
         }
+        qk(mt, sn);
+        mma_commit(s_full + 2 * mt + sn);
       }
     }
+    if (ok) mma_commit(o_done);
     if (issued) {   // let every issued MMA land before tensor memory is freed
       mma_commit(drain);
       mbar_wait_drain(drain, 0);
@@ -568,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
   if (!ok) set_status(p.a.status, CSA2_DEV_TIMEOUT);
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 16) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
