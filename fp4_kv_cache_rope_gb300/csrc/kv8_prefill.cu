@@ -32,7 +32,7 @@
 //
 // A softmax thread reads its row's 128 logits from tensor memory twice, 16 at a
 // time with the next ones on their way: once for the maximum, once for the
-// exponentials, whose P goes back in two halves, each handed over at once.  That
+// exponentials.  That
 // keeps every role within its registers: a spilled register is read back from
 // L2, because L1 is left little beside the tiles.
 #include "kv8_mma.cuh"
@@ -78,12 +78,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
     return;
   }
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
-  uint64_t* q_ready = bars;          // 8 warps
-  uint64_t* k_full = bars + 1;       // [2 stages] 4 warps
-  uint64_t* v_full = bars + 3;       // [2 stages] 4 warps
+  uint64_t* start = bars;            // the queries and K of tile 0: 12 warps
+  uint64_t* kv_full = bars + 1;      // [2: tile parity] V of tile i and K of i + 1: 8 warps
   uint64_t* s_full = bars + 5;       // [2 query tiles][2: tile parity] commit
   uint64_t* p_full = bars + 9;       // [2 query tiles] 4 warps
-  uint64_t* p_half = bars + 11;      // [2] 4 warps: the first 64 columns of P
   uint64_t* o_done = bars + 13;      // commit after the last MMA
   uint64_t* drain = bars + 14;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kFlags);
@@ -92,14 +90,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
   float* red = reinterpret_cast<float*>(smem + L::kFlags + 32);     // [4][2]
 
   if (tid == 0) {
-    mbar_init(q_ready, 8);
+    mbar_init(start, 12);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(k_full + i, 4);
-      mbar_init(v_full + i, 4);
+      mbar_init(kv_full + i, 8);
       mbar_init(s_full + i, 1);
       mbar_init(s_full + 2 + i, 1);
       mbar_init(p_full + i, 4);
-      mbar_init(p_half + i, 4);
     }
     mbar_init(o_done, 1);
     mbar_init(drain, 1);
@@ -223,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
       mul = fmaxf(p.a.scale_log2 / up * (kref > 0.0f ? kref : 1.0f), 1.2e-38f);
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_ready);
+      if (lane == 0) mbar_arrive(start);
     }
 
     float m = -INFINITY;
@@ -318,12 +314,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
           w[j] = pack16(x, y, CSA2_F16);
         }
         tmem_st8(tS + 8 * u, w);
-        if ((u & 3) == 3) {
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive((u == 3 ? p_half : p_full) + mt);
-        }
       };
       if (!masked && !__any_sync(0xffffffffu, fabsf(mm) > 65536.0f)) {
         each([&](uint32_t (&s)[16], int u) {
@@ -345,6 +335,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
           weights(s, u);
         });
       }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full + mt);
     }
     float l = 0.0f;
     {
@@ -430,7 +424,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
     const int side = warp >= 12, ct = tid & 127, cc = ct & 3, r4 = ct >> 2;
     constexpr int kPer = L::kSlabs * 4;
     const float inv = kv8_inverse(side ? vref : kref);
-    uint64_t* full = side ? v_full : k_full;
     uint8_t* tiles = smem + (side ? L::kV : L::kK);
     const uint8_t* codes = c.codes[side] + 16 * cc;
     const float* scales = c.scales[side];
@@ -522,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
       convert(tiles + st * L::kSlabs * L::kSlab);
       if (warp == 8 && lane == 0) masks[i & 3] = good;
       __syncwarp();
-      if (lane == 0) mbar_arrive(full + st);
+      if (lane == 0) mbar_arrive(side ? kv_full + st : i == 0 ? start : kv_full + (st ^ 1));
       if (i + 1 < nt) {
         load(i + 1);
         good = __ballot_sync(0xffffffffu, grow >= 0) & 0xFFu;
@@ -530,6 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
         id = fetch(i + 3);
       }
     }
+    // (there is no K behind the last tile's V)
+    if (!side && nt > 0 && ok && lane == 0) mbar_arrive(kv_full + ((nt - 1) & 1));
   } else {
     // ================================================================ MMA thread
     regs_dec<kRegsMma>();
@@ -552,11 +547,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
           mma_ss(d, a + o, k_hi, b2 + o, k_hi, idesc_qk, (s | kk) ? 1u : 0u);
         }
     };
-    // A commit takes the issuing thread some 200 cycles and the tensor cores queue
-    // few MMAs, so there are two a tile: S of either query tile.  MMAs run in
-    // order, so S of tile i + 1 also says that P V of tile i is done.
+    // A wait or a commit takes the issuing thread 200 to 300 cycles while shared
+    // memory is busy, and the tensor cores queue few MMAs: so there are three
+    // waits and two commits a tile.  MMAs run in order, so S of tile i + 1 also
+    // says that P V of tile i is done.
     bool issued = false;
-    ok = mbar_wait(q_ready, 0, abort_flag) && mbar_wait(k_full, 0, abort_flag);
+    ok = mbar_wait(start, 0, abort_flag);
     if (ok) {
       tc_fence_after();
       issued = true;
@@ -568,26 +564,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
     }
     for (int i = 0; ok && i < nt; ++i) {
       const int st = i & 1, sn = st ^ 1;
-      const bool more = i + 1 < nt;
-      ok = mbar_wait(v_full + st, (i >> 1) & 1, abort_flag);
+      ok = mbar_wait(kv_full + st, (i >> 1) & 1, abort_flag);
 #pragma unroll 1
       for (int mt = 0; ok && mt < mts; ++mt) {
+        ok = mbar_wait(p_full + mt, i & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (ok) ok = mbar_wait((half ? p_full : p_half) + mt, i & 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-            mma_ts(tmem + 256 + D * mt, tmem + 128 * mt + 8 * kk,
-                   vd + st * kTileDesc + kk * 2048 / 16, v_hi, idesc_pv, (i | kk) ? 1u : 0u);
-        }
-        if (!ok || !more) continue;
-        if (mt == 0) {
-          ok = mbar_wait(k_full + sn, ((i + 1) >> 1) & 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-        }
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(tmem + 256 + D * mt, tmem + 128 * mt + 8 * kk,
+                 vd + st * kTileDesc + kk * 2048 / 16, v_hi, idesc_pv, (i | kk) ? 1u : 0u);
+        if (i + 1 == nt) continue;
         qk(mt, sn);
         mma_commit(s_full + 2 * mt + sn);
       }
