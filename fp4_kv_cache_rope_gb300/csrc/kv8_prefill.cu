@@ -87,23 +87,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kFlags);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kFlags + 4);
   volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + L::kFlags + 8);
-  float* red = reinterpret_cast<float*>(smem + L::kFlags + 32);     // [4][2]
+  volatile float* red = reinterpret_cast<volatile float*>(smem + L::kFlags + 32);   // [K, V][4]
+  volatile float* refs = red + 8;    // [K, V] largest scale in the CTA's range
 
-  if (tid == 0) {
-    mbar_init(start, 12);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(kv_full + i, 8);
-      mbar_init(s_full + i, 1);
-      mbar_init(s_full + 2 + i, 1);
-      mbar_init(p_full + i, 4);
-    }
-    mbar_init(o_done, 1);
-    mbar_init(drain, 1);
-    *abort_flag = 0;
-    fence_barrier_init();
-  }
-  if (warp == 16) tmem_alloc(tmem_slot, 512);
-  tc_fence_before();
   griddep_wait();
   griddep_launch_dependents();
 
@@ -120,42 +106,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
   int ql = p.a.q_len ? p.a.q_len[b] : p.a.T;
   ql = ql < 0 ? 0 : (ql > p.a.T ? p.a.T : ql);
   const int row0 = rt * kTileRows;
-  const int rows = min(kTileRows, ql * p.a.G - row0);       // <= 0: nothing to do
-  const int last_tok = rows > 0 ? (row0 + rows - 1) / p.a.G : 0;
-  const int keys = rows > 0 ? max(0, min(n, n - ql + last_tok + 1)) : 0;
+  const int rows = min(kTileRows, ql * p.a.G - row0);
+  if (rows <= 0) return;                                    // uniform over the CTA
+  const int last_tok = (row0 + rows - 1) / p.a.G;
+  const int keys = max(0, min(n, n - ql + last_tok + 1));
   const int all_tiles = (keys + kTileKeys - 1) / kTileKeys;
   const int t0 = (int)((int64_t)all_tiles * split / p.splits);
   const int nt = (int)((int64_t)all_tiles * (split + 1) / p.splits) - t0;
   const int mts = rows > 128 ? 2 : 1;                       // query tiles with rows
 
-  // ---- largest scales in the range (a power of two; 0 when all are)
-  if (warp < 4) {
-    float mx[2] = {0.0f, 0.0f};
-    const int blk = 1 << c.block_shift;
-    const int end = min(keys, (t0 + nt) * kTileKeys);
-    for (int pos = t0 * kTileKeys / blk * blk + tid * blk; pos < end; pos += 128 * blk) {
-      int in_page;
-      const int page = kv8_page(c, b, pos, in_page);
-      if (page < 0) continue;
-      const int64_t at = kv8_block(c, page, h, in_page);
-      mx[0] = fmaxf(mx[0], c.scales[0][at]);
-      mx[1] = fmaxf(mx[1], c.scales[1][at]);
+  if (tid == 0) {
+    mbar_init(start, 12);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(kv_full + i, 8);
+      mbar_init(s_full + i, 1);
+      mbar_init(s_full + 2 + i, 1);
+      mbar_init(p_full + i, 4);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
-      mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
-    }
-    if (lane == 0) {
-      red[2 * warp] = mx[0];
-      red[2 * warp + 1] = mx[1];
-    }
+    mbar_init(o_done, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
   }
+  if (warp == 16) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const float kref = fmaxf(fmaxf(red[0], red[2]), fmaxf(red[4], red[6]));
-  const float vref = fmaxf(fmaxf(red[1], red[3]), fmaxf(red[5], red[7]));
   bool ok = true;   // this thread's view: false once a wait gave up
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (ok && !mbar_wait(bar, parity, abort_flag)) ok = false;
@@ -171,7 +148,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
     const int r = 128 * mt + 32 * (warp & 3) + lane;       // this thread's query row
     const int gr = row0 + r, tok = gr / p.a.G, hd = h * p.a.G + gr % p.a.G;
     const bool real = r < rows;
-    const int lim = real ? min(n, n - ql + tok + 1) : 0;
+    // (a row without a query is never written: it may see everything)
+    const int lim = real ? min(n, n - ql + tok + 1) : 0x7FFFFFFF;
     float mul = 0.0f;
     constexpr int kPer = D / 8;                            // 16-byte chunks of a row
     constexpr int kAt = 32 / kPer;                         // rows of a warp's access
@@ -215,8 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
                     make_uint4(pack16(x[0] * f, x[1] * f, CSA2_F16), pack16(x[2] * f, x[3] * f, CSA2_F16),
                                pack16(x[4] * f, x[5] * f, CSA2_F16), pack16(x[6] * f, x[7] * f, CSA2_F16)));
       }
-      // (kept above zero: hidden columns are -inf times it)
-      mul = fmaxf(p.a.scale_log2 / up * (kref > 0.0f ? kref : 1.0f), 1.2e-38f);
+      mul = p.a.scale_log2 / up;               // times K's largest scale, below
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(start);
@@ -228,13 +205,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
       wait(s_full + 2 * mt + (i & 1), (i >> 1) & 1);
       tc_fence_after();
       if (!ok) break;
+      if (i == 0) {
+        // (kept above zero: hidden columns are -inf times it)
+        const float kref = refs[0];
+        mul = fmaxf(mul * (kref > 0.0f ? kref : 1.0f), 1.2e-38f);
+      }
       // written before the tile's K was handed over, and not written again
       // before QK of tile i + 1, which waits for this tile's P
       const uint32_t groups = masks[i & 3];
       const int key0 = (t0 + i) * kTileKeys;
       const bool masked = groups != 0xFFu || __any_sync(0xffffffffu, lim < key0 + kTileKeys);
+      const int seen = masked ? (int)__reduce_min_sync(0xffffffffu, max(lim - key0, 0)) : 0;
       auto hide = [&](uint32_t (&s)[16], int u) {          // columns 16 u ..
         const bool gone = !((groups >> u) & 1u);
+        if (!gone && seen >= 16 * u + 16) return;          // every row sees them
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           if (gone || key0 + 16 * u + j >= lim) s[j] = 0xFF800000u;
@@ -315,23 +299,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
         }
         tmem_st8(tS + 8 * u, w);
       };
-      if (!masked && !__any_sync(0xffffffffu, fabsf(mm) > 65536.0f)) {
-        each([&](uint32_t (&s)[16], int u) {
+      auto exponents = [&](uint32_t (&s)[16]) {
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            float x, y;
-            unpack2(fma2(pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), f2, u2), x, y);
-            s[j] = __float_as_uint(x);
-            s[j + 1] = __float_as_uint(y);
-          }
-          weights(s, u);
-        });
-      } else {
-        each([&](uint32_t (&s)[16], int u) {
+        for (int j = 0; j < 16; j += 2) {
+          float x, y;
+          unpack2(fma2(pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), f2, u2), x, y);
+          s[j] = __float_as_uint(x);
+          s[j + 1] = __float_as_uint(y);
+        }
+      };
+      if (__any_sync(0xffffffffu, fabsf(mm) > 65536.0f)) {
+#pragma unroll 1
+        for (int u = 0; u < 8; ++u) {
+          uint32_t s[16];
+          tmem_ld16(tS + 16 * u, s);
+          tmem_ld_wait();
+          reg_fence(s);
           hide(s, u);
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             s[j] = __float_as_uint((__fmul_rn(__uint_as_float(s[j]), mul) - mm) + 7.0f);
+          weights(s, u);
+        }
+      } else if (masked) {
+        each([&](uint32_t (&s)[16], int u) {
+          hide(s, u);
+          exponents(s);
+          weights(s, u);
+        });
+      } else {
+        each([&](uint32_t (&s)[16], int u) {
+          exponents(s);
           weights(s, u);
         });
       }
@@ -355,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
     if (p.splits == 1) {
       // through shared memory (the query tile, done with), so that a row's
       // stores go out together: 16-byte chunks, swizzled by the row
-      const float f = empty ? 0.0f : vref / l;
+      const float f = empty ? 0.0f : refs[1] / l;
       uint8_t* stage = smem + L::kQ + warp * 32 * 2 * D;
 #pragma unroll
       for (int u = 0; u < D / 16; ++u) {
@@ -394,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
             empty ? -INFINITY : base2 * 0.6931471805599453f;
     } else {
       float* part = p.a.part + (int64_t)blockIdx.x * kTileRows * (D + 2);
-      const float f = empty ? 0.0f : vref;
+      const float f = empty ? 0.0f : refs[1];
 #pragma unroll
       for (int u = 0; u < D / 32; ++u) {
         uint32_t s[32];
@@ -423,10 +421,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
     regs_dec<kRegsConvert>();
     const int side = warp >= 12, ct = tid & 127, cc = ct & 3, r4 = ct >> 2;
     constexpr int kPer = L::kSlabs * 4;
-    const float inv = kv8_inverse(side ? vref : kref);
     uint8_t* tiles = smem + (side ? L::kV : L::kK);
     const uint8_t* codes = c.codes[side] + 16 * cc;
     const float* scales = c.scales[side];
+    // ---- the side's largest scale in the range (a power of two; 0 when all are)
+    float inv;
+    {
+      float mx = 0.0f;
+      const int blk = 1 << c.block_shift, end = min(keys, (t0 + nt) * kTileKeys);
+#pragma unroll 4
+      for (int pos = t0 * kTileKeys / blk * blk + ct * blk; pos < end; pos += 128 * blk) {
+        int in_page;
+        const int page = kv8_page(c, b, pos, in_page);
+        if (page >= 0) mx = fmaxf(mx, scales[kv8_block(c, page, h, in_page)]);
+      }
+      // scales are not negative: their bits compare alike
+      mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+      if (lane == 0) red[4 * side + (warp & 3)] = mx;
+      bar_sync(1 + side, 128);                 // (nothing before it can give up)
+      mx = fmaxf(fmaxf(red[4 * side], red[4 * side + 1]), fmaxf(red[4 * side + 2], red[4 * side + 3]));
+      if (ct == 0) refs[side] = mx;
+      inv = kv8_inverse(mx);
+    }
     // Lanes 0..7 look after the tile's eight 16-row groups.  A warp stops at the
     // first use of a value that is still on its way, so each lookup is a tile
     // apart from the next: page ids three tiles ahead, rows and scales two, codes
