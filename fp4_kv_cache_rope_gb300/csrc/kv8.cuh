@@ -19,9 +19,9 @@
 
 namespace csa2 {
 
-constexpr int kKv8Ctas = 512;      // upper bound of the split kernels' CTAs
+constexpr int kKv8Ctas = 640;      // upper bound of the split kernels' CTAs
 constexpr int kKv8SplitCtas = 256; // upper bound of the CTAs of a split prefill
-constexpr int kKv8SlotRows = 32;   // query rows of one partial result
+constexpr int kKv8SlotRows = 24;   // query rows of one partial result
 constexpr int kKv8Step = 128;      // cached rows of one step of a CTA
 
 struct Kv8 {
@@ -135,24 +135,60 @@ __device__ __forceinline__ void kv8_to_f32(uint32_t w, float (&v)[4]) {
   const float2 b = __half22float2(*reinterpret_cast<__half2*>(&hi));
   v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
 }
-// Largest magnitude among four codes as a number that grows with it.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Largest magnitude among sixteen codes as a number that grows with it.
 template <int FMT>
-__device__ __forceinline__ uint32_t kv8_max4(uint32_t w) {
-  const uint32_t m = FMT == CSA2_KV8_E4M3 ? (w & 0x7F7F7F7Fu) : __vabsss4(w);
-  const uint32_t x = __vmaxu4(m, m >> 16);
-  return max(x & 0xFFu, (x >> 8) & 0xFFu);
+__device__ __forceinline__ uint32_t kv8_max16(uint4 v) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w}, even = 0, odd = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (FMT == CSA2_KV8_INT8) {
+      const uint32_t neg = (w[i] >> 7) & 0x01010101u;          // |x|: ~x + 1 where negative
+      w[i] = (w[i] ^ (neg * 255u)) + neg;                      // (-128 is no code)
+    } else {
+      w[i] &= 0x7F7F7F7Fu;
+    }
+    even = max_u16x2(even, w[i] & 0x00FF00FFu);
+    odd = max_u16x2(odd, (w[i] >> 8) & 0x00FF00FFu);
+  }
+  const uint32_t m = max_u16x2(even, odd);
+  return max(m & 0xFFFFu, m >> 16);
 }
 template <int FMT>
 __device__ __forceinline__ float kv8_mag(uint32_t m) {
   return FMT == CSA2_KV8_E4M3 ? e4m3_decode(m) : (float)m;
 }
-// Four codes under scale s re-expressed with ratio = s / s_new.
+// Four codes re-expressed times ratio (a power of two; the results lie within
+// +-qmax), in f16: a code has at most 7 significant bits, so the product is
+// exact wherever it does not round to 0 anyway (2^-24 against half of the
+// smallest code, 2^-10 or 1/2), and is rounded to the format once.
 template <int FMT>
-__device__ __forceinline__ uint32_t kv8_recode(uint32_t w, float ratio) {
-  float v[4];
-  kv8_to_f32<FMT>(w, v);
-  return kv8_encode4<FMT>(v[0] * ratio, v[1] * ratio, v[2] * ratio, v[3] * ratio);
+__device__ __forceinline__ uint32_t kv8_recode(uint32_t w, __half2 ratio) {
+  uint32_t lo, hi;
+  kv8_to_f16<FMT>(w, lo, hi);
+  __half2 a = *reinterpret_cast<__half2*>(&lo), b = *reinterpret_cast<__half2*>(&hi);
+  if (FMT == CSA2_KV8_E4M3) {
+    a = __hmul2(a, ratio);
+    b = __hmul2(b, ratio);
+    uint32_t r;
+    asm("{\n.reg .b16 x, y;\ncvt.rn.satfinite.e4m3x2.f16x2 x, %1;\n"
+        "cvt.rn.satfinite.e4m3x2.f16x2 y, %2;\nmov.b32 %0, {x, y};\n}"
+        : "=r"(r)
+        : "r"(*reinterpret_cast<uint32_t*>(&a)), "r"(*reinterpret_cast<uint32_t*>(&b)));
+    return r;
+  }
+  // 1536 + v: v rounded to an integer, its low byte the code
+  const __half2 k = __half2half2(__ushort_as_half((unsigned short)0x6600));
+  a = __hfma2(a, ratio, k);
+  b = __hfma2(b, ratio, k);
+  return __byte_perm(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b), 0x6420);
 }
+// ratio as f16: below 2^-24 every product rounds to 0.
+__device__ __forceinline__ __half2 kv8_ratio(float r) { return __float2half2_rn(r); }
 
 // ------------------------------------------------------------------ row types
 __device__ __forceinline__ void bf16x2_to_f32(uint32_t w, float& a, float& b) {

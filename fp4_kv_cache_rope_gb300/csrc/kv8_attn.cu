@@ -27,10 +27,12 @@
 namespace csa2 {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4;                 // of a CTA that shares units with others
 constexpr int kThreads = 32 * kWarps;
 constexpr int kSub = 32;                  // cached rows of one warp's tile
 static_assert(kWarps * kSub == kKv8Step, "a step is one tile per warp");
+constexpr int kShort = 2048;              // capacity up to which a unit is one CTA's
+constexpr int kShortWarps = 8;
 
 struct DecodeParams {
   Kv8Attn a;
@@ -138,18 +140,18 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-template <int D>
+template <int D, int WARPS>
 struct DecodeSmem {
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kStages = 3;
   static constexpr int kTile = kSub * D;                 // bytes of K (and of V) per stage
   static constexpr int kStage = 2 * kTile;
   static constexpr int kRingWarp = kStages * kStage;
-  static constexpr int kMeta = kWarps * kRingWarp;       // per warp and stage: 4 scales, 2 flags
+  static constexpr int kMeta = WARPS * kRingWarp;        // per warp and stage: 4 scales, 2 flags
   static constexpr int kMetaWarp = kStages * 32;
-  static constexpr int kStat = kMeta + kWarps * kMetaWarp;  // m, l: fp32 [kWarps][32] each
-  static constexpr int kBytes = kStat + 2 * kWarps * 32 * 4;
+  static constexpr int kStat = kMeta + WARPS * kMetaWarp;   // m, l: fp32 [WARPS][32] each
+  static constexpr int kBytes = kStat + 2 * WARPS * 32 * 4;
   static constexpr int kRedRow = D + 4;                  // merge buffer (over the ring)
-  static_assert(kWarps * 32 * kRedRow * 4 <= kMeta, "merge buffer");
+  static constexpr bool fits(int nt) { return WARPS * 8 * nt * kRedRow * 4 <= kMeta; }
 };
 
 // Where a unit's partial result of CTA i goes: slot 2 i when the unit began in
@@ -161,14 +163,20 @@ struct Groups {
   int64_t row[2];   // row index of the group's first row, -1: none
   int64_t blk[2];   // index of its scale
 };
-// Every lane gets both; lane parity does one lookup each.
-__device__ __forceinline__ Groups resolve_groups(const Kv8& c, int b, int h, int pos, int n,
-                                                 uint32_t* status, int lane) {
-  int64_t row = -1, blk = 0;
+constexpr int kNoRows = -0x7FFFFFFF - 1;
+// A warp stops at the first use of a value that is still on its way, so the page
+// ids are read a tile before they are used.  Lane parity does one group each.
+__device__ __forceinline__ int fetch_page(const Kv8& c, int b, int pos, int n, int lane) {
   const int mine = pos + 16 * (lane & 1);
-  if (mine < n) {
+  return mine < n ? kv8_page_id(c, b, mine) : kNoRows;
+}
+__device__ __forceinline__ Groups place_groups(const Kv8& c, int id, int h, int pos,
+                                               uint32_t* status, int lane) {
+  int64_t row = -1, blk = 0;
+  if (id != kNoRows) {
     int in_page;
-    const int page = kv8_page(c, b, mine, in_page);
+    kv8_in_page(c, pos + 16 * (lane & 1), in_page);
+    const int page = kv8_check(c, id);
     if (page >= 0) {
       row = kv8_row(c, page, h, in_page);
       blk = kv8_block(c, page, h, in_page);
@@ -185,10 +193,22 @@ __device__ __forceinline__ Groups resolve_groups(const Kv8& c, int b, int h, int
   return g;
 }
 
-// NT: tiles of eight query rows.
-template <int D, int NT, int FMT>
-__global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(DecodeParams p) {
-  using L = DecodeSmem<D>;
+// CTAs that an SM holds: by the shared memory, and by the registers that more
+// query rows take.
+constexpr int decode_ctas(int D, int nt, int warps) {
+  return warps != kWarps ? 1 : D == 128 ? 2 : nt == 1 ? 4 : 3;
+}
+
+// NT: tiles of eight query rows.  WARPS = kWarps: the steps of all units are
+// shared out evenly; kShortWarps: every unit is one CTA's, and no partial results
+// are left to join.
+template <int D, int NT, int FMT, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, decode_ctas(D, NT, WARPS))
+    kv8_decode_kernel(DecodeParams p) {
+  using L = DecodeSmem<D, WARPS>;
+  static_assert(L::fits(NT), "merge buffer");
+  constexpr bool kWhole = WARPS != kWarps;
+  constexpr int kStep = WARPS * kSub;
   constexpr int kHalf = D / 64;
   constexpr int kMT = D / 16;                // 16-channel tiles of the output
   extern __shared__ __align__(128) uint8_t smem[];
@@ -200,18 +220,31 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(DecodeParams p)
   uint8_t* ring = smem + warp * L::kRingWarp;
   uint8_t* meta = smem + L::kMeta + warp * L::kMetaWarp;
   float* sm = reinterpret_cast<float*>(smem + L::kStat);
-  float* sl = sm + kWarps * 32;
+  float* sl = sm + WARPS * 32;
 
   const int units = c.heads * p.tiles;
-  const int64_t total = kv8_total(c, lane) * units;
-  const int ctas = kv8_sharers(total, p.ctas);
-  if ((int)blockIdx.x >= ctas) return;
-  int64_t x = total * blockIdx.x / ctas;
-  const int64_t x1 = total * (blockIdx.x + 1) / ctas;
-  int64_t first;
-  int b = kv8_find(c, lane, units, x, first);
-  int n = kv8_len(c, b), steps = kv8_steps(c, b);
-  int unit = (int)((x - first) / steps), st0 = (int)((x - first) % steps);
+  int b, n, steps, unit, st0;
+  int64_t x = 0, x1 = 0;
+  if (kWhole) {
+    b = blockIdx.x / units;
+    unit = blockIdx.x % units;
+    n = kv8_len(c, b);
+    steps = n <= kStep ? 1 : (n + kStep - 1) / kStep;
+    st0 = 0;
+    x1 = steps;
+  } else {
+    const int64_t total = kv8_total(c, lane) * units;
+    const int ctas = kv8_sharers(total, p.ctas);
+    if ((int)blockIdx.x >= ctas) return;
+    x = total * blockIdx.x / ctas;
+    x1 = total * (blockIdx.x + 1) / ctas;
+    int64_t first;
+    b = kv8_find(c, lane, units, x, first);
+    n = kv8_len(c, b);
+    steps = kv8_steps(c, b);
+    unit = (int)((x - first) / steps);
+    st0 = (int)((x - first) % steps);
+  }
 
   // this lane's places in a stage: 16-byte chunk `lane + 32 i` of the tile's
   // codes goes to dst[i & 1] + 512 i (D 128; rows of 64 bytes: dst[0] + 512 i)
@@ -226,12 +259,16 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(DecodeParams p)
 
     // ---- pipeline over this warp's tiles st0 .. st1
     Groups next;
-    auto resolve = [&](int st) {
-      next = resolve_groups(c, b, h, st * kKv8Step + warp * kSub, st < st1 ? n : 0, p.a.status, lane);
+    int id;
+    auto fetch = [&](int st) {
+      id = fetch_page(c, b, st * kStep + warp * kSub, st < st1 ? n : 0, lane);
+    };
+    auto place = [&](int st) {
+      next = place_groups(c, id, h, st * kStep + warp * kSub, p.a.status, lane);
     };
     auto issue = [&](int st, int stage) {
       if (st < st1) {
-        const int left = n - (st * kKv8Step + warp * kSub);
+        const int left = n - (st * kStep + warp * kSub);
         uint8_t* k = ring + stage * L::kStage;
         const int64_t at[2] = {next.row[0] * D + lane * 16, next.row[1] * D + lane * 16};
         if (left >= kSub && next.row[0] >= 0 && next.row[1] >= 0) {
@@ -260,11 +297,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(DecodeParams p)
       }
       cp_async_commit();
     };
-    resolve(st0);
+    fetch(st0);
 #pragma unroll
     for (int i = 0; i < L::kStages - 1; ++i) {
+      place(st0 + i);
+      fetch(st0 + i + 1);
       issue(st0 + i, i);
-      resolve(st0 + i + 1);
     }
 
     // ---- queries of this unit: row 8 u + g as B fragments; the logit factor
@@ -307,8 +345,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(DecodeParams p)
       __syncwarp();
       {
         const int nxt = st + L::kStages - 1;
+        place(nxt);
+        fetch(nxt + 1);
         issue(nxt, stage == 0 ? L::kStages - 1 : stage - 1);
-        resolve(nxt + 1);
       }
       const uint8_t* k = ring + stage * L::kStage;
       const uint8_t* v = k + L::kTile;
@@ -342,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(DecodeParams p)
 
       // ---- logits (base 2): s[u][i][2 r + e] is cached row 16 i + 8 r + key_of(g),
       // query row 8 u + 2 t + e
-      const int pos = st * kKv8Step + warp * kSub;
+      const int pos = st * kStep + warp * kSub;
       bool raise = false;
 #pragma unroll
       for (int u = 0; u < NT; ++u)
@@ -458,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(DecodeParams p)
     cp_async_wait<0>();
 
     // ---- merge the warps (over the ring), then write the rows or a partial result
-    const bool whole = st0 == 0 && st1 == steps;
+    const bool whole = kWhole || (st0 == 0 && st1 == steps);
     float* part = p.a.part + (2 * (int64_t)blockIdx.x + (st0 > 0 ? 0 : 1)) * slot_floats(D);
     float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
@@ -481,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(DecodeParams p)
         const int row = 8 * u + 2 * t + e;
         float top = sm[row];
 #pragma unroll
-        for (int i = 1; i < kWarps; ++i) top = fmaxf(top, sm[i * 32 + row]);
+        for (int i = 1; i < WARPS; ++i) top = fmaxf(top, sm[i * 32 + row]);
         // a sum of 0: no row was visible; of NaN: the query holds one
         const float f = ls[u][e] == 0.0f ? 0.0f : kv8_exp2(mx[u][e] - top) * (vref * 0x1p-7f);
         float* to = red + (warp * 8 * NT + row) * L::kRedRow + (D / 8) * g;
@@ -493,14 +532,14 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(DecodeParams p)
       }
     __syncthreads();
     // 8 channels a thread
-    for (int id = tid; id < 8 * NT * (D / 8); id += kThreads) {
-      const int row = id / (D / 8), ch = 8 * (id % (D / 8));
+    for (int at = tid; at < 8 * NT * (D / 8); at += 32 * WARPS) {
+      const int row = at / (D / 8), ch = 8 * (at % (D / 8));
       float top = sm[row], l = 0.0f;
 #pragma unroll
-      for (int i = 1; i < kWarps; ++i) top = fmaxf(top, sm[i * 32 + row]);
+      for (int i = 1; i < WARPS; ++i) top = fmaxf(top, sm[i * 32 + row]);
       float y[8] = {};
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
+      for (int i = 0; i < WARPS; ++i) {
         const float wl = sl[i * 32 + row];
         l += wl == 0.0f ? 0.0f : wl * kv8_exp2(sm[i * 32 + row] - top);
         const float4* from =
@@ -531,6 +570,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(DecodeParams p)
         }
       }
     }
+    if (kWhole) return;
     __syncthreads();   // the ring takes the next unit's rows
 
     // ---- next unit
@@ -662,11 +702,16 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kv8_mass_kernel(Dec
     ql = ql < 0 ? 0 : (ql > p.a.T ? p.a.T : ql);
 
     Groups at;
+    int id;
+    auto fetch = [&](int st) {
+      id = fetch_page(c, b, st * kKv8Step + warp * kSub, st < st1 ? n : 0, lane);
+    };
     uint4 raw[2][kHalf][2];     // rows 16 i + 8 r + g, 16-byte chunk 4 f + t
     float ks[2];
     auto load = [&](int st) {
       const int pos = st * kKv8Step + warp * kSub;
-      at = resolve_groups(c, b, h, pos, st < st1 ? n : 0, p.a.status, lane);
+      at = place_groups(c, id, h, pos, p.a.status, lane);
+      fetch(st + 1);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         ks[i] = at.row[i] >= 0 ? c.scales[0][at.blk[i]] : 0.0f;
@@ -681,6 +726,7 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kv8_mass_kernel(Dec
           }
       }
     };
+    fetch(st0);
     load(st0);
 
     uint32_t qf[NT][D / 16][2];
@@ -772,24 +818,40 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kv8_mass_kernel(Dec
 }
 
 template <int D, int NT, int FMT>
-cudaError_t decode_as(const DecodeParams& p, cudaStream_t s) {
-  auto kern = kv8_decode_kernel<D, NT, FMT>;
+cudaError_t decode_as(DecodeParams p, int num_sms, cudaStream_t s) {
+  const int64_t units = (int64_t)p.a.c.batch * p.a.c.heads * p.tiles;
+  // Short caches in one launch: 1000 rows take as long on the GPU as shared out
+  // and joined (10.5 us), and the host one launch less.
+  if (p.a.c.max_len <= kShort) {
+    using L = DecodeSmem<D, kShortWarps>;
+    auto kern = kv8_decode_kernel<D, NT, FMT, kShortWarps>;
+    static std::atomic<uint64_t> seen;
+    const cudaError_t e = kv8_prepare(kern, L::kBytes, seen);
+    if (e != cudaSuccess) return e;
+    return kv8_launch(kern, dim3((unsigned)units), 32 * kShortWarps, L::kBytes, s, p);
+  }
+  using L = DecodeSmem<D, kWarps>;
+  auto kern = kv8_decode_kernel<D, NT, FMT, kWarps>;
   static std::atomic<uint64_t> seen;
-  cudaError_t e = kv8_prepare(kern, DecodeSmem<D>::kBytes, seen);
+  cudaError_t e = kv8_prepare(kern, L::kBytes, seen);
   if (e != cudaSuccess) return e;
-  e = kv8_launch(kern, dim3(p.ctas), kThreads, DecodeSmem<D>::kBytes, s, p);
+  const int ctas = decode_ctas(D, NT, kWarps) * num_sms;
+  p.ctas = ctas < kKv8Ctas ? ctas : kKv8Ctas;
+  e = kv8_launch(kern, dim3(p.ctas), kThreads, L::kBytes, s, p);
   if (e != cudaSuccess) return e;
-  return kv8_launch(kv8_combine_kernel<D>, dim3(p.a.c.batch * p.a.c.heads * p.tiles, 8 * NT),
-                    D / 4 * kCombine, 0, s, p, 8 * NT);
+  return kv8_launch(kv8_combine_kernel<D>, dim3((unsigned)units, 8 * NT), D / 4 * kCombine, 0, s, p,
+                    8 * NT);
 }
 template <int D, int FMT>
-cudaError_t decode_of(DecodeParams p, cudaStream_t s) {
-  const int nt = p.rows <= 8 ? 1 : p.rows <= 16 ? 2 : p.rows <= 24 ? 3 : 4;
+cudaError_t decode_of(DecodeParams p, int num_sms, cudaStream_t s) {
+  // More than 24 rows go as several tiles of 16, whose cached rows come from L2
+  // the second time: 16 sequences of 9000 rows, 32 query rows, D 128: 47 us
+  // against 70 us in one tile of 32, which does not fit the registers.
+  const int nt = p.rows <= 8 ? 1 : p.rows <= 16 || p.rows > 24 ? 2 : 3;
   p.tiles = (p.rows + 8 * nt - 1) / (8 * nt);
-  return nt == 1   ? decode_as<D, 1, FMT>(p, s)
-         : nt == 2 ? decode_as<D, 2, FMT>(p, s)
-         : nt == 3 ? decode_as<D, 3, FMT>(p, s)
-                   : decode_as<D, 4, FMT>(p, s);
+  return nt == 1   ? decode_as<D, 1, FMT>(p, num_sms, s)
+         : nt == 2 ? decode_as<D, 2, FMT>(p, num_sms, s)
+                   : decode_as<D, 3, FMT>(p, num_sms, s);
 }
 template <int D, int FMT>
 cudaError_t mass_of(const DecodeParams& p, cudaStream_t s) {
@@ -803,10 +865,12 @@ cudaError_t mass_of(const DecodeParams& p, cudaStream_t s) {
 size_t kv8_part_bytes(int D) { return 2 * (size_t)kKv8Ctas * slot_floats(D) * 4; }
 
 cudaError_t launch_kv8_attn(const Kv8Attn& a, int num_sms, cudaStream_t s) {
-  DecodeParams p{a, a.T * a.G, 1, 2 * num_sms < kKv8Ctas ? 2 * num_sms : kKv8Ctas};
+  DecodeParams p{a, a.T * a.G, 1, 1};
   if (a.c.format == CSA2_KV8_E4M3)
-    return a.D == 64 ? decode_of<64, CSA2_KV8_E4M3>(p, s) : decode_of<128, CSA2_KV8_E4M3>(p, s);
-  return a.D == 64 ? decode_of<64, CSA2_KV8_INT8>(p, s) : decode_of<128, CSA2_KV8_INT8>(p, s);
+    return a.D == 64 ? decode_of<64, CSA2_KV8_E4M3>(p, num_sms, s)
+                     : decode_of<128, CSA2_KV8_E4M3>(p, num_sms, s);
+  return a.D == 64 ? decode_of<64, CSA2_KV8_INT8>(p, num_sms, s)
+                   : decode_of<128, CSA2_KV8_INT8>(p, num_sms, s);
 }
 
 cudaError_t launch_kv8_mass_few(const Kv8Attn& a, int num_sms, cudaStream_t s) {

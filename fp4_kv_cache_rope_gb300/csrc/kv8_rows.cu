@@ -53,12 +53,13 @@ __device__ __forceinline__ uint32_t group_max(uint32_t x, uint32_t* red, int tid
 // allow it both sides are read before either is worked on.  The maximum is taken
 // over the bits of the magnitudes (two 16-bit values at a time), which also
 // shows whether there is an infinity or a NaN.
-// EL: elements per 16 bytes (4 fp32, 8 of 16 bits).
-template <int D, int EL, int NT, int PASSES>
+// TYPE: the rows' type.
+template <int D, int TYPE, int NT, int PASSES>
 struct NewRows {
-  static constexpr int kLanes = D / EL;    // threads per row
+  static constexpr int EL = TYPE == CSA2_F32 ? 4 : 8;   // elements per 16 bytes
+  static constexpr int kLanes = D / EL;                 // threads per row
   static constexpr int kRows = NT / kLanes;
-  static constexpr int ES = 16 / EL;
+  static constexpr uint32_t kInf = TYPE == CSA2_F32 ? 0x7F800000u : TYPE == CSA2_BF16 ? 0x7F80u : 0x7C00u;
   uint4 raw[PASSES];
   float s0;                                // the block's scale so far
 
@@ -66,8 +67,8 @@ struct NewRows {
                                        int hi, bool had, const float* scale, int tid) {
     const int sub = tid / kLanes, ch = (tid % kLanes) * EL;
     const char* src = static_cast<const char*>(in.data) +
-                      (b * in.sb + (int64_t)(lo - sp.start + sub) * in.st + h * in.sh + ch) * ES;
-    const int64_t step = (int64_t)kRows * in.st * ES;
+                      (b * in.sb + (int64_t)(lo - sp.start + sub) * in.st + h * in.sh + ch) * (16 / EL);
+    const int64_t step = (int64_t)kRows * in.st * (16 / EL);
     s0 = had ? *scale : 0.0f;
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
@@ -76,24 +77,38 @@ struct NewRows {
     }
   }
 
+  // the elements of word j of an access, times inv (a power of two)
+  static __device__ __forceinline__ void scaled(uint32_t w, float inv, float (&v)[2]) {
+    if (TYPE == CSA2_F32) {
+      v[0] = __uint_as_float(w) * inv;
+    } else if (TYPE == CSA2_BF16) {
+      // exact in bf16 too, whose exponents are fp32's
+      const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w),
+                                       __float2bfloat162_rn(inv));
+      bf16x2_to_f32(*reinterpret_cast<const uint32_t*>(&x), v[0], v[1]);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+      v[0] = f.x * inv;
+      v[1] = f.y * inv;
+    }
+  }
+
   // row0: index of the block's first row; lo, hi: the new rows' positions
   template <int FMT>
-  __device__ __forceinline__ void write(const AppendParams& p, int type, uint8_t* codes,
-                                        float* scale, int64_t row0, int b0, int lo, int hi,
-                                        uint32_t* red, int tid) {
+  __device__ __forceinline__ void write(const AppendParams& p, uint8_t* codes, float* scale,
+                                        int64_t row0, int b0, int lo, int hi, uint32_t* red, int tid) {
     const int sub = tid / kLanes, ch = (tid % kLanes) * EL;
-    const uint32_t inf = EL == 4 ? 0x7F800000u : (type == CSA2_BF16 ? 0x7F80u : 0x7C00u);
     uint32_t bits = 0;
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
       const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        bits = EL == 4 ? max(bits, w[j] & 0x7FFFFFFFu) : __vmaxu2(bits, w[j] & 0x7FFF7FFFu);
+        bits = EL == 4 ? max(bits, w[j] & 0x7FFFFFFFu) : max_u16x2(bits, w[j] & 0x7FFF7FFFu);
     }
     if (EL == 8) bits = max(bits & 0xFFFFu, bits >> 16);
     bits = group_max<NT>(bits, red, tid);
-    const bool odd = bits >= inf;          // uniform over the group
+    const bool odd = bits >= kInf;         // uniform over the group
     if (odd) {                             // the maximum of the finite values then
       if (tid == 0) set_status(p.status, CSA2_DEV_NONFINITE);
       bits = 0;
@@ -103,56 +118,62 @@ struct NewRows {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int e = 0; e < (EL == 4 ? 1 : 2); ++e) {
+          for (int e = 0; e < EL / 4; ++e) {
             const uint32_t m = EL == 4 ? w[j] & 0x7FFFFFFFu : (w[j] >> (16 * e)) & 0x7FFFu;
-            if (m < inf) bits = max(bits, m);
+            if (m < kInf) bits = max(bits, m);
           }
       }
       bits = group_max<NT>(bits, red, tid);
     }
     __syncwarp();                          // every thread of the group has read s0
-    const float amax = EL == 4 ? __uint_as_float(bits)
-                       : type == CSA2_BF16
+    const float amax = TYPE == CSA2_F32 ? __uint_as_float(bits)
+                       : TYPE == CSA2_BF16
                            ? __uint_as_float(bits << 16)
                            : __half2float(__ushort_as_half((unsigned short)bits));
     const float s1 = fmaxf(s0, kv8_scale_of<FMT>(amax));
     const float inv = kv8_inverse(s1);
-    const float big = s1 > 0.0f ? (FMT == CSA2_KV8_E4M3 ? 448.0f : 127.0f) : 0.0f;
     uint8_t* dst = codes + (row0 + (lo - b0) + sub) * D + ch;
+    if (odd) {                             // infinities and NaN among the rows
+      const float big = s1 > 0.0f ? (FMT == CSA2_KV8_E4M3 ? 448.0f : 127.0f) : 0.0f;
+#pragma unroll 1
+      for (int i = 0; i < PASSES; ++i) {
+        if (lo + i * kRows + sub >= hi) continue;
+        uint4 r = raw[0];
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-      if (lo + i * kRows + sub >= hi) continue;
-      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-      float v[EL];
+        for (int k = 1; k < PASSES; ++k)
+          if (k == i) r = raw[k];
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+        float v[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (EL == 4) {
-          v[j] = __uint_as_float(w[j]);
-        } else if (type == CSA2_BF16) {
-          bf16x2_to_f32(w[j], v[2 * j % EL], v[(2 * j + 1) % EL]);
-        } else {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-          v[2 * j % EL] = f.x;
-          v[(2 * j + 1) % EL] = f.y;
+        for (int j = 0; j < 4; ++j) {
+          float x[2];
+          scaled(w[j], 1.0f, x);
+          if (EL == 4) v[j] = x[0];
+          else v[2 * j] = x[0], v[2 * j + 1] = x[1];
         }
-      }
 #pragma unroll
-      for (int j = 0; j < EL; ++j) {
-        const float x = v[j];
-        v[j] = x * inv;
-        if (odd && !(fabsf(x) <= 3.402823466e38f)) v[j] = x != x ? 0.0f : copysignf(big, x);
+        for (int j = 0; j < EL; ++j)
+          v[j] = fabsf(v[j]) <= 3.402823466e38f ? v[j] * inv : v[j] != v[j] ? 0.0f : copysignf(big, v[j]);
+        store<FMT>(dst + (int64_t)i * kRows * D, v);
       }
-      uint8_t* to = dst + (int64_t)i * kRows * D;
-      if (EL == 4) {
-        *reinterpret_cast<uint32_t*>(to) = kv8_encode4<FMT>(v[0], v[1], v[2], v[3]);
-      } else {
-        *reinterpret_cast<uint2*>(to) =
-            make_uint2(kv8_encode4<FMT>(v[0], v[1], v[2], v[3]),
-                       kv8_encode4<FMT>(v[4 % EL], v[5 % EL], v[6 % EL], v[7 % EL]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) {
+        if (lo + i * kRows + sub >= hi) continue;
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float x[2];
+          scaled(w[j], inv, x);
+          if (EL == 4) v[j] = x[0];
+          else v[2 * j] = x[0], v[2 * j + 1] = x[1];
+        }
+        store<FMT>(dst + (int64_t)i * kRows * D, v);
       }
     }
     if (s1 > s0 && s0 > 0.0f) {            // the block's earlier rows under the larger scale
-      const float ratio = s0 * inv;
+      const __half2 ratio = kv8_ratio(s0 * inv);
       uint8_t* old = codes + row0 * D;
       for (int i = tid; i < (lo - b0) * D / 8; i += NT) {
         uint2 w = *reinterpret_cast<uint2*>(old + 8 * i);
@@ -163,9 +184,18 @@ struct NewRows {
     }
     if (tid == 0 && (s1 > s0 || lo == b0)) *scale = s1;
   }
+
+  template <int FMT>
+  static __device__ __forceinline__ void store(uint8_t* to, const float (&v)[8]) {
+    if (EL == 4)
+      *reinterpret_cast<uint32_t*>(to) = kv8_encode4<FMT>(v[0], v[1], v[2], v[3]);
+    else
+      *reinterpret_cast<uint2*>(to) = make_uint2(kv8_encode4<FMT>(v[0], v[1], v[2], v[3]),
+                                                 kv8_encode4<FMT>(v[4], v[5], v[6], v[7]));
+  }
 };
 
-template <int D, int EL, int FMT, int NT, int PASSES, int SIDES>
+template <int D, int TYPE, int FMT, int NT, int PASSES, int SIDES>
 __device__ __forceinline__ void append_block(const AppendParams& p, const Span& sp, int b, int h,
                                              int side, int blk, uint32_t* red, int tid) {
   const Kv8& c = p.c;
@@ -181,16 +211,15 @@ __device__ __forceinline__ void append_block(const AppendParams& p, const Span& 
   const int64_t row0 = kv8_row(c, page, h, in_page), at = kv8_block(c, page, h, in_page);
   const bool had = sp.start > b0;
   if (SIDES == 2) {
-    NewRows<D, EL, NT, PASSES> k, v;
+    NewRows<D, TYPE, NT, PASSES> k, v;
     k.read(p.in[0], sp, b, h, lo, hi, had, c.scales[0] + at, tid);
     v.read(p.in[1], sp, b, h, lo, hi, had, c.scales[1] + at, tid);
-    k.template write<FMT>(p, p.in[0].type, c.codes[0], c.scales[0] + at, row0, b0, lo, hi, red, tid);
-    v.template write<FMT>(p, p.in[0].type, c.codes[1], c.scales[1] + at, row0, b0, lo, hi, red, tid);
+    k.template write<FMT>(p, c.codes[0], c.scales[0] + at, row0, b0, lo, hi, red, tid);
+    v.template write<FMT>(p, c.codes[1], c.scales[1] + at, row0, b0, lo, hi, red, tid);
   } else {
-    NewRows<D, EL, NT, PASSES> x;
+    NewRows<D, TYPE, NT, PASSES> x;
     x.read(p.in[side], sp, b, h, lo, hi, had, c.scales[side] + at, tid);
-    x.template write<FMT>(p, p.in[0].type, c.codes[side], c.scales[side] + at, row0, b0, lo, hi, red,
-                          tid);
+    x.template write<FMT>(p, c.codes[side], c.scales[side] + at, row0, b0, lo, hi, red, tid);
   }
   if (side == 0 && c.mass)
     for (int r = tid; r < hi - lo; r += NT) c.mass[row0 + (lo - b0) + r] = 0.0f;
@@ -199,7 +228,7 @@ __device__ __forceinline__ void append_block(const AppendParams& p, const Span& 
 // Appends of a few rows: one CTA per sequence, a warp per (head, side), so that
 // one launch also advances seq_len (every warp reads it before the barrier).
 constexpr int kFewRows = 8;
-template <int D, int EL, int FMT>
+template <int D, int TYPE, int FMT>
 __global__ void __launch_bounds__(512) kv8_append_few_kernel(AppendParams p) {
   griddep_wait();
   griddep_launch_dependents();
@@ -214,15 +243,15 @@ __global__ void __launch_bounds__(512) kv8_append_few_kernel(AppendParams p) {
   const int first = sp.start >> p.c.block_shift, last = (sp.start + sp.t - 1) >> p.c.block_shift;
   for (int i = threadIdx.x >> 5; i < 2 * p.c.heads; i += warps)
     for (int blk = first; blk <= last; ++blk)
-      append_block<D, EL, FMT, 32, kFewRows * D / EL / 32, 1>(p, sp, b, i >> 1, i & 1, blk,
-                                                              nullptr, lane);
+      append_block<D, TYPE, FMT, 32, kFewRows * D / NewRows<D, TYPE, 32, 1>::EL / 32, 1>(
+          p, sp, b, i >> 1, i & 1, blk, nullptr, lane);
 }
 
 // Longer appends: one CTA per (block, head, sequence), or side of it.  PASSES:
 // 16-byte accesses of a thread that hold a side of a block.
 constexpr int kAppendThreads = 256;
 constexpr int append_sides(int passes) { return passes <= 8 ? 2 : 1; }
-template <int D, int EL, int FMT, int PASSES>
+template <int D, int TYPE, int FMT, int PASSES>
 __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendParams p) {
   __shared__ uint32_t red[kAppendThreads / 32];
   griddep_wait();
@@ -235,7 +264,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendParams
   }
   if (sp.t == 0) return;
   constexpr int kSides = append_sides(PASSES);
-  append_block<D, EL, FMT, kAppendThreads, PASSES, kSides>(
+  append_block<D, TYPE, FMT, kAppendThreads, PASSES, kSides>(
       p, sp, b, kSides == 2 ? blockIdx.y : blockIdx.y >> 1, kSides == 2 ? 0 : blockIdx.y & 1,
       (sp.start >> p.c.block_shift) + blockIdx.x, red, threadIdx.x);
 }
@@ -248,12 +277,12 @@ __global__ void kv8_advance_kernel(AppendParams p) {
   p.c.seq_len[b] = sp.start + sp.t;
 }
 
-template <int D, int EL, int FMT>
+template <int D, int TYPE, int FMT>
 cudaError_t append_as(const AppendParams& p0, cudaStream_t s) {
   AppendParams p = p0;
   if (p.T <= kFewRows) {
     const int warps = 2 * p.c.heads < 16 ? 2 * p.c.heads : 16;
-    return kv8_launch(kv8_append_few_kernel<D, EL, FMT>, dim3(p.c.batch), 32 * warps, 0, s, p);
+    return kv8_launch(kv8_append_few_kernel<D, TYPE, FMT>, dim3(p.c.batch), 32 * warps, 0, s, p);
   }
   const int block = 1 << p.c.block_shift;
   // with `start` given nothing in the launch reads seq_len, so it may write it
@@ -263,19 +292,18 @@ cudaError_t append_as(const AppendParams& p0, cudaStream_t s) {
                     p.c.batch);
     return kv8_launch(kern, grid, kAppendThreads, 0, s, p);
   };
-  constexpr int kMost = 128 * D / EL / kAppendThreads;   // passes of 128 rows
-  const cudaError_t e = block == 128 ? run(kv8_append_kernel<D, EL, FMT, kMost>, kMost)
-                        : block == 64 ? run(kv8_append_kernel<D, EL, FMT, kMost / 2>, kMost / 2)
-                                      : run(kv8_append_kernel<D, EL, FMT, kMost / 4>, kMost / 4);
+  constexpr int kMost = 128 * D / (TYPE == CSA2_F32 ? 4 : 8) / kAppendThreads;   // passes of 128 rows
+  const cudaError_t e = block == 128 ? run(kv8_append_kernel<D, TYPE, FMT, kMost>, kMost)
+                        : block == 64 ? run(kv8_append_kernel<D, TYPE, FMT, kMost / 2>, kMost / 2)
+                                      : run(kv8_append_kernel<D, TYPE, FMT, kMost / 4>, kMost / 4);
   if (e != cudaSuccess || p.own_len) return e;
   return kv8_launch(kv8_advance_kernel, dim3((p.c.batch + 127) / 128), 128, 0, s, p);
 }
-template <int D>
+template <int D, int FMT>
 cudaError_t append_of(const AppendParams& p, cudaStream_t s) {
-  const bool wide = p.in[0].type == CSA2_F32;
-  if (p.c.format == CSA2_KV8_E4M3)
-    return wide ? append_as<D, 4, CSA2_KV8_E4M3>(p, s) : append_as<D, 8, CSA2_KV8_E4M3>(p, s);
-  return wide ? append_as<D, 4, CSA2_KV8_INT8>(p, s) : append_as<D, 8, CSA2_KV8_INT8>(p, s);
+  return p.in[0].type == CSA2_F32    ? append_as<D, CSA2_F32, FMT>(p, s)
+         : p.in[0].type == CSA2_BF16 ? append_as<D, CSA2_BF16, FMT>(p, s)
+                                     : append_as<D, CSA2_F16, FMT>(p, s);
 }
 
 // ------------------------------------------------------------------- eviction
@@ -366,11 +394,14 @@ __global__ void __launch_bounds__(kSelThreads) kv8_evict_select_kernel(EvictPara
     __syncthreads();
     const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
     each([&](int, bool in, uint32_t k) {
-      // (weights share their leading bits: the lanes with one digit add once)
       const bool hit = in && (k & mask) == prefix;
       const uint32_t d = hit ? (k >> shift) & 255u : 256u;
-      const uint32_t same = __match_any_sync(0xffffffffu, d);
-      if (hit && lane == __ffs(same) - 1) atomicAdd(&mine[d], (uint32_t)__popc(same));
+      if (shift == 24) {     // weights share their leading bits: equal digits add once
+        const uint32_t same = __match_any_sync(0xffffffffu, d);
+        if (hit && lane == __ffs(same) - 1) atomicAdd(&mine[d], (uint32_t)__popc(same));
+      } else if (hit) {
+        atomicAdd(&mine[d], 1u);
+      }
     });
     cluster_sync();
     if (tid < 256) {
@@ -444,33 +475,42 @@ __global__ void __launch_bounds__(kSelThreads) kv8_evict_select_kernel(EvictPara
   cluster_sync();                                  // peers may still read this CTA's counts
 }
 
-// A block of the result: its rows' codes (one side) in the registers of a CTA,
-// 16 codes a thread and pass.
+template <int FMT>
+__device__ __forceinline__ uint4 recode16(uint4 w, __half2 ratio) {
+  return make_uint4(kv8_recode<FMT>(w.x, ratio), kv8_recode<FMT>(w.y, ratio),
+                    kv8_recode<FMT>(w.z, ratio), kv8_recode<FMT>(w.w, ratio));
+}
+
+// A block of the result: its rows' codes, K and V, in the registers of a CTA, 16
+// codes a thread and pass.
 constexpr int kMoveThreads = 256;
 constexpr int kMoveCluster = 8;
 template <int D, int FMT, int PASSES>
 struct MovedBlock {
   static constexpr int kLanes = D / 16, kRows = kMoveThreads / kLanes;
-  uint4 code[PASSES];
-  float scale[PASSES], mass[PASSES];
-  float amax;
+  uint4 code[2][PASSES];
+  float scale[2][PASSES], mass[PASSES];
+  float amax[2];
   int rows;
   bool moved;
 
-  // reads the rows; every thread of the CTA gets the block's largest value
-  __device__ __forceinline__ void read(const EvictParams& p, int b, int h, int side, int blk, int m,
+  // reads the rows; every thread of the CTA gets the sides' largest values
+  __device__ __forceinline__ void read(const EvictParams& p, int b, int h, int blk, int m,
                                        const int32_t* kept, uint32_t* red) {
     const Kv8& s = p.src;
     const int b0 = blk << p.dst.block_shift;
     rows = min(1 << p.dst.block_shift, m - b0);
     const int sub = threadIdx.x / kLanes, ch = (threadIdx.x % kLanes) * 16;
     bool other = false;
-    float big = 0.0f;
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
       const int r = i * kRows + sub;
-      code[i] = make_uint4(0, 0, 0, 0);
-      scale[i] = mass[i] = 0.0f;
+      mass[i] = 0.0f;
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        code[side][i] = make_uint4(0, 0, 0, 0);
+        scale[side][i] = 0.0f;
+      }
       if (r >= rows) continue;
       const int from = kept[b0 + r];
       other |= from != b0 + r;
@@ -480,22 +520,27 @@ struct MovedBlock {
         set_status(p.status, CSA2_DEV_BAD_PAGE);
         continue;
       }
-      const int64_t row = kv8_row(s, page, h, in_page);
-      code[i] = *reinterpret_cast<const uint4*>(s.codes[side] + row * D + ch);
-      scale[i] = s.scales[side][kv8_block(s, page, h, in_page)];
-      if (side == 0) mass[i] = s.mass[row];
-    }
+      const int64_t row = kv8_row(s, page, h, in_page), at = kv8_block(s, page, h, in_page);
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-      const uint32_t mx = max(max(kv8_max4<FMT>(code[i].x), kv8_max4<FMT>(code[i].y)),
-                              max(kv8_max4<FMT>(code[i].z), kv8_max4<FMT>(code[i].w)));
-      big = fmaxf(big, kv8_mag<FMT>(mx) * scale[i]);
+      for (int side = 0; side < 2; ++side) {
+        code[side][i] = *reinterpret_cast<const uint4*>(s.codes[side] + row * D + ch);
+        scale[side][i] = s.scales[side][at];
+      }
+      mass[i] = s.mass[row];
     }
     moved = __syncthreads_or(other);
-    // magnitudes compare as their bits do
-    amax = __uint_as_float(group_max<kMoveThreads>(__float_as_uint(big), red, threadIdx.x));
+    if (!moved) return;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      float big = 0.0f;
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i)
+        big = fmaxf(big, kv8_mag<FMT>(kv8_max16<FMT>(code[side][i])) * scale[side][i]);
+      // magnitudes compare as their bits do
+      amax[side] = __uint_as_float(group_max<kMoveThreads>(__float_as_uint(big), red, threadIdx.x));
+    }
   }
-  __device__ __forceinline__ void write(const EvictParams& p, int b, int h, int side, int blk) {
+  __device__ __forceinline__ void write(const EvictParams& p, int b, int h, int blk) {
     const Kv8& d = p.dst;
     int din;
     const int page = kv8_page(d, b, blk << d.block_shift, din);
@@ -503,57 +548,61 @@ struct MovedBlock {
       if (threadIdx.x == 0) set_status(p.status, CSA2_DEV_BAD_PAGE);
       return;
     }
-    const int64_t drow = kv8_row(d, page, h, din);
+    const int64_t drow = kv8_row(d, page, h, din), at = kv8_block(d, page, h, din);
     const int sub = threadIdx.x / kLanes, ch = (threadIdx.x % kLanes) * 16;
-    const float s1 = kv8_scale_of<FMT>(amax), inv = kv8_inverse(s1);
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-      const int r = i * kRows + sub;
-      if (r >= rows) continue;
-      uint4 w = code[i];
-      const float ratio = scale[i] * inv;
-      if (moved && ratio != 1.0f) {
-        w.x = kv8_recode<FMT>(w.x, ratio);
-        w.y = kv8_recode<FMT>(w.y, ratio);
-        w.z = kv8_recode<FMT>(w.z, ratio);
-        w.w = kv8_recode<FMT>(w.w, ratio);
+    for (int side = 0; side < 2; ++side) {
+      const float s1 = moved ? kv8_scale_of<FMT>(amax[side]) : 0.0f, inv = kv8_inverse(s1);
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) {
+        const int r = i * kRows + sub;
+        if (r >= rows) continue;
+        uint4 w = code[side][i];
+        const float f = scale[side][i] * inv;
+        if (moved && f != 1.0f) {
+          // beyond f16's range (E4M3: rows of the smallest codes alone) in two
+          // steps, the first of which is exact
+          const bool far = f > 32768.0f;
+          if (far) w = recode16<FMT>(w, kv8_ratio(32768.0f));
+          w = recode16<FMT>(w, kv8_ratio(far ? f * 0x1p-15f : f));
+        }
+        *reinterpret_cast<uint4*>(d.codes[side] + (drow + r) * D + ch) = w;
+        if (side == 0 && ch == 0 && d.mass) d.mass[drow + r] = mass[i];
+        if (r == 0 && ch == 0) d.scales[side][at] = moved ? s1 : scale[side][i];
       }
-      *reinterpret_cast<uint4*>(d.codes[side] + (drow + r) * D + ch) = w;
-      if (side == 0 && ch == 0 && d.mass) d.mass[drow + r] = mass[i];
-      if (r == 0 && ch == 0) d.scales[side][kv8_block(d, page, h, din)] = moved ? s1 : scale[i];
     }
   }
 };
 
-// Into another cache: one CTA per (block, side, head, sequence).  In place: a
-// cluster per (side, head, sequence) walks the blocks upwards, one block a CTA
-// and round; it reads a round's rows, meets at the cluster's barrier, and writes
-// them.  A kept row never moves to a later place, so the sources of the rounds
-// still to come lie behind the rows being written.
+// Into another cache: one CTA per (block, head, sequence).  In place: a cluster
+// per (head, sequence) walks the blocks upwards, one block a CTA and round; it
+// reads a round's rows, meets at the cluster's barrier, and writes them.  A kept
+// row never moves to a later place, so the sources of the rounds still to come
+// lie behind the rows being written.
 template <int D, int FMT, int PASSES, bool PLACE>
 __global__ void __launch_bounds__(kMoveThreads) kv8_evict_move_kernel(EvictParams p) {
   __shared__ uint32_t red[kMoveThreads / 32];
   griddep_wait();
   griddep_launch_dependents();
-  const int h = blockIdx.y >> 1, side = blockIdx.y & 1, b = blockIdx.z;
+  const int h = blockIdx.y, b = blockIdx.z;
   const int n = p.old_len[b], m = min(n, p.keep);
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.dst.seq_len[b] = m;
+  if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) p.dst.seq_len[b] = m;
   const int32_t* kept = p.kept + ((int64_t)b * p.src.heads + h) * p.keep;
   const int blocks = (m + (1 << p.dst.block_shift) - 1) >> p.dst.block_shift;
   MovedBlock<D, FMT, PASSES> x;
   if (!PLACE) {
     if ((int)blockIdx.x >= blocks) return;
-    x.read(p, b, h, side, blockIdx.x, m, kept, red);
-    x.write(p, b, h, side, blockIdx.x);
+    x.read(p, b, h, blockIdx.x, m, kept, red);
+    x.write(p, b, h, blockIdx.x);
     return;
   }
   if (n == m) return;                              // uniform over the cluster
   for (int first = 0; first < blocks; first += kMoveCluster) {
     const int blk = first + (int)blockIdx.x;       // the cluster is the grid's x
     const bool mine = blk < blocks;
-    if (mine) x.read(p, b, h, side, blk, m, kept, red);
+    if (mine) x.read(p, b, h, blk, m, kept, red);
     cluster_sync();
-    if (mine && x.moved) x.write(p, b, h, side, blk);
+    if (mine && x.moved) x.write(p, b, h, blk);
   }
 }
 
@@ -577,7 +626,7 @@ cudaError_t launch_cluster(void (*kern)(A...), dim3 grid, int threads, int clust
 template <int D, int FMT, int PASSES>
 cudaError_t move_as(const EvictParams& p, cudaStream_t s) {
   const int blocks = (p.keep + (1 << p.dst.block_shift) - 1) >> p.dst.block_shift;
-  const dim3 grid(p.in_place ? kMoveCluster : blocks, 2 * p.src.heads, p.src.batch);
+  const dim3 grid(p.in_place ? kMoveCluster : blocks, p.src.heads, p.src.batch);
   return p.in_place ? launch_cluster(kv8_evict_move_kernel<D, FMT, PASSES, true>, grid, kMoveThreads,
                                      kMoveCluster, s, p)
                     : kv8_launch(kv8_evict_move_kernel<D, FMT, PASSES, false>, grid, kMoveThreads, 0,
@@ -599,7 +648,9 @@ cudaError_t launch_kv8_append(const Kv8& c, int D, const Kv8Rows& k, const Kv8Ro
                               const int32_t* new_len, const int32_t* start, uint32_t* status,
                               cudaStream_t s) {
   AppendParams p{c, {k, v}, T, new_len, start, status, 0};
-  return D == 64 ? append_of<64>(p, s) : append_of<128>(p, s);
+  if (c.format == CSA2_KV8_E4M3)
+    return D == 64 ? append_of<64, CSA2_KV8_E4M3>(p, s) : append_of<128, CSA2_KV8_E4M3>(p, s);
+  return D == 64 ? append_of<64, CSA2_KV8_INT8>(p, s) : append_of<128, CSA2_KV8_INT8>(p, s);
 }
 
 cudaError_t launch_kv8_evict(const Kv8& src, const Kv8& dst, bool in_place, int D, int keep,

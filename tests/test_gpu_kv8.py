@@ -419,6 +419,27 @@ def test_evict(i, fmt, into):
         d.untouched_behind(lens2)
 
 
+@pytest.mark.parametrize("fmt", [O.E4M3, O.INT8])
+def test_evict_of_rows_far_below_their_block(fmt):
+    """The rows that stay hold the smallest codes only: their blocks' new scales
+    are up to 2^17 below the old ones; and blocks of zeros."""
+    for small in (2.0 ** -6, 2.0 ** -16, 2.0 ** -17, 1.5 * 2.0 ** -18, 0.0):
+        p = Pair(1, 2, 64, 64, 32, 32, fmt, seed=72)
+        ws = p.c.workspace(1, 2)
+        k, v = (torch.sign(p.rows(64, 2, "f32")) * 448.0 for _ in "kv")
+        k[:, 1::2] *= small
+        v[:, 1::2] *= small
+        p.append(k, v, ws)
+        p.set_mass([[np.tile([0.0, 1.0], 32)] * 2])
+        kept = torch.empty(1, 2, 32, dtype=torch.int32, device="cuda")
+        K.kv8_evict(p.c, 32, 0, 0, kept, ws)
+        for h in range(2):
+            for s in "kv":
+                p.seq[0, h, s] = p.seq[0, h, s].keep(np.arange(1, 64, 2))
+        p.len = [32]
+        p.check()
+
+
 def test_evict_of_a_sequence_with_a_bad_page():
     p = filled(1, 1, 64, [100], 16, 16, O.E4M3, seed=71)
     ws = p.c.workspace(1, 1)
