@@ -232,13 +232,11 @@ __device__ __forceinline__ int64_t kv8_total(const Kv8& c, int lane) {
 __device__ __forceinline__ int kv8_sharers(int64_t total, int ctas) {
   return total < ctas ? (int)total : ctas;
 }
-// Steps in front of sequence b (of one unit each).
-__device__ __forceinline__ int64_t kv8_before(const Kv8& c, int lane, int b) {
-  int64_t s = 0;
-  for (int i = lane; i < b; i += 32) s += kv8_steps(c, i);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
+// a * b / d (in 32 bits where they do: a 64-bit division is a long sequence)
+__device__ __forceinline__ int64_t kv8_muldiv(int64_t a, int64_t b, int64_t d) {
+  const int64_t y = a * b;
+  if (y < (int64_t)1 << 32 && d < (int64_t)1 << 32) return (uint32_t)y / (uint32_t)d;
+  return y / d;
 }
 // The sequence that holds step x when each has `units` units, and the step of
 // its first unit (whole warp; x below the total).
@@ -262,6 +260,77 @@ __device__ __forceinline__ int kv8_find(const Kv8& c, int lane, int units, int64
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
   }
+}
+
+// CTA `cta`'s first and last step, and where the first one lies.
+struct Kv8Share {
+  int ctas;               // CTAs that take part
+  int64_t x, x1;          // steps [x, x1)
+  int b, n, steps;        // the first step's sequence, its length and steps of a unit
+  int unit, step;         // and the unit and its step
+};
+__device__ __forceinline__ Kv8Share kv8_share(const Kv8& c, int lane, int units, int max_ctas,
+                                              int cta) {
+  Kv8Share r;
+  int64_t first;
+  if (c.batch <= 32) {    // one look at the lengths
+    const int n = lane < c.batch ? kv8_len(c, lane) : 0;
+    const int mine = lane < c.batch ? (n <= kKv8Step ? 1 : (n + kKv8Step - 1) / kKv8Step) : 0;
+    int incl = mine;      // at most 32 * 2^14 steps
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const int64_t total = (int64_t)__shfl_sync(0xffffffffu, incl, 31) * units;
+    r.ctas = kv8_sharers(total, max_ctas);
+    r.x = kv8_muldiv(total, cta, r.ctas);
+    r.x1 = kv8_muldiv(total, cta + 1, r.ctas);
+    const uint32_t hit = __ballot_sync(0xffffffffu, (int64_t)incl * units > r.x);
+    r.b = hit ? __ffs(hit) - 1 : c.batch - 1;
+    first = (int64_t)__shfl_sync(0xffffffffu, incl - mine, r.b) * units;
+    r.n = __shfl_sync(0xffffffffu, n, r.b);
+    r.steps = __shfl_sync(0xffffffffu, mine, r.b);
+  } else {
+    const int64_t total = kv8_total(c, lane) * units;
+    r.ctas = kv8_sharers(total, max_ctas);
+    r.x = kv8_muldiv(total, cta, r.ctas);
+    r.x1 = kv8_muldiv(total, cta + 1, r.ctas);
+    r.b = kv8_find(c, lane, units, r.x < total ? r.x : total - 1, first);
+    r.n = kv8_len(c, r.b);
+    r.steps = kv8_steps(c, r.b);
+  }
+  r.unit = (int)kv8_muldiv(r.x - first, 1, r.steps);
+  r.step = (int)(r.x - first - (int64_t)r.unit * r.steps);
+  return r;
+}
+// The CTAs c0 .. c1 that share unit `unit` of sequence b.
+__device__ __forceinline__ void kv8_sharers_of(const Kv8& c, int lane, int units, int max_ctas,
+                                               int b, int unit, int& c0, int& c1) {
+  int64_t all = 0, before = 0;
+  int steps = 0;
+  for (int i = lane; i < c.batch; i += 32) {
+    const int s = kv8_steps(c, i);
+    all += s;
+    if (i < b) before += s;
+    if (i == b) steps = s;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    steps += __shfl_xor_sync(0xffffffffu, steps, o);
+  }
+  const int64_t total = all * units, x0 = before * units + (int64_t)unit * steps;
+  const int ctas = kv8_sharers(total, max_ctas);
+  // CTA i has the steps from total i / ctas on: step x is that of the last i
+  // with total i < (x + 1) ctas
+  c0 = (int)((((x0 + 1) * ctas - 1) < (int64_t)1 << 32 && total < (int64_t)1 << 32)
+                 ? (uint32_t)((x0 + 1) * ctas - 1) / (uint32_t)total
+                 : ((x0 + 1) * ctas - 1) / total);
+  const int64_t e = (x0 + steps) * ctas - 1;
+  c1 = (int)((e < (int64_t)1 << 32 && total < (int64_t)1 << 32) ? (uint32_t)e / (uint32_t)total
+                                                                : e / total);
 }
 
 // ------------------------------------------------------------------ launchers

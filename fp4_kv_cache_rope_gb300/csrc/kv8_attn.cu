@@ -233,17 +233,15 @@ __global__ void __launch_bounds__(32 * WARPS, decode_ctas(D, NT, WARPS))
     st0 = 0;
     x1 = steps;
   } else {
-    const int64_t total = kv8_total(c, lane) * units;
-    const int ctas = kv8_sharers(total, p.ctas);
-    if ((int)blockIdx.x >= ctas) return;
-    x = total * blockIdx.x / ctas;
-    x1 = total * (blockIdx.x + 1) / ctas;
-    int64_t first;
-    b = kv8_find(c, lane, units, x, first);
-    n = kv8_len(c, b);
-    steps = kv8_steps(c, b);
-    unit = (int)((x - first) / steps);
-    st0 = (int)((x - first) % steps);
+    const Kv8Share at = kv8_share(c, lane, units, p.ctas, blockIdx.x);
+    if ((int)blockIdx.x >= at.ctas) return;
+    x = at.x;
+    x1 = at.x1;
+    b = at.b;
+    n = at.n;
+    steps = at.steps;
+    unit = at.unit;
+    st0 = at.step;
   }
 
   // this lane's places in a stage: 16-byte chunk `lane + 32 i` of the tile's
@@ -591,11 +589,10 @@ __global__ void __launch_bounds__(32 * WARPS, decode_ctas(D, NT, WARPS))
 constexpr int kCombine = 4;
 template <int D>
 __global__ void __launch_bounds__(D / 4 * kCombine) kv8_combine_kernel(DecodeParams p, int tile_rows) {
-  constexpr int kThreadsC = D / 4 * kCombine;
   griddep_wait();
   griddep_launch_dependents();
   const Kv8& c = p.a.c;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int units = c.heads * p.tiles;
   const int b = blockIdx.x / units, unit = blockIdx.x % units, row = blockIdx.y;
   const int h = unit / p.tiles, gr = (unit % p.tiles) * tile_rows + row;
@@ -603,63 +600,43 @@ __global__ void __launch_bounds__(D / 4 * kCombine) kv8_combine_kernel(DecodePar
   int ql = p.a.q_len ? p.a.q_len[b] : p.a.T;
   ql = ql < 0 ? 0 : (ql > p.a.T ? p.a.T : ql);
   if (gr >= p.rows || tok >= ql) return;
-  const int64_t total = kv8_total(c, lane) * units;
-  const int steps = kv8_steps(c, b);
-  const int64_t x0 = kv8_before(c, lane, b) * units + (int64_t)unit * steps, x1 = x0 + steps;
-  const int ctas = kv8_sharers(total, p.ctas);
-  const int c0 = (int)(((x0 + 1) * ctas - 1) / total), c1 = (int)((x1 * ctas - 1) / total);
+  int c0, c1;
+  kv8_sharers_of(c, lane, units, p.ctas, b, unit, c0, c1);
   if (c0 == c1) return;
-  // the unit began in CTA c0's second slot and went on in the others' first
-  __shared__ float w[kKv8Ctas], red[2][kThreadsC / 32];
-  __shared__ float4 sum[kCombine][D / 4];
+  // the unit began in CTA c0's second slot and went on in the others' first; each
+  // group joins its parts as they come, then the groups are joined
+  __shared__ float tops[kCombine], sums[kCombine];
+  __shared__ float4 outs[kCombine][D / 4];
   const int parts = c1 - c0 + 1;
-  auto slot = [&](int i) { return p.a.part + (2 * (int64_t)(c0 + i) + (i == 0)) * slot_floats(D); };
-  float top = -INFINITY;
-  for (int i = tid; i < parts; i += kThreadsC) {
-    w[i] = slot(i)[kKv8SlotRows * D + row];
-    top = fmaxf(top, w[i]);
-  }
-#pragma unroll
-  for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-  if (lane == 0) red[0][warp] = top;
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < kThreadsC / 32; ++k) top = fmaxf(top, red[0][k]);
-  float l = 0.0f;
-  for (int i = tid; i < parts; i += kThreadsC) {
-    const float pl = slot(i)[kKv8SlotRows * (D + 1) + row];
-    w[i] = pl == 0.0f ? 0.0f : kv8_exp2(w[i] - top);   // NaN sums stay NaN
-    l += pl == 0.0f ? 0.0f : pl * w[i];
-  }
-#pragma unroll
-  for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-  if (lane == 0) red[1][warp] = l;
-  __syncthreads();
   const int grp = tid / (D / 4), ch = tid % (D / 4);
+  float top = -INFINITY, l = 0.0f;
   float4 o = make_float4(0, 0, 0, 0);
+  auto join = [&](float m, float pl, const float4& y) {
+    const float nt = fmaxf(top, m);
+    // a sum of 0: the part saw no row; of NaN: the query holds one, and it stays
+    const float f = l == 0.0f ? 0.0f : kv8_exp2(top - nt), g = pl == 0.0f ? 0.0f : kv8_exp2(m - nt);
+    l = l * f + pl * g;
+    o.x = o.x * f + y.x * g;
+    o.y = o.y * f + y.y * g;
+    o.z = o.z * f + y.z * g;
+    o.w = o.w * f + y.w * g;
+    top = nt;
+  };
 #pragma unroll 4
   for (int i = grp; i < parts; i += kCombine) {
-    const float4 y = reinterpret_cast<const float4*>(slot(i) + row * D)[ch];
-    const float f = w[i];
-    o.x = fmaf(y.x, f, o.x);
-    o.y = fmaf(y.y, f, o.y);
-    o.z = fmaf(y.z, f, o.z);
-    o.w = fmaf(y.w, f, o.w);
+    const float* part = p.a.part + (2 * (int64_t)(c0 + i) + (i == 0)) * slot_floats(D);
+    join(part[kKv8SlotRows * D + row], part[kKv8SlotRows * (D + 1) + row],
+         reinterpret_cast<const float4*>(part + row * D)[ch]);
   }
-  sum[grp][ch] = o;
+  if (ch == 0) {
+    tops[grp] = top;
+    sums[grp] = l;
+  }
+  outs[grp][ch] = o;
   __syncthreads();
   if (grp > 0) return;
-  l = 0.0f;
 #pragma unroll
-  for (int k = 0; k < kThreadsC / 32; ++k) l += red[1][k];
-#pragma unroll
-  for (int k = 1; k < kCombine; ++k) {
-    const float4 y = sum[k][ch];
-    o.x += y.x;
-    o.y += y.y;
-    o.z += y.z;
-    o.w += y.w;
-  }
+  for (int k = 1; k < kCombine; ++k) join(tops[k], sums[k], outs[k][ch]);
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint16_t* out = static_cast<uint16_t*>(const_cast<void*>(p.a.out.data)) + b * p.a.out.sb +
                   tok * p.a.out.st + hd * p.a.out.sh + 4 * ch;
@@ -671,6 +648,9 @@ __global__ void __launch_bounds__(D / 4 * kCombine) kv8_combine_kernel(DecodePar
 }
 
 // ---------------------------------------------------------------------- mass
+// CTAs that an SM holds, by the registers of the query rows.
+constexpr int mass_ctas(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
+
 // mass_j = decay mass_j + sum over the query rows of 2^(c q k_j - lse), for up to
 // 8 NT query rows: their fragments stay in registers while a warp streams its
 // cached rows, the next tile's codes loaded while this one is worked on.  A
@@ -681,53 +661,55 @@ __global__ void __launch_bounds__(D / 4 * kCombine) kv8_combine_kernel(DecodePar
 // Both constants are held in two fp32 parts: at logits of 20 to 30 the rounding
 // of one part alone would be 1e-6 of the weight.
 template <int D, int NT, int FMT>
-__global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kv8_mass_kernel(DecodeParams p) {
+__global__ void __launch_bounds__(kThreads, mass_ctas(NT)) kv8_mass_kernel(DecodeParams p) {
   constexpr int kHalf = D / 64;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const Kv8& c = p.a.c;
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t total = kv8_total(c, lane) * c.heads;
-  const int ctas = kv8_sharers(total, p.ctas);
-  if ((int)blockIdx.x >= ctas) return;
-  int64_t x = total * blockIdx.x / ctas;
-  const int64_t x1 = total * (blockIdx.x + 1) / ctas;
-  int64_t first;
-  int b = kv8_find(c, lane, c.heads, x, first);
-  int n = kv8_len(c, b), steps = kv8_steps(c, b);
-  int h = (int)((x - first) / steps), st0 = (int)((x - first) % steps);
+  const Kv8Share first = kv8_share(c, lane, c.heads, p.ctas, blockIdx.x);
+  if ((int)blockIdx.x >= first.ctas) return;
+  int64_t x = first.x;
+  const int64_t x1 = first.x1;
+  int b = first.b, n = first.n, steps = first.steps, h = first.unit, st0 = first.step;
   while (x < x1) {
     const int st1 = (int)min((int64_t)steps, st0 + (x1 - x));
     int ql = p.a.q_len ? p.a.q_len[b] : p.a.T;
     ql = ql < 0 ? 0 : (ql > p.a.T ? p.a.T : ql);
 
-    Groups at;
+    // one tile's codes are on their way while another is worked on, and the page
+    // ids of one more
+    struct Tile {
+      Groups at;
+      uint4 raw[2][kHalf][2];   // rows 16 i + 8 r + g, 16-byte chunk 4 f + t
+      float ks[2];
+    };
+    Tile tile;
     int id;
     auto fetch = [&](int st) {
       id = fetch_page(c, b, st * kKv8Step + warp * kSub, st < st1 ? n : 0, lane);
     };
-    uint4 raw[2][kHalf][2];     // rows 16 i + 8 r + g, 16-byte chunk 4 f + t
-    float ks[2];
-    auto load = [&](int st) {
+    auto load = [&](Tile& x, int st) {
       const int pos = st * kKv8Step + warp * kSub;
-      at = place_groups(c, id, h, pos, p.a.status, lane);
+      x.at = place_groups(c, id, h, pos, p.a.status, lane);
       fetch(st + 1);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        ks[i] = at.row[i] >= 0 ? c.scales[0][at.blk[i]] : 0.0f;
+        x.ks[i] = 0.0f;
+        if (x.at.row[i] >= 0) x.ks[i] = c.scales[0][x.at.blk[i]];
 #pragma unroll
         for (int f = 0; f < kHalf; ++f)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            raw[i][f][r] = make_uint4(0, 0, 0, 0);
-            if (at.row[i] >= 0 && pos + 16 * i + 8 * r + g < n)
-              raw[i][f][r] = *reinterpret_cast<const uint4*>(
-                  c.codes[0] + (at.row[i] + 8 * r + g) * D + (4 * f + t) * 16);
+            x.raw[i][f][r] = make_uint4(0, 0, 0, 0);
+            if (x.at.row[i] >= 0 && pos + 16 * i + 8 * r + g < n)
+              x.raw[i][f][r] = *reinterpret_cast<const uint4*>(
+                  c.codes[0] + (x.at.row[i] + 8 * r + g) * D + (4 * f + t) * 16);
           }
       }
     };
     fetch(st0);
-    load(st0);
+    load(tile, st0);
 
     uint32_t qf[NT][D / 16][2];
     float mul[NT][2], ml[NT][2], l2[NT][2], ll[NT][2];
@@ -760,8 +742,8 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kv8_mass_kernel(Dec
 
     for (int st = st0; st < st1; ++st) {
       const int pos = st * kKv8Step + warp * kSub;
-      const Groups here = at;
-      const float kscale[2] = {ks[0], ks[1]};
+      const Groups here = tile.at;
+      const float kscale[2] = {tile.ks[0], tile.ks[1]};
       float s[NT][2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -769,8 +751,8 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kv8_mass_kernel(Dec
         for (int u = 0; u < NT; ++u) s[u][i][0] = s[u][i][1] = s[u][i][2] = s[u][i][3] = 0.0f;
 #pragma unroll
         for (int f = 0; f < kHalf; ++f) {
-          const uint32_t* xa = reinterpret_cast<const uint32_t*>(&raw[i][f][0]);
-          const uint32_t* xb = reinterpret_cast<const uint32_t*>(&raw[i][f][1]);
+          const uint32_t* xa = reinterpret_cast<const uint32_t*>(&tile.raw[i][f][0]);
+          const uint32_t* xb = reinterpret_cast<const uint32_t*>(&tile.raw[i][f][1]);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint32_t a[4];
@@ -781,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kv8_mass_kernel(Dec
           }
         }
       }
-      load(st + 1);
+      load(tile, st + 1);
       const bool some = pos + kSub > full;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -853,11 +835,17 @@ cudaError_t decode_of(DecodeParams p, int num_sms, cudaStream_t s) {
          : nt == 2 ? decode_as<D, 2, FMT>(p, num_sms, s)
                    : decode_as<D, 3, FMT>(p, num_sms, s);
 }
+template <int D, int NT, int FMT>
+cudaError_t mass_as(DecodeParams p, int num_sms, cudaStream_t s) {
+  const int ctas = mass_ctas(NT) * num_sms;
+  p.ctas = ctas < kKv8Ctas ? ctas : kKv8Ctas;
+  return kv8_launch(kv8_mass_kernel<D, NT, FMT>, dim3(p.ctas), kThreads, 0, s, p);
+}
 template <int D, int FMT>
-cudaError_t mass_of(const DecodeParams& p, cudaStream_t s) {
-  return p.rows <= 8    ? kv8_launch(kv8_mass_kernel<D, 1, FMT>, dim3(p.ctas), kThreads, 0, s, p)
-         : p.rows <= 16 ? kv8_launch(kv8_mass_kernel<D, 2, FMT>, dim3(p.ctas), kThreads, 0, s, p)
-                        : kv8_launch(kv8_mass_kernel<D, 4, FMT>, dim3(p.ctas), kThreads, 0, s, p);
+cudaError_t mass_of(const DecodeParams& p, int num_sms, cudaStream_t s) {
+  return p.rows <= 8    ? mass_as<D, 1, FMT>(p, num_sms, s)
+         : p.rows <= 16 ? mass_as<D, 2, FMT>(p, num_sms, s)
+                        : mass_as<D, 4, FMT>(p, num_sms, s);
 }
 
 }  // namespace
@@ -874,10 +862,12 @@ cudaError_t launch_kv8_attn(const Kv8Attn& a, int num_sms, cudaStream_t s) {
 }
 
 cudaError_t launch_kv8_mass_few(const Kv8Attn& a, int num_sms, cudaStream_t s) {
-  DecodeParams p{a, a.T * a.G, 1, 3 * num_sms < kKv8Ctas ? 3 * num_sms : kKv8Ctas};
+  const DecodeParams p{a, a.T * a.G, 1, 1};
   if (a.c.format == CSA2_KV8_E4M3)
-    return a.D == 64 ? mass_of<64, CSA2_KV8_E4M3>(p, s) : mass_of<128, CSA2_KV8_E4M3>(p, s);
-  return a.D == 64 ? mass_of<64, CSA2_KV8_INT8>(p, s) : mass_of<128, CSA2_KV8_INT8>(p, s);
+    return a.D == 64 ? mass_of<64, CSA2_KV8_E4M3>(p, num_sms, s)
+                     : mass_of<128, CSA2_KV8_E4M3>(p, num_sms, s);
+  return a.D == 64 ? mass_of<64, CSA2_KV8_INT8>(p, num_sms, s)
+                   : mass_of<128, CSA2_KV8_INT8>(p, num_sms, s);
 }
 
 }  // namespace csa2
