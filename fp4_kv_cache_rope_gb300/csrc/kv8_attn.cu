@@ -657,9 +657,10 @@ constexpr int mass_ctas(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
 // cached row belongs to one warp, so nothing is added atomically and the order
 // of the sum is fixed.
 //
-// The exponent is x = s f - lse2 with f = c log2(e) 2^e s_K and lse2 = lse log2(e).
-// Both constants are held in two fp32 parts: at logits of 20 to 30 the rounding
-// of one part alone would be 1e-6 of the weight.
+// The exponent is x = s f - hi with f = (1 - eps) c log2(e) 2^e s_K as rounded and
+// lse log2(e) = hi + lo; what the roundings leave goes into the factor
+// 2^(eps hi - lo) of the sum (but for eps x, nothing for the weights that count).
+// At logits of 20 to 30 it is 1e-6 of the weight.
 template <int D, int NT, int FMT>
 __global__ void __launch_bounds__(kThreads, mass_ctas(NT)) kv8_mass_kernel(DecodeParams p) {
   constexpr int kHalf = D / 64;
@@ -712,7 +713,8 @@ __global__ void __launch_bounds__(kThreads, mass_ctas(NT)) kv8_mass_kernel(Decod
     load(tile, st0);
 
     uint32_t qf[NT][D / 16][2];
-    float mul[NT][2], ml[NT][2], l2[NT][2], ll[NT][2];
+    float mul[NT][2], l2[NT][2], gain[NT][2];
+    const float eps = p.a.scale_low / p.a.scale_log2;
     int lim[NT][2], full = 0x7FFFFFFF;
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
@@ -725,16 +727,16 @@ __global__ void __launch_bounds__(kThreads, mass_ctas(NT)) kv8_mass_kernel(Decod
       if (y == -INFINITY) y = 0.0f;
       // a row without weight: a constant so large that every weight is 0
       const float hi = see ? y * 1.44269502f : INFINITY;
-      const float lo = see ? fmaf(y, 1.44269502f, -hi) + y * 1.92596299e-8f : 0.0f;
+      const float g2 =
+          see ? exp2f(eps * hi - (fmaf(y, 1.44269502f, -hi) + y * 1.92596299e-8f)) : 1.0f;
       if (see) full = min(full, see);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int from = 4 * (2 * t + e);
         const float fe = __shfl_sync(0xffffffffu, f, from);
         mul[u][e] = p.a.scale_log2 * fe;
-        ml[u][e] = p.a.scale_low * fe;
         l2[u][e] = __shfl_sync(0xffffffffu, hi, from);
-        ll[u][e] = __shfl_sync(0xffffffffu, lo, from);
+        gain[u][e] = __shfl_sync(0xffffffffu, g2, from);
         lim[u][e] = __shfl_sync(0xffffffffu, see, from);
       }
     }
@@ -776,9 +778,9 @@ __global__ void __launch_bounds__(kThreads, mass_ctas(NT)) kv8_mass_kernel(Decod
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const float z = s[u][i][2 * r + e] * kscale[i];       // exact: a power of two
-              float w = kv8_exp2(fmaf(z, mul[u][e], -l2[u][e]) + fmaf(z, ml[u][e], -ll[u][e]));
+              float w = kv8_exp2(fmaf(z, mul[u][e], -l2[u][e]));
               if (some && pos + row >= lim[u][e]) w = 0.0f;
-              sum += w;
+              sum = fmaf(w, gain[u][e], sum);
             }
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);

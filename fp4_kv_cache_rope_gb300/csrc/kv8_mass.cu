@@ -11,9 +11,11 @@
 // two is exact in both.  2 D flop per pair against one exponential: the tensor
 // cores and the issue slots of the eight exponential warps are about even.
 //
-// x = fma(s, f, -hi) with lse log2(e) = hi + lo in two fp32 parts and the second
-// part of f = c log2(e) in a second fma; lo enters as the factor 2^-lo of the
-// sum's fma.  With one part each the weights would be off by 1e-6.
+// x = fma(s, f, -hi) with lse log2(e) = hi + lo in two fp32 parts; f = c log2(e)
+// is rounded too, f = (1 - eps) true f.  What both leave, eps (x + hi) - lo, is
+// eps hi - lo but for eps x, which is nothing for the weights that count: it
+// enters as the factor 2^(eps hi - lo) of the sum's fma.  Without it the weights
+// would be off by 1e-6.
 //
 // A cached row is one thread's in each of four warp groups: even and odd query
 // tiles, left and right half of their columns.  Their four sums are added in a
@@ -41,7 +43,7 @@ struct MassSmem {
   static constexpr int kQSlab = kCols * 128;
   static constexpr int kK = 0;
   static constexpr int kQ = kSlabs * kKSlab;          // 2 stages
-  static constexpr int kConst = kQ + 2 * kSlabs * kQSlab;   // [4][-hi, 2^-lo][256]
+  static constexpr int kConst = kQ + 2 * kSlabs * kQSlab;   // [4][-hi, 2^(eps hi - lo)][256]
   static constexpr int kSum = kConst + 4 * 2 * kCols * 4;   // [2][3][128]
   static constexpr int kBars = kSum + 2 * 3 * kKeys * 4;
   static constexpr int kFlags = kBars + 128;          // abort, tmem, K's reference scale [4]
@@ -150,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
       // query rows below this one do not see the thread's cached row
       const int64_t see = (int64_t)(it.key0 + key - (it.n - it.ql)) * p.a.G;
       bool got = false;
-      float f = 0.0f, fl = 0.0f;
+      float f = 0.0f;
       for (int i = 0; i < it.nt; ++i, ++q) {
         if ((q & 1) != (uint32_t)buf) continue;
         wait(s_full + buf, (q >> 1) & 1);
@@ -161,11 +163,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
           // (the tile after next is not written before this warp group's next
           // query tile is done with, so four slots are enough)
           f = p.a.scale_log2 * refs[k & 3];
-          fl = p.a.scale_low * refs[k & 3];
         }
         const float* cst = reinterpret_cast<const float*>(smem + L::kConst) + 2 * kCols * (q & 3) +
                            kCols / 2 * half;
-        const uint64_t f2 = pack2(f, f), fl2 = pack2(fl, fl);
+        const uint64_t f2 = pack2(f, f);
         const int64_t hid64 = see - (int64_t)(it.first + i) * kCols - kCols / 2 * half;
         const int hidden = hid64 < 0 ? 0 : (hid64 > kCols ? kCols : (int)hid64);
         auto add = [&](auto masked, int u) {
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
             for (int e = 0; e < 2; ++e) {
               const uint64_t s2 = pack2(__uint_as_float(s[j + 2 * e]), __uint_as_float(s[j + 2 * e + 1]));
               float x, y;
-              unpack2(fma2(s2, fl2, fma2(s2, f2, hh[e])), x, y);
+              unpack2(fma2(s2, f2, hh[e]), x, y);
               x = kv8_exp2(x);
               y = kv8_exp2(y);
               if (decltype(masked)::value) {
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
 #pragma unroll 1
           for (int u = 0; u < kCols / 64; ++u) add(std::true_type{}, u);
         } else {
-#pragma unroll 1
+#pragma unroll
           for (int u = 0; u < kCols / 64; ++u) add(std::false_type{}, u);
         }
         tc_fence_before();
@@ -242,6 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
     // ============================================================ loading warps
     const int ct = tid - 32 * kExpWarps;
     const bool bf16 = p.a.q.type == CSA2_BF16;
+    const float eps = p.a.scale_low / p.a.scale_log2;
     for (int64_t id; (id = item_id(round)) >= 0; ++round) {
       const Item it = item_of(p, lane, id);
       if (it.nt == 0) continue;
@@ -354,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
             if (y != -INFINITY) {
               const float hi = y * 1.44269502f;
               nh = -hi;
-              g = exp2f(-(fmaf(y, 1.44269502f, -hi) + y * 1.92596299e-8f));
+              g = exp2f(eps * hi - (fmaf(y, 1.44269502f, -hi) + y * 1.92596299e-8f));
             }
           }
           cst[ct + 128 * v] = nh;
