@@ -539,8 +539,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
         id = fetch(i + 3);
       }
     }
-    // (there is no K behind the last tile's V)
-    if (!side && nt > 0 && ok && lane == 0) mbar_arrive(kv_full + ((nt - 1) & 1));
+    // There is no K behind the last tile's V, but its arrival is counted: when a
+    // tile nt would be converted, so that it cannot fall into an earlier phase.
+    if (!side && nt > 0) {
+      if (nt >= 2) wait(s_full + 2 * (mts - 1) + (nt & 1), ((nt - 2) >> 1) & 1);
+      if (ok && lane == 0) mbar_arrive(kv_full + ((nt - 1) & 1));
+    }
   } else {
     // ================================================================ MMA thread
     regs_dec<kRegsMma>();
