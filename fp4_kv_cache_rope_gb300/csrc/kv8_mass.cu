@@ -11,11 +11,11 @@
 // two is exact in both.  2 D flop per pair against one exponential: the tensor
 // cores and the issue slots of the eight exponential warps are about even.
 //
-// x = fma(s, f, -hi) with lse log2(e) = hi + lo in two fp32 parts; f = c log2(e)
-// is rounded too, f = (1 - eps) true f.  What both leave, eps (x + hi) - lo, is
-// eps hi - lo but for eps x, which is nothing for the weights that count: it
-// enters as the factor 2^(eps hi - lo) of the sum's fma.  Without it the weights
-// would be off by 1e-6.
+// x = fma(s, f, -a) with a fp32 constant per query.  f = c log2(e) is rounded,
+// f = (1 - eps) true f: with a = (1 - eps) lse log2(e), rounded once, what is left
+// is eps x, nothing for the weights that count.  (As two constants, -a and a
+// factor of the sum for a's own rounding, 3e-7 of a weight at lse 14, the shared
+// memory reads cost 7%.)
 //
 // A cached row is one thread's in each of four warp groups: even and odd query
 // tiles, left and right half of their columns.  Their four sums are added in a
@@ -43,8 +43,8 @@ struct MassSmem {
   static constexpr int kQSlab = kCols * 128;
   static constexpr int kK = 0;
   static constexpr int kQ = kSlabs * kKSlab;          // 2 stages
-  static constexpr int kConst = kQ + 2 * kSlabs * kQSlab;   // [4][-hi, 2^(eps hi - lo)][256]
-  static constexpr int kSum = kConst + 4 * 2 * kCols * 4;   // [2][3][128]
+  static constexpr int kConst = kQ + 2 * kSlabs * kQSlab;   // [4][256] -a
+  static constexpr int kSum = kConst + 4 * kCols * 4;   // [2][3][128]
   static constexpr int kBars = kSum + 2 * 3 * kKeys * 4;
   static constexpr int kFlags = kBars + 128;          // abort, tmem, K's reference scale [4]
   // tensor memory holds one CTA, so a second is kept off the SM
@@ -164,8 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
           // query tile is done with, so four slots are enough)
           f = p.a.scale_log2 * refs[k & 3];
         }
-        const float* cst = reinterpret_cast<const float*>(smem + L::kConst) + 2 * kCols * (q & 3) +
-                           kCols / 2 * half;
+        const float* cst = reinterpret_cast<const float*>(smem + L::kConst) + kCols * (q & 3) + kCols / 2 * half;
         const uint64_t f2 = pack2(f, f);
         const int64_t hid64 = see - (int64_t)(it.first + i) * kCols - kCols / 2 * half;
         const int hidden = hid64 < 0 ? 0 : (hid64 > kCols ? kCols : (int)hid64);
@@ -177,9 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
             const float4 h = *reinterpret_cast<const float4*>(cst + 32 * u + j);
-            const float4 g = *reinterpret_cast<const float4*>(cst + kCols + 32 * u + j);
             const uint64_t hh[2] = {pack2(h.x, h.y), pack2(h.z, h.w)};
-            const uint64_t gg[2] = {pack2(g.x, g.y), pack2(g.z, g.w)};
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const uint64_t s2 = pack2(__uint_as_float(s[j + 2 * e]), __uint_as_float(s[j + 2 * e + 1]));
@@ -191,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
                 if (32 * u + j + 2 * e < hidden) x = 0.0f;
                 if (32 * u + j + 2 * e + 1 < hidden) y = 0.0f;
               }
-              acc[e] = fma2(pack2(x, y), gg[e], acc[e]);
+              acc[e] = add2(pack2(x, y), acc[e]);
             }
           }
         };
@@ -347,20 +344,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
           step(pq, 16, g16, q_by, q_wrap);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        float* cst = reinterpret_cast<float*>(smem + L::kConst) + 2 * kCols * (q & 3);
+        float* cst = reinterpret_cast<float*>(smem + L::kConst) + kCols * (q & 3);
 #pragma unroll
         for (int v = 0; v < kCols / 128; ++v) {
-          float nh = -INFINITY, g = 1.0f;       // no weight
+          float a = INFINITY;                   // no weight
           if (pl.r < it.rows) {
             const float y = lsrc[pl.off];
             if (y != -INFINITY) {
               const float hi = y * 1.44269502f;
-              nh = -hi;
-              g = exp2f(eps * hi - (fmaf(y, 1.44269502f, -hi) + y * 1.92596299e-8f));
+              a = hi + (fmaf(y, 1.44269502f, -hi) + y * 1.92596299e-8f - eps * hi);
             }
           }
-          cst[ct + 128 * v] = nh;
-          cst[kCols + ct + 128 * v] = g;
+          cst[ct + 128 * v] = -a;
           step(pl, 128, g128, l_by, l_wrap);
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
