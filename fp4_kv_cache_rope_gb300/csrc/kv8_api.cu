@@ -90,6 +90,11 @@ csa2_status done(cudaError_t e) {
   return CSA2_ERR_CUDA;
 }
 
+bool overlap(const int32_t* a, const int32_t* b, int64_t n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && x < y + 4 * n && y < x + 4 * n;
+}
+
 struct Kv8Ws {
   size_t status, old_len, part, total;
 };
@@ -141,6 +146,10 @@ csa2_status csa2_kv8_append(const csa2_kv8_cache* cache, const csa2_rows* k, con
   if (!kv8_ok(cache) || !ws || !aligned(ws, 256) || T < 0 || T > CSA2_MAX_LEN)
     return CSA2_ERR_INVALID;
   if (!aligned(new_len, 4) || !aligned(start, 4)) return CSA2_ERR_INVALID;
+  // seq_len is written while these are read
+  if (overlap(new_len, cache->seq_len, cache->batch) ||
+      (start != cache->seq_len && overlap(start, cache->seq_len, cache->batch)))
+    return CSA2_ERR_INVALID;
   if (T == 0 && !start) return CSA2_OK;
   if (T > 0 && (!rows_ok(k, true) || !rows_ok(v, true) || k->type != v->type))
     return CSA2_ERR_INVALID;

@@ -84,6 +84,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Kv8& c = p.a.c;
+  griddep_wait();
+  griddep_launch_dependents();
   if ((smem_u32(smem) & 1023u) != 0) {
     if (tid == 0) set_status(p.a.status, CSA2_DEV_BAD_ALIGN);
     return;
@@ -118,8 +120,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
   }
   if (warp == kExpWarps + 4) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
-  griddep_wait();
-  griddep_launch_dependents();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;

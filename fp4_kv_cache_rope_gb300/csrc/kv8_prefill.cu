@@ -73,6 +73,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Kv8& c = p.a.c;
+  // (waits first: a later kernel of the stream takes this one's end for that of
+  // the kernels before it, too)
+  griddep_wait();
+  griddep_launch_dependents();
   if ((smem_u32(smem) & 1023u) != 0) {
     if (tid == 0) set_status(p.a.status, CSA2_DEV_BAD_ALIGN);
     return;
@@ -90,8 +94,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
   volatile float* red = reinterpret_cast<volatile float*>(smem + L::kFlags + 32);   // [K, V][4]
   volatile float* refs = red + 8;    // [K, V] largest scale in the CTA's range
 
-  griddep_wait();
-  griddep_launch_dependents();
 
   // ---- this CTA's share: heads fastest, then key splits, sequences, row tiles
   // (the last rows, which see the most keys, first)

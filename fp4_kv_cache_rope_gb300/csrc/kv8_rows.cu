@@ -286,7 +286,8 @@ cudaError_t append_as(const AppendParams& p0, cudaStream_t s) {
   }
   const int block = 1 << p.c.block_shift;
   // with `start` given nothing in the launch reads seq_len, so it may write it
-  p.own_len = p.start != nullptr;
+  // (`start` may be seq_len itself)
+  p.own_len = p.start != nullptr && p.start != p.c.seq_len;
   auto run = [&](auto kern, int passes) {
     const dim3 grid((p.T + block - 2) / block + 1, p.c.heads * (append_sides(passes) == 2 ? 1 : 2),
                     p.c.batch);

@@ -410,7 +410,8 @@ size_t csa2_kv8_workspace_size(const csa2_kv8_cache *cache, int32_t T, int32_t H
  * positions start[b] + i (device int32 [B]; NULL: seq_len[b]); afterwards
  * seq_len[b] = start[b] + new_len[b].  A start below seq_len[b] drops the rows
  * from there on (proposed tokens that were refused); the rows in front of
- * start must be held.
+ * start must be held.  start may be seq_len itself; otherwise neither it nor
+ * new_len overlaps seq_len.
  * A block that begins with the append takes the scale of its new rows.  A
  * block with earlier rows takes the larger of its scale and that of the new
  * rows; when that raises it, the earlier rows' codes become the format's
@@ -459,7 +460,7 @@ csa2_status csa2_kv8_mass(const csa2_kv8_cache *cache, const csa2_rows *q, int32
  * row; NaN counts as the largest, a row on a bad page as the smallest);
  * sink + recent <= keep.  kept (int32
  * [B, Hkv, keep]) gets the rows' former positions, -1 behind them.
- * dst NULL: in place, seq_len[b] becomes keep; sequences with at most `keep`
+ * dst NULL: in place (keep <= max_len), seq_len[b] becomes keep; sequences with at most `keep`
  * rows are not touched.  Otherwise the rows go to dst, another cache of the
  * same batch, kv_heads, dim, block and format with max_len >= keep, whose
  * seq_len becomes min(seq_len, keep); it may lie in the same pool but shares no

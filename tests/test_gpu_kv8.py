@@ -67,6 +67,21 @@ def test_append_at_a_start_drops_what_was_behind(fmt):
         p.check()
 
 
+@pytest.mark.parametrize("T", [3, 90])
+def test_append_with_seq_len_as_start(T):
+    p = Pair(3, 5, 64, 400, 16, 16, O.E4M3, seed=8)
+    ws = p.c.workspace(1, 5)
+    for step in range(3):
+        k, v = p.rows(T, 5, "f16"), p.rows(T, 5, "f16")
+        K.kv8_append(p.c, k.cuda(), v.cuda(), ws, start=p.c.seq_len)
+        for b in range(3):
+            for h in range(5):
+                for s, x in (("k", k), ("v", v)):
+                    p.seq[b, h, s].append(x[b, :, h].double().numpy())
+            p.len[b] += T
+        p.check()
+
+
 @pytest.mark.parametrize("T", [2, 60])
 def test_append_values_at_the_edges(T):
     for fmt in (O.E4M3, O.INT8):
@@ -326,6 +341,92 @@ def test_attention_strided_tensors_and_streams():
         assert torch.equal(a, b)
         K.kv8_attn(p.c, q, b.zero_(), ws)              # and the same bits again
         assert torch.equal(a, b)
+
+
+def test_a_short_wait_limit_ends_in_a_status_or_the_right_result():
+    """With a limit of 1 ns every on-chip wait gives up that is not over when the
+    hardware's own suspension of it ends.  A call then reports it, or, where none
+    did, its result is the right one; the next calls are right either way."""
+    p = filled(2, 2, 128, [2000, 900], 64, 64, O.E4M3, seed=55)
+    q = p.rows(600, 8, "bf16", 0.7)
+    qd, lse = run_attention(p, q, 4)
+    ws = p.c.workspace(600, 8)
+    out, again = torch.empty_like(qd), torch.empty_like(qd)
+    K.kv8_attn(p.c, qd, out, ws)
+    K.kv8_mass(p.c, qd, lse, ws, decay=0.0)
+    mass = p.c.mass.clone()
+    for call, got, want in ((lambda: K.kv8_attn(p.c, qd, again, ws), again, out),
+                            (lambda: K.kv8_mass(p.c, qd, lse, ws, decay=0.0), p.c.mass, mass)):
+        try:
+            K.set_wait_limit(1)
+            call()
+            torch.cuda.synchronize()
+        finally:
+            K.set_wait_limit(0)
+        status = K.get_status(ws)
+        assert status in (0, K.DEV_TIMEOUT)
+        assert status or torch.equal(got.nan_to_num(7.0), want.nan_to_num(7.0))
+        K.reset_status(ws)
+    qd, lse = run_attention(p, q, 4)
+    check_mass(p, q, qd, lse, 4, None)
+
+
+@pytest.mark.parametrize("T", [1, 6, 90])
+def test_captured_and_replayed(T):
+    """A graph of all operators, captured before any of them ran on these shapes,
+    replayed on new inputs in the same buffers, two graphs on one workspace."""
+    G, Hkv, D = 3, 3, 64
+    for fmt in (O.E4M3, O.INT8):
+        a, b = (Pair(2, Hkv, D, 512, 32, 32, fmt, seed=56 + i) for i in range(2))
+        ws = a.c.workspace(T, G * Hkv)
+        runs = []
+        for p in (a, b):
+            x = {n: torch.zeros(2, T, h, D, dtype=torch.float16, device="cuda")
+                 for n, h in (("k", Hkv), ("v", Hkv), ("q", G * Hkv), ("o", G * Hkv))}
+            x["lse"] = torch.zeros(2, T, G * Hkv, device="cuda")
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                K.kv8_append(p.c, x["k"], x["v"], ws)
+                K.kv8_attn(p.c, x["q"], x["o"], ws, lse=x["lse"])
+                K.kv8_mass(p.c, x["q"], x["lse"], ws, decay=0.0)
+            runs.append((p, g, x))
+        for _ in range(3):
+            ins = []
+            for p, g, x in runs:
+                new = {n: p.rows(T, x[n].shape[2], "f16", 0.7) for n in "kvq"}
+                for n in "kvq":
+                    x[n].copy_(new[n])
+                ins.append(new)
+                g.replay()
+            torch.cuda.synchronize()
+            for (p, g, x), new in zip(runs, ins):
+                for bb in range(2):
+                    for h in range(Hkv):
+                        for s in "kv":
+                            p.seq[bb, h, s].append(new[s][bb, :, h].double().numpy())
+                    p.len[bb] += T
+                p.check()
+                for bb in range(2):
+                    for h in range(Hkv):
+                        hs = slice(h * G, (h + 1) * G)
+                        ro, rl, tol, _ = attention_bounds(new["q"][bb, :, hs].double().numpy(), p, bb,
+                                                          h, G, T, 1 / math.sqrt(D), HALF["f16"])
+                        assert (np.abs(x["o"][bb, :, hs].cpu().double().numpy() - ro) <= tol).all()
+                        m = p.at("mass", bb, h)[: p.len[bb]]
+                        assert abs(m.sum() - T * G) < 1e-4 * T * G
+        assert K.get_status(ws) == 0
+
+
+def test_output_over_the_queries():
+    """out may be q: rows are read before they are written."""
+    p = filled(2, 2, 64, [3000, 700], 64, 64, O.E4M3, seed=57)
+    for T in (1, 7, 40, 200):
+        q = p.rows(T, 8, "bf16").cuda()
+        ws = p.c.workspace(T, 8)
+        out = torch.empty_like(q)
+        K.kv8_attn(p.c, q, out, ws)
+        K.kv8_attn(p.c, q, q, ws)
+        assert torch.equal(q, out)
 
 
 def test_a_page_shared_by_two_sequences():

@@ -157,6 +157,8 @@ def test_calls_refuse_before_any_launch():
         K._kv8_append(cp, ok, ok, 4, None, None, None, None),
         K._kv8_append(cp, ok, ok, 4, None, None, 264, None),
         K._kv8_append(cp, ok, ok, 4, 258, None, 256, None),
+        K._kv8_append(cp, ok, ok, 4, 256, None, 256, None),       # new_len is seq_len
+        K._kv8_append(cp, ok, ok, 4, None, 260, 256, None),       # start overlaps seq_len
         K._kv8_append(cp, ok, rows(type=K.F16), 4, None, None, 256, None),
         K._kv8_append(cp, rows(type=3), rows(type=3), 4, None, None, 256, None),
         K._kv8_append(cp, rows(data=264), ok, 4, None, None, 256, None),
