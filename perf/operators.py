@@ -444,7 +444,9 @@ def run(S):
             K.kv8_attn(S["cache"], S["q"], S["out"], S["ws"], lse=S["lse"], q_len=S["new_len"])
             return S["out"], S["lse"]
         if c["op"] == "mass":
-            K.kv8_mass(S["cache"], S["q"], S["lse"], S["ws"], q_len=S["new_len"], decay=0.0)
+            # (the plain form's log normalisers may come transposed)
+            K.kv8_mass(S["cache"], S["q"], S["lse"].contiguous(), S["ws"], q_len=S["new_len"],
+                       decay=0.0)
             return S["s"]["mass"]
         K.kv8_evict(S["cache"], c["keep"], c["sink"], c["recent"], S["kept"], S["ws"],
                     dst=S["dst_cache"])
