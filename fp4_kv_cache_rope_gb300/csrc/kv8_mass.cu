@@ -9,7 +9,7 @@
 // operand tile once and streams the queries that see them, 256 rows at a time;
 // queries go in as they are (16-bit), K in their type: a code times a power of
 // two is exact in both.  2 D flop per pair against one exponential: the tensor
-// cores and the issue slots of the eight exponential warps are about even.
+// cores and the issue slots of the exponential warps are about even.
 //
 // x = fma(s, f, -a) with a fp32 constant per query.  f = c log2(e) is rounded,
 // f = (1 - eps) true f: with a = (1 - eps) lse log2(e), rounded once, what is left
@@ -19,10 +19,17 @@
 //
 // A cached row is one thread's in each of four warp groups: even and odd query
 // tiles, left and right half of their columns.  Their four sums are added in a
-// fixed order and written by the first group.
+// fixed order and written by a group that has the item's first query tile, so
+// that items of a single tile alternate between two pairs of groups.
 //
-// Warps (672 threads): 0-15 exponentials; 16-19 load (K into its tile, queries
-// by 16-byte asynchronous copies into a two-stage ring); 20 issues the MMAs.
+// Warps (768 threads): 0-15 exponentials; 16-19 copy queries (16 bytes at a
+// time, asynchronously, into a two-stage ring); 20-22 turn K's codes into one of
+// two operand tiles; 23 issues the MMAs.  With few query tiles to an item it is
+// the loading that takes the time: a second K tile, warps of its own for K and
+// an item's codes asked for one item ahead took 100 tokens of 4 heads on 8
+// caches of 16384 rows from 120 to 75 us, 90 tokens of 2 on 21 of 120721 from
+// 1312 to 855 us (a prompt of 4096 on itself, 16 tiles to an item and more: 95
+// to 91).
 #include <type_traits>
 
 #include "kv8_mma.cuh"
@@ -33,20 +40,23 @@ namespace {
 constexpr int kKeys = 128;
 static_assert(kKeys == kKv8Step, "the items are the steps of the split");
 constexpr int kCols = 256;
-constexpr int kThreads = 672;
 constexpr int kExpWarps = 16;
+constexpr int kQWarps = 4;
+constexpr int kKWarps = 3;
+constexpr int kThreads = 32 * (kExpWarps + kQWarps + kKWarps + 1);   // 80 registers each
 
 template <int D>
 struct MassSmem {
   static constexpr int kSlabs = D / 64;
   static constexpr int kKSlab = kKeys * 128;          // [128 rows x 64 channels], swizzled
   static constexpr int kQSlab = kCols * 128;
-  static constexpr int kK = 0;
-  static constexpr int kQ = kSlabs * kKSlab;          // 2 stages
-  static constexpr int kConst = kQ + 2 * kSlabs * kQSlab;   // [4][256] -a
+  static constexpr int kK = 0;                        // 2 stages
+  static constexpr int kQ = 2 * kSlabs * kKSlab;      // 2 stages
+  static constexpr int kCode = kQ + 2 * kSlabs * kQSlab;   // the next item's codes, by chunk
+  static constexpr int kConst = kCode + kKeys * kSlabs * 64;   // [4][256] -a
   static constexpr int kSum = kConst + 4 * kCols * 4;   // [2][3][128]
   static constexpr int kBars = kSum + 2 * 3 * kKeys * 4;
-  static constexpr int kFlags = kBars + 128;          // abort, tmem, K's reference scale [4]
+  static constexpr int kFlags = kBars + 192;          // abort, tmem, K's reference scale [4]
   // tensor memory holds one CTA, so a second is kept off the SM
   static constexpr int kBytes = kFlags + 64 < 120 * 1024 ? 120 * 1024 : kFlags + 64;
 };
@@ -59,17 +69,28 @@ struct MassParams {
 struct Item {
   int b, h, key0, n, ql, rows, first, nt;   // rows = ql * G; query tiles first .. first + nt
 };
-__device__ __forceinline__ Item item_of(const MassParams& p, int lane, int64_t id) {
+// The sequence of the last item looked up, and its items [before, end): the next
+// one mostly lies in it too.
+struct Seq {
+  int b, n, ql;
+  int64_t before, end;
+};
+__device__ __forceinline__ Item item_of(const MassParams& p, int lane, int64_t id, Seq& s) {
   const Kv8& c = p.a.c;
+  if (id >= s.end) {
+    s.b = kv8_find(c, lane, c.heads, id, s.before);
+    s.n = kv8_len(c, s.b);
+    s.end = s.before + (int64_t)kv8_steps(c, s.b) * c.heads;
+    const int ql = p.a.q_len ? p.a.q_len[s.b] : p.a.T;
+    s.ql = ql < 0 ? 0 : (ql > p.a.T ? p.a.T : ql);
+  }
   Item it;
-  int64_t before;
-  it.b = kv8_find(c, lane, c.heads, id, before);
-  const int k = (int)(id - before);
+  const int k = (int)(id - s.before);
+  it.b = s.b;
+  it.n = s.n;
+  it.ql = s.ql;
   it.h = k % c.heads;
   it.key0 = k / c.heads * kKeys;
-  it.n = kv8_len(c, it.b);
-  int ql = p.a.q_len ? p.a.q_len[it.b] : p.a.T;
-  it.ql = ql < 0 ? 0 : (ql > p.a.T ? p.a.T : ql);
   it.rows = it.ql * p.a.G;
   const int tok0 = max(0, it.key0 - (it.n - it.ql));   // the first query that sees row key0
   it.first = tok0 * p.a.G / kCols;
@@ -78,11 +99,37 @@ __device__ __forceinline__ Item item_of(const MassParams& p, int lane, int64_t i
   return it;
 }
 
+// Sixteen codes times a power of two, in the queries' type.  bf16: a code as f16
+// has at most eight significant bits and an exponent field of five that is not
+// zero, so its bits moved down by three are a bf16 2^112 too small.
+template <int FMT, typename V>
+__device__ __forceinline__ void codes_to(uint4 w, float fs, uint32_t (&o)[8]) {
+  const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t h[2];
+    kv8_to_f16<FMT>(ww[j], h[0], h[1]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (std::is_same<V, __nv_bfloat162>::value) {
+        const uint32_t u = (h[e] >> 3 & 0x0FFF0FFFu) | (h[e] & 0x80008000u);
+        const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u),
+                            __float2bfloat162_rn(fs * 5.19229686e33f));
+        o[2 * j + e] = *reinterpret_cast<const uint32_t*>(&x);
+      } else {
+        const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&h[e]), __float2half2_rn(fs));
+        o[2 * j + e] = *reinterpret_cast<const uint32_t*>(&x);
+      }
+    }
+  }
+}
+
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p) {
   using L = MassSmem<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kMmaWarp = kExpWarps + kQWarps + kKWarps;
   const Kv8& c = p.a.c;
   griddep_wait();
   griddep_launch_dependents();
@@ -91,23 +138,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
     return;
   }
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
-  uint64_t* k_full = bars;        // 4 warps, one phase per item
-  uint64_t* k_empty = bars + 1;   // commit of the item's last MMA
-  uint64_t* q_full = bars + 2;    // [2] 4 warps
-  uint64_t* q_empty = bars + 4;   // [2] commit
-  uint64_t* s_full = bars + 6;    // [2] commit
-  uint64_t* s_empty = bars + 8;   // [2] 8 warps
-  uint64_t* x_full = bars + 10;   // [2] 12 warps: the other groups' sums of a round are there
-  uint64_t* x_empty = bars + 12;  // [2] 4 warps: ... were read
-  uint64_t* drain = bars + 14;
+  uint64_t* k_full = bars;        // [2] 3 warps, one phase per item
+  uint64_t* k_empty = bars + 2;   // [2] commit of the item's last MMA
+  uint64_t* q_full = bars + 4;    // [2] 4 warps
+  uint64_t* q_empty = bars + 6;   // [2] commit
+  uint64_t* s_full = bars + 8;    // [2] commit
+  uint64_t* s_empty = bars + 10;  // [2] 8 warps
+  uint64_t* x_full = bars + 12;   // [2] 12 warps: the other groups' sums of a round are there
+  uint64_t* x_empty = bars + 14;  // [2] 4 warps: ... were read
+  uint64_t* drain = bars + 16;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kFlags);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kFlags + 4);
   volatile float* refs = reinterpret_cast<volatile float*>(smem + L::kFlags + 8);
   if (tid == 0) {
-    mbar_init(k_full, 4);
-    mbar_init(k_empty, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + i, 4);
+      mbar_init(k_full + i, kKWarps);
+      mbar_init(k_empty + i, 1);
+      mbar_init(q_full + i, kQWarps);
       mbar_init(q_empty + i, 1);
       mbar_init(s_full + i, 1);
       mbar_init(s_empty + i, 8);
@@ -118,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == kExpWarps + 4) tmem_alloc(tmem_slot, 512);
+  if (warp == kMmaWarp) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -140,6 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
   };
   // q counts the CTA's query tiles over all items, k its items with queries
   uint32_t q = 0, k = 0, round = 0;
+  Seq seq{0, 0, 0, 0, 0};
   if (warp < kExpWarps) {
     // ======================================================== exponential warps
     const int wg = warp >> 2, buf = wg >> 1, half = wg & 1, key = 32 * (warp & 3) + lane;
@@ -147,12 +195,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
         tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kCols * buf + kCols / 2 * half;
     float* sums = reinterpret_cast<float*>(smem + L::kSum);
     for (int64_t id; (id = item_id(round)) >= 0; ++round) {
-      const Item it = item_of(p, lane, id);
+      const Item it = item_of(p, lane, id, seq);
       uint64_t acc[2] = {0, 0};
       // query rows below this one do not see the thread's cached row
       const int64_t see = (int64_t)(it.key0 + key - (it.n - it.ql)) * p.a.G;
       bool got = false;
       float f = 0.0f;
+      // (the page's entry is asked for before the queries, and the weight before
+      // the other groups' sums)
+      const int other_wg = (wg - 2 * (int)(q & 1)) & 3;   // 0: this one writes
+      const bool mine = other_wg == 0 && it.key0 + key < it.n;
+      const int id_ = mine ? kv8_page_id(c, it.b, it.key0 + key) : 0;
       for (int i = 0; i < it.nt; ++i, ++q) {
         if ((q & 1) != (uint32_t)buf) continue;
         wait(s_full + buf, (q >> 1) & 1);
@@ -192,12 +245,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
             }
           }
         };
+        // 32-column chunks with a query in them
+        const int chunks = (it.rows - (it.first + i) * kCols - kCols / 2 * half + 31) >> 5;
         if (__any_sync(0xffffffffu, hidden > 0)) {
 #pragma unroll 1
           for (int u = 0; u < kCols / 64; ++u) add(std::true_type{}, u);
         } else {
 #pragma unroll
-          for (int u = 0; u < kCols / 64; ++u) add(std::false_type{}, u);
+          for (int u = 0; u < kCols / 64; ++u)
+            if (u < chunks) add(std::false_type{}, u);
         }
         tc_fence_before();
         __syncwarp();
@@ -211,91 +267,45 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
       const float sum = (a0 + a1) + (a2 + a3);
       // (waits with a limit, not a named barrier: a warp may have given up)
       float* slot = sums + (round & 1) * 3 * kKeys + key;
-      if (wg > 0) {
+      if (other_wg > 0) {
         if (round >= 2) wait(x_empty + (round & 1), ((round >> 1) - 1) & 1);
         if (!ok) break;
-        slot[(wg - 1) * kKeys] = sum;
+        slot[(other_wg - 1) * kKeys] = sum;
         __syncwarp();
         if (lane == 0) mbar_arrive(x_full + (round & 1));
         continue;
+      }
+      float* m = nullptr;
+      float old = 0.0f;
+      if (mine) {
+        const int page = kv8_check(c, id_);
+        if (page >= 0) {
+          int in_page;
+          kv8_in_page(c, it.key0 + key, in_page);
+          m = c.mass + kv8_row(c, page, it.h, in_page);
+          if (p.a.decay != 0.0f) old = *m;
+        } else {
+          set_status(p.a.status, CSA2_DEV_BAD_PAGE);
+        }
       }
       wait(x_full + (round & 1), (round >> 1) & 1);
       if (!ok) break;
       const float other = (slot[0] + slot[kKeys]) + slot[2 * kKeys];
       __syncwarp();
       if (lane == 0) mbar_arrive(x_empty + (round & 1));
-      if (it.key0 + key < it.n) {
-        int in_page;
-        const int page = kv8_page(c, it.b, it.key0 + key, in_page);
-        if (page >= 0) {
-          float* m = c.mass + kv8_row(c, page, it.h, in_page);
-          const float w = sum + other;
-          *m = p.a.decay == 0.0f ? w : *m * p.a.decay + w;
-        } else {
-          set_status(p.a.status, CSA2_DEV_BAD_PAGE);
-        }
+      if (m) {
+        const float w = sum + other;
+        *m = p.a.decay == 0.0f ? w : old * p.a.decay + w;
       }
     }
-  } else if (warp < kExpWarps + 4) {
-    // ============================================================ loading warps
+  } else if (warp < kExpWarps + kQWarps) {
+    // ============================================================ query warps
     const int ct = tid - 32 * kExpWarps;
-    const bool bf16 = p.a.q.type == CSA2_BF16;
     const float eps = p.a.scale_low / p.a.scale_log2;
     for (int64_t id; (id = item_id(round)) >= 0; ++round) {
-      const Item it = item_of(p, lane, id);
+      const Item it = item_of(p, lane, id, seq);
       if (it.nt == 0) continue;
-      // ---- K: 16-byte chunk cc (of a 64-channel half) of rows r4 + 32 v
-      if (k > 0) wait(k_empty, (k - 1) & 1);
-      if (!ok) break;
-      {
-        const int cc = ct & 3, r4 = ct >> 2;
-        int64_t grow = -1;
-        float gs = 0.0f;
-        const int pos = it.key0 + 16 * (lane & 7);
-        if (pos < it.n) {
-          int in_page;
-          const int page = kv8_page(c, it.b, pos, in_page);
-          if (page >= 0) {
-            grow = kv8_row(c, page, it.h, in_page);
-            gs = c.scales[0][kv8_block(c, page, it.h, in_page)];
-          }
-        }
-        float ref = gs;
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
-        gs *= kv8_inverse(ref);
-        if (ct == 0) refs[k & 3] = ref;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int row = r4 + 32 * v;
-          const int64_t g = __shfl_sync(0xffffffffu, grow, row >> 4);
-          const float fs = __shfl_sync(0xffffffffu, gs, row >> 4);
-          const bool in = g >= 0 && it.key0 + row < it.n;
-#pragma unroll
-          for (int s = 0; s < L::kSlabs; ++s) {
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (in)
-              w = *reinterpret_cast<const uint4*>(c.codes[0] + (g + (row & 15)) * D + 64 * s + 16 * cc);
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-            uint32_t o[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float x[4];
-              kv8_to_f32<FMT>(ww[j], x);
-              o[2 * j] = pack16(x[0] * fs, x[1] * fs, bf16 ? CSA2_BF16 : CSA2_F16);
-              o[2 * j + 1] = pack16(x[2] * fs, x[3] * fs, bf16 ? CSA2_BF16 : CSA2_F16);
-            }
-            uint8_t* slab = smem + L::kK + s * L::kKSlab;
-            st_swizzled(slab, row, 2 * cc, make_uint4(o[0], o[1], o[2], o[3]));
-            st_swizzled(slab, row, 2 * cc + 1, make_uint4(o[4], o[5], o[6], o[7]));
-          }
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(k_full);
-        ++k;
-      }
-      // ---- queries.  A stage is free once its MMA is done; the constants' four
+      // A stage is free once its MMA is done; the constants' four
       // slots are: the MMA of tile q - 2 waited for the sums of tile q - 4.
       // Query row r is token r / G, head r % G of the group: each thread keeps
       // the place of its next row of queries (they go up by 16) and of its next
@@ -329,6 +339,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
         const int st = q & 1;
         if (q >= 2) wait(q_empty + st, ((q >> 1) - 1) & 1);
         if (!ok) break;
+        float y[kCols / 128];   // (asked for before the queries' copies)
+#pragma unroll
+        for (int v = 0; v < kCols / 128; ++v) {
+          y[v] = pl.r < it.rows ? lsrc[pl.off] : -INFINITY;
+          step(pl, 128, g128, l_by, l_wrap);
+        }
         const uint32_t stage = smem_u32(smem + L::kQ + st * L::kSlabs * L::kQSlab) + dst;
 #pragma unroll 4
         for (int v = 0; v < kCols / 16; ++v) {
@@ -343,27 +359,120 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
                          : "memory");
           step(pq, 16, g16, q_by, q_wrap);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
         float* cst = reinterpret_cast<float*>(smem + L::kConst) + kCols * (q & 3);
 #pragma unroll
         for (int v = 0; v < kCols / 128; ++v) {
           float a = INFINITY;                   // no weight
-          if (pl.r < it.rows) {
-            const float y = lsrc[pl.off];
-            if (y != -INFINITY) {
-              const float hi = y * 1.44269502f;
-              a = hi + (fmaf(y, 1.44269502f, -hi) + y * 1.92596299e-8f - eps * hi);
-            }
+          if (y[v] != -INFINITY) {
+            const float hi = y[v] * 1.44269502f;
+            a = hi + (fmaf(y[v], 1.44269502f, -hi) + y[v] * 1.92596299e-8f - eps * hi);
           }
           cst[ct + 128 * v] = -a;
-          step(pl, 128, g128, l_by, l_wrap);
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        asm volatile("cp.async.wait_all;" ::: "memory");
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full + st);
       }
       if (!ok) break;
+    }
+  } else if (warp < kMmaWarp) {
+    // ============================================================== K warps
+    // 16-byte chunks i = ct + 96 v of the item.  An item's codes are asked for
+    // while the one before is converted (each thread into the place that it has
+    // just read), its page and scales before that.
+    const int ct = tid - 32 * (kExpWarps + kQWarps);
+    const bool bf16 = p.a.q.type == CSA2_BF16;
+    constexpr int kChunks = kKeys * L::kSlabs * 4;
+    constexpr int kIters = (kChunks + 32 * kKWarps - 1) / (32 * kKWarps), kBatch = 4;
+    const uint32_t code = smem_u32(smem + L::kCode);
+    Item it;
+    int64_t grow = -1;   // of the 16 rows lane & 7, or -1
+    float gs = 0.0f;
+    // the next item with queries
+    auto meta = [&]() -> bool {
+      for (;; ++round) {
+        const int64_t id = item_id(round);
+        if (id < 0) return false;
+        it = item_of(p, lane, id, seq);
+        if (it.nt > 0) break;
+      }
+      ++round;
+      grow = -1;
+      gs = 0.0f;
+      const int pos = it.key0 + 16 * (lane & 7);
+      if (pos < it.n) {
+        int in_page;
+        const int page = kv8_page(c, it.b, pos, in_page);
+        if (page >= 0) {
+          grow = kv8_row(c, page, it.h, in_page);
+          gs = c.scales[0][kv8_block(c, page, it.h, in_page)];
+        }
+      }
+      return true;
+    };
+    auto ask = [&](int i) {   // chunk i = (row * kSlabs + half) * 4 + chunk (whole warp)
+      const int row = i / (4 * L::kSlabs);
+      const int64_t g = __shfl_sync(0xffffffffu, grow, (row >> 4) & 7);
+      const bool in = i < kChunks && g >= 0 && it.key0 + row < it.n;
+      if (i < kChunks)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(code + 16 * i),
+                     "l"(c.codes[0] + (in ? (g + (row & 15)) * D + 16 * (i % (4 * L::kSlabs)) : 0)),
+                     "r"(in ? 16u : 0u)
+                     : "memory");
+    };
+    bool more = meta();
+    if (more) {
+#pragma unroll
+      for (int v = 0; v < kIters; ++v) ask(ct + 32 * kKWarps * v);
+    }
+    while (more) {
+      float ref = gs;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
+      const float rel = gs * kv8_inverse(ref);
+      more = meta();
+      if (k >= 2) wait(k_empty + (k & 1), ((k >> 1) - 1) & 1);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (!ok) break;
+      if (ct == 0) refs[k & 3] = ref;
+      auto put = [&](auto type) {
+        using V = decltype(type);
+#pragma unroll
+        for (int v0 = 0; v0 < kIters; v0 += kBatch) {
+          uint4 w[kBatch];
+#pragma unroll
+          for (int v = 0; v < kBatch; ++v) {
+            const int i = ct + 32 * kKWarps * (v0 + v);
+            w[v] = i < kChunks ? *reinterpret_cast<const uint4*>(smem + L::kCode + 16 * i)
+                               : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int v = 0; v < kBatch; ++v) {
+            const int i = ct + 32 * kKWarps * (v0 + v), row = i / (4 * L::kSlabs);
+            const float fs = __shfl_sync(0xffffffffu, rel, (row >> 4) & 7);
+            uint32_t o[8];
+            codes_to<FMT, V>(w[v], fs, o);
+            uint8_t* slab = smem + L::kK + ((k & 1) * L::kSlabs + i / 4 % L::kSlabs) * L::kKSlab;
+            if (i < kChunks) {
+              st_swizzled(slab, row, 2 * (i & 3), make_uint4(o[0], o[1], o[2], o[3]));
+              st_swizzled(slab, row, 2 * (i & 3) + 1, make_uint4(o[4], o[5], o[6], o[7]));
+            }
+          }
+          if (more) {
+#pragma unroll
+            for (int v = 0; v < kBatch; ++v) ask(ct + 32 * kKWarps * (v0 + v));
+          }
+        }
+      };
+      if (bf16)
+        put(__nv_bfloat162());
+      else
+        put(__half2());
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(k_full + (k & 1));
+      ++k;
     }
   } else {
     // ================================================================== MMA warp
@@ -373,10 +482,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
     const uint64_t qd = smem_desc(smem_u32(smem + L::kQ), 16, 1024, 2);
     bool issued = false;
     for (int64_t id; (id = item_id(round)) >= 0; ++round) {
-      const Item it = item_of(p, lane, id);
+      const Item it = item_of(p, lane, id, seq);
       if (it.nt == 0) continue;
-      wait(k_full, k & 1);
-      ++k;
+      wait(k_full + (k & 1), (k >> 1) & 1);
       for (int i = 0; i < it.nt; ++i, ++q) {
         const int st = q & 1;
         wait(q_full + st, (q >> 1) & 1);
@@ -388,16 +496,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
           for (int s = 0; s < L::kSlabs; ++s)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_f16(tmem + kCols * st, kd + (s * L::kKSlab + kk * 32) / 16,
+              mma_f16(tmem + kCols * st, kd + (((k & 1) * L::kSlabs + s) * L::kKSlab + kk * 32) / 16,
                       qd + (st * L::kSlabs * L::kQSlab + s * L::kQSlab + kk * 32) / 16, idesc,
                       (s | kk) ? 1u : 0u);
           mma_commit(q_empty + st);
           mma_commit(s_full + st);
-          if (i + 1 == it.nt) mma_commit(k_empty);
+          if (i + 1 == it.nt) mma_commit(k_empty + (k & 1));
         }
         issued = true;
       }
       if (!ok) break;
+      ++k;
     }
     if (issued && lane == 0) {   // let every issued MMA land before tensor memory is freed
       mma_commit(drain);
@@ -408,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
   if (!ok) set_status(p.a.status, CSA2_DEV_TIMEOUT);
   tc_fence_before();
   __syncthreads();
-  if (warp == kExpWarps + 4) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -240,6 +240,37 @@ def check_mass(p, q, qd, lse, G, q_lens):
                 assert (np.abs(m[:n] - f * w[b, h]) <= f * w[b, h] * w[b, h, "rel"] + 1e-36).all()
 
 
+@pytest.mark.parametrize("T,D,fmt", [(435, 128, O.E4M3), (333, 64, O.INT8), (90, 128, O.INT8)])
+def test_weights_of_many_query_tiles_sum_to_one_per_query_and_repeat(T, D, fmt):
+    B, Hkv, G, n = 7, 4, 13, 577
+    p = filled(B, Hkv, D, [n] * B, 32, 32, fmt, seed=41)
+    q = p.rows(T, Hkv * G, "f16", 0.7).cuda()
+    ws = p.c.workspace(T, Hkv * G)
+    out = torch.empty_like(q)
+    lse = torch.empty(B, T, Hkv * G, device="cuda")
+    K.kv8_attn(p.c, q, out, ws, lse=lse)
+    first = None
+    for _ in range(12):
+        K.kv8_mass(p.c, q, lse, ws, decay=0.0)
+        first = p.c.mass.clone() if first is None else first
+        assert torch.equal(p.c.mass.view(torch.int32), first.view(torch.int32))
+    assert K.get_status(ws) == 0
+    # a weight is off by its logit's error (D + 4 roundings of at most 2^-23 of the
+    # sum of its products' magnitudes, at most |q| |k|), here and in lse, by lse's
+    # own roundings, and by the additions: T G of them
+    big = 0.0
+    for b in range(B):
+        for h in range(Hkv):
+            k = p.seq[b, h, "k"].values()
+            big = max(big, (q[b, :, h * G:(h + 1) * G].double().norm(dim=-1).max().item()
+                            * np.linalg.norm(k, axis=-1).max() / math.sqrt(D)))
+    rel = 2 * ((D + 4) * 2.0 ** -23 * big + 2.0 ** -22 * lse.abs().max().item() + 2.0 ** -20) + (
+        T * G + n) * 2.0 ** -23
+    for b in range(B):
+        for h in range(Hkv):
+            assert abs(p.at("mass", b, h)[:n].astype(np.float64).sum() / (T * G) - 1) <= rel
+
+
 @pytest.mark.parametrize("T", [1, 140])
 def test_attention_of_extreme_rows(T):
     """Large and tiny queries, V blocks whose scales lie far apart, zero rows,
