@@ -188,9 +188,15 @@ csa2_status csa2_kv8_mass(const csa2_kv8_cache* cache, const csa2_rows* q, int32
   Kv8Attn a = attn_of(cache, T ? q : nullptr, H, T, q_len, softmax_scale, ws);
   a.lse = const_cast<float*>(lse);
   a.decay = decay;
-  // Up to 32 query rows per (sequence, K/V head) stay in a warp's registers.
-  return done(T * a.G <= 32 ? launch_kv8_mass_few(a, sms(), (cudaStream_t)stream)
-                            : launch_kv8_mass_many(a, sms(), (cudaStream_t)stream));
+  // Up to 32 query rows per (sequence, K/V head) stay in a warp's registers: 16
+  // sequences of 9000 rows, 4 heads, D 128 take 34 us with 32 rows, the tensor
+  // cores' kernel 97 us with any number up to 256.  Up to 64 in two launches is
+  // faster too (63 us with 64 rows), unless the cache is so small that the
+  // launches are what takes the time (2 sequences of 2000: 24 us against 13 us).
+  const int64_t tiles = (int64_t)cache->batch * cache->kv_heads * ((cache->max_len + 127) / 128);
+  const int rows = T * a.G <= 32 || tiles <= 4 * (int64_t)sms() ? 32 : 64;
+  return done(T * a.G <= rows ? launch_kv8_mass_few(a, sms(), (cudaStream_t)stream)
+                              : launch_kv8_mass_many(a, sms(), (cudaStream_t)stream));
 }
 
 csa2_status csa2_kv8_evict(const csa2_kv8_cache* cache, const csa2_kv8_cache* dst, int32_t keep,

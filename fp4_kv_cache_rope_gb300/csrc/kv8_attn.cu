@@ -38,6 +38,7 @@ struct DecodeParams {
   Kv8Attn a;
   int32_t rows, tiles;                    // query rows per (sequence, K/V head), tiles of them
   int32_t ctas;
+  int32_t row0;                           // first query row (weights)
 };
 
 // The cached row of column n (0..7) of an 8-column tile.  Chosen so that the
@@ -651,8 +652,8 @@ __global__ void __launch_bounds__(D / 4 * kCombine) kv8_combine_kernel(DecodePar
 // CTAs that an SM holds, by the registers of the query rows.
 constexpr int mass_ctas(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
 
-// mass_j = decay mass_j + sum over the query rows of 2^(c q k_j - lse), for up to
-// 8 NT query rows: their fragments stay in registers while a warp streams its
+// mass_j = decay mass_j + sum over the query rows of 2^(c q k_j - lse), for
+// 8 NT query rows from row0 on: their fragments stay in registers while a warp streams its
 // cached rows, the next tile's codes loaded while this one is worked on.  A
 // cached row belongs to one warp, so nothing is added atomically and the order
 // of the sum is fixed.
@@ -718,13 +719,13 @@ __global__ void __launch_bounds__(kThreads, mass_ctas(NT)) kv8_mass_kernel(Decod
     int lim[NT][2], full = 0x7FFFFFFF;
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
-      const int row = 8 * u + g, tok = row / p.a.G, hd = h * p.a.G + row % p.a.G;
+      const int row = p.row0 + 8 * u + g, tok = row / p.a.G, hd = h * p.a.G + row % p.a.G;
       const bool ok = row < p.rows && tok < ql;
       const float f = load_query<D>(p.a.q, b * p.a.q.sb + tok * p.a.q.st + hd * p.a.q.sh, ok, t,
                                     1.0f, qf[u]);
       float y = ok ? p.a.lse[((int64_t)b * p.a.T + tok) * p.a.H + hd] : -INFINITY;
-      const int see = ok && y != -INFINITY ? min(n, n - ql + tok + 1) : 0;
-      if (y == -INFINITY) y = 0.0f;
+      const int see = ok && fabsf(y) != INFINITY ? min(n, n - ql + tok + 1) : 0;
+      if (fabsf(y) == INFINITY) y = 0.0f;
       // a row without weight: a constant so large that every weight is 0
       const float hi = see ? y * 1.44269502f : INFINITY;
       const float g2 =
@@ -856,9 +857,21 @@ cudaError_t mass_as(DecodeParams p, int num_sms, cudaStream_t s) {
 }
 template <int D, int FMT>
 cudaError_t mass_of(const DecodeParams& p, int num_sms, cudaStream_t s) {
-  return p.rows <= 8    ? mass_as<D, 1, FMT>(p, num_sms, s)
-         : p.rows <= 16 ? mass_as<D, 2, FMT>(p, num_sms, s)
-                        : mass_as<D, 4, FMT>(p, num_sms, s);
+  const int rows = p.rows - p.row0;
+  return rows <= 8    ? mass_as<D, 1, FMT>(p, num_sms, s)
+         : rows <= 16 ? mass_as<D, 2, FMT>(p, num_sms, s)
+                      : mass_as<D, 4, FMT>(p, num_sms, s);
+}
+template <int FMT>
+cudaError_t mass_rows(DecodeParams p, int num_sms, cudaStream_t s) {
+  do {   // 32 query rows at a time; those behind the first add to what they left
+    const cudaError_t e =
+        p.a.D == 64 ? mass_of<64, FMT>(p, num_sms, s) : mass_of<128, FMT>(p, num_sms, s);
+    if (e != cudaSuccess) return e;
+    p.row0 += 32;
+    p.a.decay = 1.0f;
+  } while (p.row0 < p.rows);
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -866,7 +879,7 @@ cudaError_t mass_of(const DecodeParams& p, int num_sms, cudaStream_t s) {
 size_t kv8_part_bytes(int D) { return 2 * (size_t)kKv8Ctas * slot_floats(D) * 4; }
 
 cudaError_t launch_kv8_attn(const Kv8Attn& a, int num_sms, cudaStream_t s) {
-  DecodeParams p{a, a.T * a.G, 1, 1};
+  DecodeParams p{a, a.T * a.G, 1, 1, 0};
   if (a.c.format == CSA2_KV8_E4M3)
     return a.D == 64 ? decode_of<64, CSA2_KV8_E4M3>(p, num_sms, s)
                      : decode_of<128, CSA2_KV8_E4M3>(p, num_sms, s);
@@ -875,12 +888,9 @@ cudaError_t launch_kv8_attn(const Kv8Attn& a, int num_sms, cudaStream_t s) {
 }
 
 cudaError_t launch_kv8_mass_few(const Kv8Attn& a, int num_sms, cudaStream_t s) {
-  const DecodeParams p{a, a.T * a.G, 1, 1};
-  if (a.c.format == CSA2_KV8_E4M3)
-    return a.D == 64 ? mass_of<64, CSA2_KV8_E4M3>(p, num_sms, s)
-                     : mass_of<128, CSA2_KV8_E4M3>(p, num_sms, s);
-  return a.D == 64 ? mass_of<64, CSA2_KV8_INT8>(p, num_sms, s)
-                   : mass_of<128, CSA2_KV8_INT8>(p, num_sms, s);
+  const DecodeParams p{a, a.T * a.G, 1, 1, 0};
+  return a.c.format == CSA2_KV8_E4M3 ? mass_rows<CSA2_KV8_E4M3>(p, num_sms, s)
+                                     : mass_rows<CSA2_KV8_INT8>(p, num_sms, s);
 }
 
 }  // namespace csa2

@@ -446,7 +446,7 @@ csa2_status csa2_kv8_attn(const csa2_kv8_cache *cache, const csa2_rows *q, int32
  *   mass_j = decay * mass_j + sum over the head's G query heads and the queries
  *            that see row j of exp(softmax_scale * q . k_j - lse)
  * with q, q_len and softmax_scale as given to csa2_kv8_attn, whose lse it takes
- * (fp32 [B, T, H]; a query with lse = -inf adds nothing).  decay 1 accumulates,
+ * (fp32 [B, T, H]; a query with lse = -inf or +inf adds nothing).  decay 1 accumulates,
  * 0 starts anew (whatever mass held).  Rows behind seq_len are left as they were.
  */
 csa2_status csa2_kv8_mass(const csa2_kv8_cache *cache, const csa2_rows *q, int32_t H, int32_t T,

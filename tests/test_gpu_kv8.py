@@ -271,6 +271,25 @@ def test_weights_of_many_query_tiles_sum_to_one_per_query_and_repeat(T, D, fmt):
             assert abs(p.at("mass", b, h)[:n].astype(np.float64).sum() / (T * G) - 1) <= rel
 
 
+@pytest.mark.parametrize("T,G,D,fmt", [(11, 3, 128, O.E4M3), (16, 4, 64, O.INT8), (5, 13, 64, O.E4M3)])
+def test_weights_of_33_to_65_query_rows_in_a_large_cache(T, G, D, fmt):
+    # (large by its capacity: 612 tiles of 128 rows)
+    p = filled(3, 4, D, [300, 170, 9], 16, 0, fmt, seed=44, cap=6500)
+    q = p.rows(T, 4 * G, "f16", 0.7)
+    qd, lse = run_attention(p, q, G, [T, T // 2, 3])
+    check_mass(p, q, qd, lse, G, [T, T // 2, 3])
+
+
+@pytest.mark.parametrize("T", [3, 50])
+def test_queries_whose_lse_is_infinite_add_nothing(T):
+    p = filled(2, 2, 64, [300, 170], 16, 0, O.E4M3, seed=43)
+    q = p.rows(T, 4, "bf16", 0.7)
+    qd, lse = run_attention(p, q, 2)
+    bad = lse.clone()
+    bad[0, 0, 1], bad[1, T - 1, 2], bad[0, T // 2] = float("inf"), float("-inf"), float("inf")
+    check_mass(p, q, qd, bad, 2, None)
+
+
 @pytest.mark.parametrize("T", [1, 140])
 def test_attention_of_extreme_rows(T):
     """Large and tiny queries, V blocks whose scales lie far apart, zero rows,
