@@ -127,14 +127,6 @@ __device__ __forceinline__ void kv8_to_f16(uint32_t w, uint32_t& lo, uint32_t& h
     hi = *reinterpret_cast<uint32_t*>(&hb);
   }
 }
-template <int FMT>
-__device__ __forceinline__ void kv8_to_f32(uint32_t w, float (&v)[4]) {
-  uint32_t lo, hi;
-  kv8_to_f16<FMT>(w, lo, hi);
-  const float2 a = __half22float2(*reinterpret_cast<__half2*>(&lo));
-  const float2 b = __half22float2(*reinterpret_cast<__half2*>(&hi));
-  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
-}
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));

@@ -22,6 +22,11 @@
 // go to f16 for the P V product times 2^7 and times the block's V scale over
 // the largest V scale so far: at most 2^15, with f16's full 11 bits down to
 // 2^-21; their sum is taken in fp32 before that rounding.
+//
+// Measured at D 128 and 8 K/V heads, one token a sequence: 32 sequences of up to
+// 32768 rows 234 us (6.4 TB/s, 94% of a copy's), 8 of 131072 315 us (6.8 TB/s).
+// Few bytes are bound by latency: 5 tokens of 16 sequences of up to 9001 rows, 4
+// heads, D 64, 30 us for 8 us of bytes.
 #include "kv8.cuh"
 
 namespace csa2 {

@@ -14,6 +14,10 @@
 // exponentials of the other are taken.  The arithmetic per cached byte is
 // 256 rows' worth, so the tensor cores (4 D flop per query row and cached row)
 // bound it; converting a tile's codes to f16 is paid once per 256 query rows.
+// 4096 tokens of 64 heads at the end of 16384 rows, D 128: 1.68 ms, 1.15 PFLOP/s
+// (61% of a library product's burst rate).  A tile of 128 rows takes 4600 cycles,
+// of which the MMAs are 2100; the rest is the chain logits, maximum,
+// exponentials, P, of which two query tiles in flight hide only a part.
 //
 // Exactness.  Queries are scaled per row by a power of two into f16's range;
 // codes are converted to f16 times their block's scale over the largest scale

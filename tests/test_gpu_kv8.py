@@ -2,6 +2,8 @@
 bytes, kept rows and moved weights exactly; attention, its log normaliser and
 the accumulated weights within bounds derived in kv8_tools.attention_bounds."""
 import math
+import os
+import re
 
 import numpy as np
 import pytest
@@ -685,3 +687,21 @@ def test_serving_loop(fmt, graph):
         p.c.mass = real
         evicted()
     assert K.get_status(ws) == 0
+
+
+def test_readme_example():
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    blocks = re.findall(r"```py\n(.*?)```", text, re.S)
+    assert len(blocks) == 1
+    env = {}
+    exec(compile(blocks[0], "README.md", "exec"), env)
+    B, Hkv, G, keep = env["B"], env["Hkv"], env["H"] // env["Hkv"], env["keep"]
+    cache, kept = env["cache"], env["kept"].cpu()
+    assert cache.seq_len.tolist() == [keep + 1] * B
+    assert (kept.diff(dim=-1) > 0).all()
+    assert torch.equal(kept[..., :4], torch.arange(4, dtype=torch.int32).expand(B, Hkv, 4))
+    assert torch.equal(kept[..., -64:], torch.arange(1436, 1500, dtype=torch.int32).expand(B, Hkv, 64))
+    # the token's weights sum to one a query; behind them 0.99 of what stayed
+    m = cache.mass[:, :, : keep + 1].double()
+    assert torch.isfinite(m).all() and (m.sum(-1) <= 0.99 * env["prompt"] * G + G + 0.1).all()
+    assert (m.sum(-1) > G).all() and torch.isfinite(env["out"]).all() and torch.isfinite(env["out1"]).all()
