@@ -242,7 +242,7 @@ def check_mass(p, q, qd, lse, G, q_lens):
                 assert (np.abs(m[:n] - f * w[b, h]) <= f * w[b, h] * w[b, h, "rel"] + 1e-36).all()
 
 
-@pytest.mark.parametrize("T,D,fmt", [(435, 128, O.E4M3), (333, 64, O.INT8), (90, 128, O.INT8)])
+@pytest.mark.parametrize("T,D,fmt", [(435, 128, O.E4M3), (333, 64, O.INT8), (90, 128, O.INT8), (30, 128, O.E4M3)])
 def test_weights_of_many_query_tiles_sum_to_one_per_query_and_repeat(T, D, fmt):
     B, Hkv, G, n = 7, 4, 13, 577
     p = filled(B, Hkv, D, [n] * B, 32, 32, fmt, seed=41)
