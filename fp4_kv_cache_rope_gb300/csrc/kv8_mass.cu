@@ -10,17 +10,17 @@
 // queries go in as they are (16-bit), K in their type: a code times its block's
 // scale over the largest of the tile, a power of two, which is exact in bf16 and
 // in f16 unless that is 2^-15 or less (then off by at most 2^-24 of the largest
-// value).  2 D flop per pair against one exponential.  A prompt of 4096
-// tokens, 32 heads, D 128: 82 us; its products are 37 us at a library product's
+// value).  2 D flop per pair against one exponential.  A prompt of 4096 tokens,
+// 32 heads, D 128: 82 us; its products are 37 us at a library product's
 // rate, its exponentials 29 us at 32 a cycle and SM.  The CTA with the most tiles
 // has 64 for a mean of 56, and a tile takes 2400 cycles, in which its 64 KB of
 // queries are copied 16 bytes at a time.
 //
 // x = fma(s, f, -a) with a fp32 constant per query.  f = c log2(e) is rounded,
 // f = (1 - eps) true f: with a = (1 - eps) lse log2(e), rounded once, what is left
-// is eps x, nothing for the weights that count.  (As two
-// constants, -a and a factor of the sum for a's own rounding, 3e-7 of a weight at
-// lse 14, the shared memory reads cost 7%.)
+// is eps x, nothing for the weights that count.  (As two constants, -a and a
+// factor of the sum for a's own rounding, 3e-7 of a weight at lse 14, the shared
+// memory reads cost 7%.)
 //
 // The accumulation of S cuts off instead of rounding: over random sums a chain of
 // k steps came out k 16 2^-31 of it too small (4 steps 4e-8, 8 steps 6.5e-8), which
@@ -35,8 +35,8 @@
 // that items of a single tile alternate between two pairs of groups.
 //
 // Warps (768 threads): 0-15 exponentials; 16-19 copy queries (16 bytes at a
-// time, asynchronously, into a ring); 20-22 turn K's codes into one of
-// two operand tiles; 23 issues the MMAs.  With few query tiles to an item it is
+// time, asynchronously, into a ring); 20-22 turn K's codes into one of two
+// operand tiles; 23 issues the MMAs.  With few query tiles to an item it is
 // the loading that takes the time: a second K tile, warps of its own for K and
 // an item's codes asked for one item ahead took 100 tokens of 4 heads on 8
 // caches of 16384 rows from 120 to 73 us, 90 tokens of 2 on 21 of 120721 from
