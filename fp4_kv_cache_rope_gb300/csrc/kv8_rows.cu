@@ -562,10 +562,14 @@ struct MovedBlock {
         const int r = i * kRows + sub;
         if (r >= rows) continue;
         uint4 w = code[side][i];
-        const float f = scale[side][i] * inv;
+        // A code that is not 0 is at least 2^-9 and the new scale at least its
+        // value / 448, so f stays below 2^18.  A zero row does not bear on the new
+        // scale and knows no such bound: held below f16's infinity, times which it
+        // would not be 0.
+        const float f = fminf(scale[side][i] * inv, 0x1p17f);
         if (moved && f != 1.0f) {
-          // beyond f16's range (E4M3: rows of the smallest codes alone) in two
-          // steps, the first of which is exact
+          // beyond f16's range (E4M3: rows of the smallest codes and zero rows) in
+          // two steps, the first of which is exact
           const bool far = f > 32768.0f;
           if (far) w = recode16<FMT>(w, kv8_ratio(32768.0f));
           w = recode16<FMT>(w, kv8_ratio(far ? f * 0x1p-15f : f));
