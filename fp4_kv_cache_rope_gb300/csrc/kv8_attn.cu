@@ -728,10 +728,14 @@ __global__ void __launch_bounds__(kThreads, mass_ctas(NT)) kv8_mass_kernel(Decod
       const bool ok = row < p.rows && tok < ql;
       const float f = load_query<D>(p.a.q, b * p.a.q.sb + tok * p.a.q.st + hd * p.a.q.sh, ok, t,
                                     1.0f, qf[u]);
-      float y = ok ? p.a.lse[((int64_t)b * p.a.T + tok) * p.a.H + hd] : -INFINITY;
-      const int see = ok && fabsf(y) != INFINITY ? min(n, n - ql + tok + 1) : 0;
-      if (fabsf(y) == INFINITY) y = 0.0f;
-      // a row without weight: a constant so large that every weight is 0
+      const float y = ok ? p.a.lse[((int64_t)b * p.a.T + tok) * p.a.H + hd] : -INFINITY;
+      const int see = ok && fabsf(y) != INFINITY ? max(0, min(n, n - ql + tok + 1)) : 0;
+      // a row without weight: a constant so large that every weight is 0, and a
+      // zero row, because a NaN or an infinity in it would still count
+      if (see == 0) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) qf[u][i][0] = qf[u][i][1] = 0u;
+      }
       const float hi = see ? y * 1.44269502f : INFINITY;
       const float g2 =
           see ? exp2f(eps * hi - (fmaf(y, 1.44269502f, -hi) + y * 1.92596299e-8f)) : 1.0f;

@@ -354,7 +354,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
           x.off += wrap;
         }
       };
-      Place pq = place(r0 + (ct >> 3), st_, sh_), pl = place(r0 + ct, p.a.H, 1);
+      // A warp copies rows 4 w .. 4 w + 3 of every 16 of a tile, 8 lanes a row, and
+      // its lanes make the constants of the same rows, cr + 128 v: so a row without
+      // weight is cleared by the warp that copied it.
+      const int cr = 16 * (lane >> 2) + 4 * (ct >> 5) + (lane & 3);
+      Place pq = place(r0 + (ct >> 3), st_, sh_), pl = place(r0 + cr, p.a.H, 1);
       const int64_t q_by = 16 / G * st_ + 16 % G * sh_, q_wrap = st_ - G * sh_;
       const int64_t l_by = 128 / G * (int64_t)p.a.H + 128 % G, l_wrap = p.a.H - G;
       const char* qsrc = static_cast<const char*>(p.a.q.data) +
@@ -366,6 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
         if (q >= kStages) wait(q_empty + st, (q / kStages - 1) & 1);
         if (!ok) break;
         float y[kCols / 128];   // (asked for before the queries' copies)
+        const int held = (it.rows - pl.r + 127) >> 7;   // (the v's below it are query rows)
 #pragma unroll
         for (int v = 0; v < kCols / 128; ++v) {
           y[v] = pl.r < it.rows ? lsrc[pl.off] : -INFINITY;
@@ -404,9 +409,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
             const float hi = y[v] * 1.44269502f;
             a = hi + (fmaf(y[v], 1.44269502f, -hi) + y[v] * 1.92596299e-8f - eps * hi);
           }
-          cst[ct + 128 * v] = -a;
+          cst[cr + 128 * v] = -a;
         }
+        // rows without weight: a NaN or an infinity in them would count all the same
+        // (the vote is taken while the copies are on their way)
+        bool gone = false;
+#pragma unroll
+        for (int v = 0; v < kCols / 128; ++v) gone |= v < held && fabsf(y[v]) == INFINITY;
+        const bool clear = __any_sync(0xffffffffu, gone);
         asm volatile("cp.async.wait_all;" ::: "memory");
+        if (clear) {
+          __syncwarp();
+#pragma unroll
+          for (int v = 0; v < kCols / 128; ++v) {
+            if (!(v < held && fabsf(y[v]) == INFINITY)) continue;
+#pragma unroll 1
+            for (int k = 0; k < 8 * L::kSlabs; ++k)
+              *reinterpret_cast<uint4*>(smem + L::kQ + (st * L::kSlabs + (k >> 3)) * L::kQSlab +
+                                        (cr + 128 * v) * 128 + 16 * (k & 7)) = make_uint4(0, 0, 0, 0);
+          }
+        }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full + st);

@@ -1,6 +1,8 @@
-"""GPU tests of the 8-bit K/V cache where a row that must not count holds what
-would spoil the others: zero rows moved between blocks whose scales lie far
-apart."""
+"""GPU tests of the 8-bit K/V cache where a row or a query that must not count
+holds what would spoil the others: zero rows moved between blocks whose scales
+lie far apart, NaN and infinities in queries without weight."""
+import math
+
 import numpy as np
 import pytest
 
@@ -50,3 +52,64 @@ def test_evict_keeps_zero_rows_zero_beside_rows_far_smaller(block, page, D, fmt,
         d.len = [keep]
         d.check()
         assert K.get_status(ws) == 0
+
+
+def _weights(p, q, lse, ws, q_len=None):
+    p.c.mass.fill_(3.0)
+    K.kv8_mass(p.c, q, lse, ws, q_len=q_len, decay=0.0)
+    assert K.get_status(ws) == 0
+    return p.c.mass.clone()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T,G,D,cap", [(3, 2, 64, 0), (5, 5, 128, 0), (12, 4, 64, 80000), (50, 2, 64, 0),
+                                       (90, 3, 128, 0), (310, 2, 128, 0)])
+def test_a_query_without_weight_adds_nothing_whatever_it_holds(T, G, D, cap, dtype):
+    """lse -inf or +inf: the query adds nothing, be it NaN, infinite or a number."""
+    B, Hkv = 2, 2
+    lens = [700, 333]
+    p = Pair(B, Hkv, D, max(cap, 720), 16, 0 if cap else 16, O.E4M3, seed=93)
+    ws = p.c.workspace(T, Hkv * G)
+    p.append(p.rows(700, Hkv, "bf16"), p.rows(700, Hkv, "bf16"), ws, lens=lens)
+    q = p.rows(T, Hkv * G, dtype, 0.7).cuda()
+    out, lse = torch.empty_like(q), torch.empty(B, T, Hkv * G, device="cuda")
+    K.kv8_attn(p.c, q, out, ws, lse=lse)
+    gone = torch.from_numpy(p.rng.random((B, T, Hkv * G)) < 0.3).cuda()
+    gone[0, 0, 0], gone[1, T - 1, 1], gone[1, 0] = True, True, True
+    sign = torch.from_numpy(p.rng.random((B, T, Hkv * G)) < 0.5).cuda()
+    lse = torch.where(gone, torch.where(sign, math.inf, -math.inf), lse)
+    want = _weights(p, q, lse, ws)
+    held = torch.zeros_like(want, dtype=torch.bool)
+    for b in range(B):
+        pages = [b] if p.table is None else p.table[b].tolist()
+        left = lens[b]
+        for g in pages:
+            held[g, :, :max(0, left)] = True
+            left -= held.shape[2]
+    assert torch.isfinite(want).all() and (want[held] >= 0).all()
+    for bad in (math.nan, math.inf, -math.inf):
+        spoiled = q.clone()
+        spoiled[gone] = bad
+        assert torch.equal(_weights(p, spoiled, lse, ws), want), bad
+        one = q.clone()
+        one[..., 7][gone] = bad
+        assert torch.equal(_weights(p, one, lse, ws), want), bad
+
+
+@pytest.mark.parametrize("T,G,D", [(9, 2, 64), (30, 1, 128), (40, 3, 64), (80, 8, 128)])
+def test_queries_in_front_of_the_first_row_add_nothing_whatever_they_hold(T, G, D):
+    """More queries than rows: the first ones see none."""
+    Hkv, n = 2, T - 4
+    p = Pair(1, Hkv, D, 720, 16, 16, O.INT8, seed=94)
+    ws = p.c.workspace(T, Hkv * G)
+    p.append(p.rows(n, Hkv, "bf16"), p.rows(n, Hkv, "bf16"), ws)
+    q = p.rows(T, Hkv * G, "f16", 0.7).cuda()
+    out, lse = torch.empty_like(q), torch.empty(1, T, Hkv * G, device="cuda")
+    K.kv8_attn(p.c, q, out, ws, lse=lse)
+    want = _weights(p, q, lse, ws)
+    assert torch.isfinite(want).all()
+    q[:, :4] = math.nan
+    again = torch.empty_like(lse)
+    K.kv8_attn(p.c, q, out, ws, lse=again)
+    assert torch.equal(again, lse) and (out[:, :4] == 0).all()
+    assert torch.equal(_weights(p, q, again, ws), want)
