@@ -799,9 +799,10 @@ __global__ void __launch_bounds__(kThreads, mass_ctas(NT)) kv8_mass_kernel(Decod
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const float z = s[u][i][2 * r + e] * kscale[i];       // exact: a power of two
-              float w = kv8_exp2(fmaf(z, mul[u][e], -l2[u][e]));
-              if (some && pos + row >= lim[u][e]) w = 0.0f;
-              sum = fmaf(w, gain[u][e], sum);
+              const float w = kv8_exp2(fmaf(z, mul[u][e], -l2[u][e]));
+              // (a hidden weight is left out and not taken as 0: its gain may be NaN)
+              const float with = fmaf(w, gain[u][e], sum);
+              sum = some && pos + row >= lim[u][e] ? sum : with;
             }
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);

@@ -113,3 +113,27 @@ def test_queries_in_front_of_the_first_row_add_nothing_whatever_they_hold(T, G, 
     K.kv8_attn(p.c, q, out, ws, lse=again)
     assert torch.equal(again, lse) and (out[:, :4] == 0).all()
     assert torch.equal(_weights(p, q, again, ws), want)
+    again[:, :4] = math.nan                     # nor does their lse count
+    assert torch.equal(_weights(p, q, again, ws), want)
+
+
+@pytest.mark.parametrize("T,G,D", [(5, 3, 64), (8, 1, 128), (6, 5, 128), (60, 3, 64), (90, 8, 128)])
+def test_a_nan_query_spoils_only_the_weights_of_rows_that_it_sees(T, G, D):
+    Hkv, n = 2, 500
+    p = Pair(1, Hkv, D, 720, 32, 32, O.E4M3, seed=95)
+    ws = p.c.workspace(T, Hkv * G)
+    p.append(p.rows(n, Hkv, "bf16"), p.rows(n, Hkv, "bf16"), ws)
+    q = p.rows(T, Hkv * G, "bf16", 0.7).cuda()
+    out, lse = torch.empty_like(q), torch.empty(1, T, Hkv * G, device="cuda")
+    K.kv8_attn(p.c, q, out, ws, lse=lse)
+    _weights(p, q, lse, ws)
+    want = [p.at("mass", 0, h)[:n] for h in range(Hkv)]
+    q[0, 1, 0, 3] = math.nan                    # token 1, head 0: of the first K/V head
+    K.kv8_attn(p.c, q, out, ws, lse=lse)
+    assert torch.isnan(lse[0, 1, 0]) and lse.isnan().sum() == 1
+    _weights(p, q, lse, ws)
+    got = [p.at("mass", 0, h)[:n] for h in range(Hkv)]
+    sees = n - T + 2
+    assert np.isnan(got[0][:sees]).all()
+    assert np.array_equal(got[0][sees:], want[0][sees:])
+    assert np.array_equal(got[1], want[1])
