@@ -524,7 +524,8 @@ def kv8_mass(cache, q, lse, ws, q_len=None, softmax_scale=0.0, decay=1.0, stream
 def kv8_evict(cache, keep, sink, recent, kept, ws, dst=None, stream=None):
     """Cut every sequence to at most `keep` rows: the first `sink`, the last
     `recent`, and the heaviest by cache.mass between them, in place or into the
-    cache `dst`.  kept (int32 [batch, kv_heads, keep]): their former positions."""
+    cache `dst`, which shares no storage with `cache` (two paged ones: no page).
+    kept (int32 [batch, kv_heads, keep]): their former positions."""
     kp = _kv8_arg(cache, kept, "kept", "int32", (cache.batch, cache.kv_heads, keep))
     if kp is None or cache.mass is None:
         raise Csa2Error("csa2_kv8_evict: it takes `kept`, and a cache with mass")

@@ -95,6 +95,33 @@ bool overlap(const int32_t* a, const int32_t* b, int64_t n) {
   return a && x < y + 4 * n && y < x + 4 * n;
 }
 
+// Whether two caches whose places the host knows (at least one is contiguous)
+// have storage in common.  Two paged ones may lie in one pool of pages.
+bool shares_storage(const csa2_kv8_cache& a, const csa2_kv8_cache& b) {
+  if (a.page_size > 0 && b.page_size > 0) return false;
+  struct Range {
+    uintptr_t at, end;
+  };
+  auto ranges = [](const csa2_kv8_cache& c, Range (&r)[5]) {
+    const uintptr_t rows = (uintptr_t)(c.page_size > 0 ? c.num_pages : c.batch) * c.kv_heads *
+                           (c.page_size > 0 ? c.page_size : c.max_len);
+    const void* p[5] = {c.k_codes, c.v_codes, c.k_scales, c.v_scales, c.mass};
+    const uintptr_t bytes[5] = {rows * c.dim, rows * c.dim, rows / c.block * 4, rows / c.block * 4,
+                                c.mass ? rows * 4 : 0};
+    for (int i = 0; i < 5; ++i) {
+      r[i].at = reinterpret_cast<uintptr_t>(p[i]);
+      r[i].end = r[i].at + bytes[i];
+    }
+  };
+  Range x[5], y[5];
+  ranges(a, x);
+  ranges(b, y);
+  for (const Range& i : x)
+    for (const Range& j : y)
+      if (i.at < j.end && j.at < i.end) return true;
+  return false;
+}
+
 struct Kv8Ws {
   size_t status, old_len, part, total;
 };
@@ -208,7 +235,8 @@ csa2_status csa2_kv8_evict(const csa2_kv8_cache* cache, const csa2_kv8_cache* ds
   const csa2_kv8_cache* d = dst ? dst : cache;
   if (dst && (!kv8_ok(dst) || dst->batch != cache->batch || dst->kv_heads != cache->kv_heads ||
               dst->dim != cache->dim || dst->block != cache->block ||
-              dst->format != cache->format || dst->seq_len == cache->seq_len))
+              dst->format != cache->format ||
+              overlap(dst->seq_len, cache->seq_len, cache->batch) || shares_storage(*cache, *dst)))
     return CSA2_ERR_INVALID;
   if (keep > d->max_len) return CSA2_ERR_INVALID;
   uint8_t* w = static_cast<uint8_t*>(ws);

@@ -463,8 +463,9 @@ csa2_status csa2_kv8_mass(const csa2_kv8_cache *cache, const csa2_rows *q, int32
  * dst NULL: in place (keep <= max_len), seq_len[b] becomes keep; sequences with at most `keep`
  * rows are not touched.  Otherwise the rows go to dst, another cache of the
  * same batch, kv_heads, dim, block and format with max_len >= keep, whose
- * seq_len becomes min(seq_len, keep); it may lie in the same pool but shares no
- * page with `cache`, which stays as it is.
+ * seq_len becomes min(seq_len, keep).  It shares nothing with `cache`, which
+ * stays as it is: two paged caches may lie in one pool, on different pages (the
+ * caller's to see to); other storage in common is refused, as is a common seq_len.
  * A block of the result whose rows all keep their positions keeps its codes
  * and scale.  Any other holds what an append of its rows' values would give.
  * mass moves with the rows.  Rows behind the new length are left as they were.

@@ -54,6 +54,36 @@ def test_evict_keeps_zero_rows_zero_beside_rows_far_smaller(block, page, D, fmt,
         assert K.get_status(ws) == 0
 
 
+def test_evict_between_neighbours_in_one_allocation():
+    """Two contiguous caches whose arrays lie end to end share nothing."""
+    B, Hkv, D, n, keep, block = 2, 2, 64, 128, 48, 16
+    p = Pair(B, Hkv, D, n, block, 0, O.E4M3, seed=96)
+    d = Pair(B, Hkv, D, n, block, 0, O.E4M3, seed=97)
+    both = {}
+    for name in ("k_codes", "v_codes", "k_scales", "v_scales", "mass", "seq_len"):
+        both[name] = torch.cat([getattr(p.c, name), getattr(d.c, name)])
+    for i, x in ((0, p), (1, d)):
+        x.c = K.Cache8(B, Hkv, D, n, block=block, fmt=O.E4M3,
+                       tensors={k: t[i * B:(i + 1) * B] for k, t in both.items()})
+    ws = p.c.workspace(1, Hkv)
+    p.append(p.rows(100, Hkv, "f32"), p.rows(100, Hkv, "f32"), ws)
+    w = p.rng.random((B, Hkv, 100)).astype(np.float32)
+    p.set_mass(w)
+    kept = torch.empty(B, Hkv, keep, dtype=torch.int32, device="cuda")
+    K.kv8_evict(p.c, keep, 2, 9, kept, ws, dst=d.c)
+    for b in range(B):
+        for h in range(Hkv):
+            rows = O.evict(w[b, h], 100, keep, 2, 9)
+            for s in "kv":
+                d.seq[b, h, s] = p.seq[b, h, s].keep(rows)
+    d.len = [keep] * B
+    p.check()
+    d.check()
+    with pytest.raises(K.Csa2Error):
+        K.kv8_evict(p.c, keep, 2, 9, kept, ws, dst=p.c)
+    p.check()
+
+
 def _weights(p, q, lse, ws, q_len=None):
     p.c.mass.fill_(3.0)
     K.kv8_mass(p.c, q, lse, ws, q_len=q_len, decay=0.0)

@@ -1,0 +1,43 @@
+"""Refusals of the 8-bit K/V cache's calls, before any launch: arguments whose
+memory overlaps where the kernels read and write it without an order."""
+import ctypes
+
+import fp4_kv_cache_rope_gb300 as K
+
+
+def contiguous(at, seq_len):
+    """A contiguous cache of 2 x 4 x 1024 rows, its arrays one after another from
+    `at` on: 1 MiB of K, of V, 2 x 512 bytes of scales, 32 KiB of weights."""
+    mib = 1 << 20
+    return K.Csa2Kv8Cache(2, 4, 128, 64, 0, 0, 1024, 0, K.KV8_E4M3, at, at + mib, at + 2 * mib,
+                          at + 2 * mib + 512, at + 2 * mib + 1024, None, seq_len)
+
+
+def evict(a, b):
+    return K._kv8_evict(ctypes.byref(a), ctypes.byref(b), 100, 0, 0, 256, 256, None)
+
+
+def test_evict_refuses_another_cache_over_its_own_storage():
+    base = 1 << 30
+    size = (2 << 20) + 1024 + 2 * 4 * 1024 * 4
+    src = contiguous(base, 1 << 20)
+    for at in (base, base + 256, base - 256, base + (1 << 20), base - (1 << 20), base + (2 << 20),
+               base + size - 16, base - size + 16):
+        assert evict(src, contiguous(at, 1 << 21)) == K.CSA2_ERR_INVALID, at
+    # one array of one over another of the other
+    for field, value in [("k_codes", src.v_codes), ("v_codes", src.k_codes + (1 << 20) - 16),
+                         ("k_scales", src.mass), ("v_scales", src.k_scales), ("mass", src.v_codes + 64),
+                         ("mass", src.v_scales - 4)]:
+        d = contiguous(1 << 33, 1 << 21)
+        setattr(d, field, value)
+        assert evict(src, d) == K.CSA2_ERR_INVALID, field
+    # a contiguous cache inside a paged one's pool, either way round
+    pool = K.Csa2Kv8Cache.from_buffer_copy(src)
+    pool.page_size, pool.max_pages_per_seq, pool.num_pages, pool.page_table = 64, 16, 32, 512
+    inside = contiguous(1 << 33, 1 << 21)
+    inside.k_codes = pool.k_codes + (1 << 20) - 128
+    assert evict(pool, inside) == K.CSA2_ERR_INVALID
+    assert evict(inside, pool) == K.CSA2_ERR_INVALID
+    # seq_len apart by one of two entries
+    for off in (-4, 0, 4):
+        assert evict(src, contiguous(1 << 33, (1 << 20) + off)) == K.CSA2_ERR_INVALID, off
