@@ -64,6 +64,24 @@ bool rows_ok(const csa2_rows* r, bool wide) {
   const int64_t es = r->type == CSA2_F32 ? 4 : 2;
   return r->stride_b * es % 16 == 0 && r->stride_t * es % 16 == 0 && r->stride_h * es % 16 == 0;
 }
+// Whether no two rows of [B, T, H, D] overlap, by nested strides: each at least
+// what the dimensions with smaller ones extend over.
+bool rows_apart(const csa2_rows& r, int64_t B, int64_t T, int64_t H, int64_t D) {
+  const int64_t n[3] = {B, T, H}, stride[3] = {r.stride_b, r.stride_t, r.stride_h};
+  uint64_t extent = (uint64_t)D;
+  bool done[3] = {B <= 1, T <= 1, H <= 1};
+  auto size = [&](int i) { return stride[i] < 0 ? 0 - (uint64_t)stride[i] : (uint64_t)stride[i]; };
+  for (;;) {
+    int at = -1;
+    for (int i = 0; i < 3; ++i)
+      if (!done[i] && (at < 0 || size(i) < size(at))) at = i;
+    if (at < 0) return true;
+    const uint64_t st = size(at);
+    if (st < extent || st > ((uint64_t)1 << 62) / (uint64_t)n[at]) return false;
+    extent += st * (uint64_t)(n[at] - 1);
+    done[at] = true;
+  }
+}
 Kv8Rows rows_of(const csa2_rows& r) {
   return Kv8Rows{r.data, r.stride_b, r.stride_t, r.stride_h, r.type};
 }
@@ -193,7 +211,9 @@ csa2_status csa2_kv8_attn(const csa2_kv8_cache* cache, const csa2_rows* q, int32
     return CSA2_ERR_INVALID;
   if (!aligned(q_len, 4) || !aligned(lse, 4)) return CSA2_ERR_INVALID;
   if (T == 0) return CSA2_OK;
-  if (!rows_ok(q, false) || !rows_ok(out, false) || q->type != out->type) return CSA2_ERR_INVALID;
+  if (!rows_ok(q, false) || !rows_ok(out, false) || q->type != out->type ||
+      !rows_apart(*out, cache->batch, T, H, cache->dim))
+    return CSA2_ERR_INVALID;
   Kv8Attn a = attn_of(cache, q, H, T, q_len, softmax_scale, ws);
   a.out = rows_of(*out);
   a.lse = lse;

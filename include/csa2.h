@@ -389,7 +389,10 @@ typedef struct csa2_kv8_cache {
 #define CSA2_KV8_INT8 1
 
 /* Rows [B, T, heads, D] of a tensor whose last dimension is contiguous; the
- * strides are in elements.  data and the strides in bytes are multiples of 16. */
+ * strides are in elements.  data and the strides in bytes are multiples of 16.
+ * Rows that are read may overlap (a stride of 0 repeats one).  Rows that are
+ * written may not: each stride is at least what the dimensions with smaller ones
+ * extend over. */
 typedef struct csa2_rows {
   void *data;
   int64_t stride_b, stride_t, stride_h;
@@ -434,7 +437,9 @@ csa2_status csa2_kv8_append(const csa2_kv8_cache *cache, const csa2_rows *k, con
  *   o = sum_j softmax_j(softmax_scale * q . k_j) v_j
  *   lse (fp32 [B, T, H] or NULL) = ln sum_j exp(softmax_scale * q . k_j)
  * A query that sees no row gives zeros and lse = -inf.  out and lse behind
- * q_len[b] are left as they were.  softmax_scale <= 0 selects 1/sqrt(D).
+ * q_len[b] are left as they were.  out may be q itself (the same rows at the same
+ * places); otherwise it shares no memory with q.  softmax_scale <= 0 selects
+ * 1/sqrt(D).
  * Rows on a page outside [0, num_pages) are left out (CSA2_DEV_BAD_PAGE).
  */
 csa2_status csa2_kv8_attn(const csa2_kv8_cache *cache, const csa2_rows *q, int32_t H, int32_t T,

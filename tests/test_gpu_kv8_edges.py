@@ -167,3 +167,29 @@ def test_a_nan_query_spoils_only_the_weights_of_rows_that_it_sees(T, G, D):
     assert np.isnan(got[0][:sees]).all()
     assert np.array_equal(got[0][sees:], want[0][sees:])
     assert np.array_equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("T", [1, 5, 70])
+def test_attention_takes_every_output_without_overlap(T):
+    B, Hkv, G, D = 2, 2, 4, 64
+    H = Hkv * G
+    p = Pair(B, Hkv, D, 400, 16, 16, O.E4M3, seed=98)
+    ws = p.c.workspace(T, H)
+    p.append(p.rows(300, Hkv, "bf16"), p.rows(300, Hkv, "bf16"), ws)
+    q = p.rows(T, H, "bf16").cuda()
+    want = torch.empty_like(q)
+    K.kv8_attn(p.c, q, want, ws)
+    def full(*s): return torch.full(s, 7.0, dtype=q.dtype, device="cuda")  # noqa: E704
+    fused = full(B, T, 3 * H, D)
+    for out in (full(T, H, B, D).permute(2, 0, 1, 3), full(H, B, T, D).permute(1, 2, 0, 3),
+                full(B, H, T, D).transpose(1, 2), fused[:, :, H:2 * H], full(B, T, H, D + 8)[..., :D],
+                full(B, 2 * T, H, D)[:, ::2], full(B, T, 2 * H, D)[:, :, 1::2]):
+        K.kv8_attn(p.c, q, out, ws)
+        assert torch.equal(out, want)
+    assert (fused[:, :, :H] == 7.0).all() and (fused[:, :, 2 * H:] == 7.0).all()
+    one = q[:1, :1, :1].expand(B, T, H, D)          # a query that repeats
+    K.kv8_attn(p.c, one, want, ws)
+    assert torch.isfinite(want).all()
+    for shape in ((1, T, H, D), (B, T, 1, D)) + (((B, 1, H, D),) if T > 1 else ()):
+        with pytest.raises(K.Csa2Error):
+            K.kv8_attn(p.c, q, full(*shape).expand(B, T, H, D), ws)

@@ -41,3 +41,22 @@ def test_evict_refuses_another_cache_over_its_own_storage():
     # seq_len apart by one of two entries
     for off in (-4, 0, 4):
         assert evict(src, contiguous(1 << 33, (1 << 20) + off)) == K.CSA2_ERR_INVALID, off
+
+
+def test_attention_refuses_outputs_whose_rows_overlap():
+    """q may repeat rows; out may not."""
+    c = contiguous(1 << 30, 1 << 20)
+    c.dim, B, T, H = 64, 2, 3, 8
+    D = c.dim
+    q = K.Csa2Rows(1 << 31, 0, 0, 0, K.BF16)
+
+    def attn(sb, st, sh, T=T, H=H):
+        out = K.Csa2Rows(1 << 32, sb, st, sh, K.BF16)
+        return K._kv8_attn(ctypes.byref(c), ctypes.byref(q), H, T, None, 0.0, ctypes.byref(out), None, 256,
+                           None)
+
+    for strides in [(0, H * D, D), (T * H * D, 0, D), (T * H * D, H * D, 0), (T * H * D, H * D, 8),
+                    (T * H * D, D, D), (H * D, H * D, D), (T * H * D - 8, H * D, D),
+                    (T * H * D, H * D, -8), (D, 2 * D, 6 * D + 8 - D), (1 << 62, H * D, D),
+                    (-(1 << 63), H * D, D), (0, 0, 0)]:
+        assert attn(*strides) == K.CSA2_ERR_INVALID, strides
