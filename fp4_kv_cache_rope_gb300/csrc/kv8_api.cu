@@ -157,6 +157,12 @@ bool heads_ok(const csa2_kv8_cache* c, int32_t T, int32_t H) {
          (int64_t)c->batch * H * (T + 1) < (int64_t)1 << 31;
 }
 
+// The kernels' factor is the scale times log2(e), in fp32: beyond that range, and
+// where it would lose bits, there is none.
+bool scale_ok(float scale) {
+  return scale <= 0.0f || (scale >= 0x1p-100f && scale <= 0x1p100f);
+}
+
 Kv8Attn attn_of(const csa2_kv8_cache* c, const csa2_rows* q, int32_t H, int32_t T,
                 const int32_t* q_len, float scale, void* ws) {
   Kv8Attn a{};
@@ -207,7 +213,7 @@ csa2_status csa2_kv8_append(const csa2_kv8_cache* cache, const csa2_rows* k, con
 csa2_status csa2_kv8_attn(const csa2_kv8_cache* cache, const csa2_rows* q, int32_t H, int32_t T,
                           const int32_t* q_len, float softmax_scale, const csa2_rows* out,
                           float* lse, void* ws, void* stream) {
-  if (!kv8_ok(cache) || !ws || !aligned(ws, 256) || !heads_ok(cache, T, H) || isnan(softmax_scale))
+  if (!kv8_ok(cache) || !ws || !aligned(ws, 256) || !heads_ok(cache, T, H) || !scale_ok(softmax_scale))
     return CSA2_ERR_INVALID;
   if (!aligned(q_len, 4) || !aligned(lse, 4)) return CSA2_ERR_INVALID;
   if (T == 0) return CSA2_OK;
@@ -228,7 +234,7 @@ csa2_status csa2_kv8_mass(const csa2_kv8_cache* cache, const csa2_rows* q, int32
                           const int32_t* q_len, const float* lse, float softmax_scale, float decay,
                           void* ws, void* stream) {
   if (!kv8_ok(cache) || !cache->mass || !ws || !aligned(ws, 256) || !heads_ok(cache, T, H) ||
-      isnan(softmax_scale) || !(decay >= 0.0f && decay <= 1.0f))
+      !scale_ok(softmax_scale) || !(decay >= 0.0f && decay <= 1.0f))
     return CSA2_ERR_INVALID;
   if (!aligned(q_len, 4) || !aligned(lse, 4)) return CSA2_ERR_INVALID;
   if (T > 0 && (!rows_ok(q, false) || !lse)) return CSA2_ERR_INVALID;

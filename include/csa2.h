@@ -439,7 +439,7 @@ csa2_status csa2_kv8_append(const csa2_kv8_cache *cache, const csa2_rows *k, con
  * A query that sees no row gives zeros and lse = -inf.  out and lse behind
  * q_len[b] are left as they were.  out may be q itself (the same rows at the same
  * places); otherwise it shares no memory with q.  softmax_scale <= 0 selects
- * 1/sqrt(D).
+ * 1/sqrt(D); a positive one lies within 2^-100 .. 2^100.
  * Rows on a page outside [0, num_pages) are left out (CSA2_DEV_BAD_PAGE).
  */
 csa2_status csa2_kv8_attn(const csa2_kv8_cache *cache, const csa2_rows *q, int32_t H, int32_t T,

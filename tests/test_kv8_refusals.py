@@ -1,6 +1,8 @@
 """Refusals of the 8-bit K/V cache's calls, before any launch: arguments whose
-memory overlaps where the kernels read and write it without an order."""
+memory overlaps where the kernels read and write it without an order, and
+numbers that the kernels cannot work with."""
 import ctypes
+import math
 
 import fp4_kv_cache_rope_gb300 as K
 
@@ -60,3 +62,16 @@ def test_attention_refuses_outputs_whose_rows_overlap():
                     (T * H * D, H * D, -8), (D, 2 * D, 6 * D + 8 - D), (1 << 62, H * D, D),
                     (-(1 << 63), H * D, D), (0, 0, 0)]:
         assert attn(*strides) == K.CSA2_ERR_INVALID, strides
+
+
+def test_softmax_scales_out_of_range():
+    c = contiguous(1 << 30, 1 << 20)
+    r = K.Csa2Rows(1 << 31, 8 * 128, 8 * 128, 128, K.BF16)
+    for scale in (math.inf, math.nan, 3.0e38, 2.0 ** 101, 1e-40, 2.0 ** -101):
+        assert K._kv8_attn(ctypes.byref(c), ctypes.byref(r), 8, 1, None, scale, ctypes.byref(r), None, 256,
+                           None) == K.CSA2_ERR_INVALID, scale
+        assert K._kv8_mass(ctypes.byref(c), ctypes.byref(r), 8, 1, None, 256, scale, 1.0, 256,
+                           None) == K.CSA2_ERR_INVALID, scale
+    # no query rows: nothing is launched for a scale that is taken
+    for scale in (0.0, -1.0, 2.0 ** -100, 0.125, 2.0 ** 100):
+        assert K._kv8_attn(ctypes.byref(c), None, 8, 0, None, scale, None, None, 256, None) == K.CSA2_OK
