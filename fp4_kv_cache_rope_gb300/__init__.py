@@ -373,6 +373,8 @@ class Cache8:
         if tensors is None:
             tensors = {n: torch.zeros(shape, dtype=dt, device=device)
                        for n, (dt, shape) in shapes.items() if n != "mass" or mass}
+        if tensors.get("seq_len") is None:
+            raise Csa2Error("Cache8: the given storage lacks seq_len")
         device = tensors["seq_len"].device
         for n, (dt, shape) in shapes.items():
             t = tensors.get(n)

@@ -4,6 +4,9 @@ numbers that the kernels cannot work with."""
 import ctypes
 import math
 
+import pytest
+import torch
+
 import fp4_kv_cache_rope_gb300 as K
 
 
@@ -75,3 +78,13 @@ def test_softmax_scales_out_of_range():
     # no query rows: nothing is launched for a scale that is taken
     for scale in (0.0, -1.0, 2.0 ** -100, 0.125, 2.0 ** 100):
         assert K._kv8_attn(ctypes.byref(c), None, 8, 0, None, scale, None, None, 256, None) == K.CSA2_OK
+
+
+@pytest.mark.parametrize("missing", ["k_codes", "v_codes", "k_scales", "v_scales", "seq_len"])
+def test_a_cache_over_given_storage_names_what_is_missing(missing):
+    c = K.Cache8(2, 4, 64, 128, block=32, mass=True, device="cpu")
+    given = {n: getattr(c, n) for n in ("k_codes", "v_codes", "k_scales", "v_scales", "mass", "seq_len")}
+    assert K.Cache8(2, 4, 64, 128, block=32, tensors=given).mass is c.mass
+    for gone in ({n: t for n, t in given.items() if n != missing}, given | {missing: None}):
+        with pytest.raises(K.Csa2Error, match=missing):
+            K.Cache8(2, 4, 64, 128, block=32, tensors=gone)
