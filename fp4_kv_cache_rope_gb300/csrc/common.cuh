@@ -165,11 +165,21 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
                "r"(bytes)
                : "memory");
 }
+// The hardware suspends a try for longer than a phase of most kernels takes, so a
+// very short limit is not looked at before the phase is over.  A build with
+// CSA2_POLLED_WAITS polls instead, so that tests can make any wait run out.
+#ifdef CSA2_POLLED_WAITS
+#define CSA2_MBAR_TRY "mbarrier.test_wait.parity.shared::cta.b64"
+constexpr uint32_t kTriesPerLook = 1;
+#else
+#define CSA2_MBAR_TRY "mbarrier.try_wait.parity.shared::cta.b64"
+constexpr uint32_t kTriesPerLook = 8;
+#endif
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n.reg .pred p;\n"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      CSA2_MBAR_TRY " p, [%1], %2;\n"
       "selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
@@ -189,7 +199,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   const uint64_t lim = g_wait_ns;
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 7) == 0) {
+    if (i % kTriesPerLook == 0) {
       if (*abort) return false;
       if (globaltimer() - t0 > lim) {
         *abort = 1;

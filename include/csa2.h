@@ -453,6 +453,8 @@ csa2_status csa2_kv8_attn(const csa2_kv8_cache *cache, const csa2_rows *q, int32
  * with q, q_len and softmax_scale as given to csa2_kv8_attn, whose lse it takes
  * (fp32 [B, T, H]; a query with lse = -inf or +inf adds nothing).  decay 1 accumulates,
  * 0 starts anew (whatever mass held).  Rows behind seq_len are left as they were.
+ * After CSA2_DEV_TIMEOUT some rows' mass is updated and some is not: such a call may
+ * be repeated with decay 0 alone.
  */
 csa2_status csa2_kv8_mass(const csa2_kv8_cache *cache, const csa2_rows *q, int32_t H, int32_t T,
                           const int32_t *q_len, const float *lse, float softmax_scale, float decay,
