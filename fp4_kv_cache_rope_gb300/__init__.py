@@ -512,7 +512,8 @@ def kv8_attn(cache, q, out, ws, lse=None, q_len=None, softmax_scale=0.0, stream=
 
 def kv8_mass(cache, q, lse, ws, q_len=None, softmax_scale=0.0, decay=1.0, stream=None):
     """cache.mass = decay * cache.mass + the weight that each row got from the
-    queries q, given the lse that kv8_attn returned for them."""
+    queries q, given the lse that kv8_attn returned for them.  Pages that two
+    sequences share lose updates: weights need pages of their own."""
     rq, T = _kv8_rows(cache, q, "q")
     H = q.shape[2]
     if cache.mass is None or lse is None:

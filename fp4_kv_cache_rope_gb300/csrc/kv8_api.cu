@@ -224,8 +224,8 @@ csa2_status csa2_kv8_attn(const csa2_kv8_cache* cache, const csa2_rows* q, int32
   a.out = rows_of(*out);
   a.lse = lse;
   // Up to 64 query rows per (sequence, K/V head) go to the kernel that is bound by
-  // the cache's bytes (16 sequences of 9000 rows, D 128: 63 us for 48 rows, 80 us
-  // for 64), more to the tensor cores' (80 us for up to 128).
+  // the cache's bytes, more to the tensor cores' (16 sequences of 9000 rows, 4 heads,
+  // D 128: 62 us against 80 us for 48 rows, 78 against 80 for 64, 92 against 82 for 80).
   return done(a.T * a.G <= 64 ? launch_kv8_attn(a, sms(), (cudaStream_t)stream)
                               : launch_kv8_prefill(a, sms(), (cudaStream_t)stream));
 }
@@ -243,7 +243,7 @@ csa2_status csa2_kv8_mass(const csa2_kv8_cache* cache, const csa2_rows* q, int32
   a.decay = decay;
   // Up to 32 query rows per (sequence, K/V head) stay in a warp's registers: 16
   // sequences of 9000 rows, 4 heads, D 128 take 34 us with 32 rows, the tensor
-  // cores' kernel 97 us with any number up to 256.  Up to 64 in two launches is
+  // cores' kernel 97 us with 32 and 99 us with 64.  Up to 64 in two launches is
   // faster too (63 us with 64 rows), unless the cache is so small that the
   // launches are what takes the time (2 sequences of 2000: 24 us against 13 us).
   const int64_t tiles = (int64_t)cache->batch * cache->kv_heads * ((cache->max_len + 127) / 128);

@@ -18,10 +18,10 @@
 //
 // Exactness.  Queries are scaled per row by a power of two into f16's range
 // (the logit factor absorbs it); logits, maxima, sums and outputs are fp32.
-// The running maximum is raised when a logit exceeds it by 2^8.  The weights P
-// go to f16 for the P V product times 2^7 and times the block's V scale over
-// the largest V scale so far: at most 2^15, with f16's full 11 bits down to
-// 2^-21; their sum is taken in fp32 before that rounding.
+// The running maximum is raised when a base-2 logit exceeds it by 8 (a weight of
+// 2^8).  The weights P go to f16 for the P V product times 2^7 and times the block's
+// V scale over the largest V scale so far: at most 2^15, with f16's full 11 bits
+// down to 2^-21; their sum is taken in fp32 before that rounding.
 //
 // Measured at D 128 and 8 K/V heads, one token a sequence: 32 sequences of up to
 // 32768 rows 234 us (6.4 TB/s, 94% of a copy's), 8 of 131072 315 us (6.8 TB/s).

@@ -27,7 +27,9 @@
 // f makes up for; and with few queries D 128 goes in two chains that are added
 // here.  Errors (norm): 55 tokens of 8 heads on 61176 rows 3.1e-6 as it is, 1.7e-6
 // made up for, 1.1e-6 in two chains, 1.2e-6 by rounded fp32 sums; 1249 tokens of 4
-// heads 1.0e-6, 0.31e-6, 0.20e-6, 0.23e-6.
+// heads 1.0e-6, 0.31e-6, 0.20e-6, 0.23e-6.  Sums whose products share a sign lose
+// two to four times as much, so that a part of it is left (logits of 35, bf16, two
+// chains: 7.9e-7 as it is, 4.3e-7 made up for; f16, one chain: 4.6e-6, 2.6e-6).
 //
 // A cached row is one thread's in each of four warp groups: even and odd query
 // tiles, left and right half of their columns.  Their four sums are added in a
@@ -36,12 +38,11 @@
 //
 // Warps (768 threads): 0-15 exponentials; 16-19 copy queries (16 bytes at a
 // time, asynchronously, into a ring); 20-22 turn K's codes into one of two
-// operand tiles; 23 issues the MMAs.  With few query tiles to an item it is
-// the loading that takes the time: a second K tile, warps of its own for K and
-// an item's codes asked for one item ahead took 100 tokens of 4 heads on 8
-// caches of 16384 rows from 120 to 73 us, 90 tokens of 2 on 21 of 120721 from
-// 1312 to 837 us (a prompt of 4096 on itself, up to 64 tiles to an item: 95 to
-// 91).
+// operand tiles; 23 issues the MMAs.  With few query tiles to an item it is the
+// loading that takes the time: hence a second K tile, warps of its own for K and
+// an item's codes asked for one item ahead.  100 tokens of 4 heads on 8 caches of
+// 16384 rows take 72 us (120 us before these three), 90 tokens of 2 on 21 of
+// 120721 849 us (1312 us).
 #include <type_traits>
 
 #include "kv8_mma.cuh"
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_many_kernel(MassParams p
                          "l"(from + 128 * s), "r"(size)
                          : "memory");
         };
-        if (g16 == 0) {   // 16 rows on are whole tokens: fewer instructions (91 -> 89 us)
+        if (g16 == 0) {   // 16 rows on are whole tokens: fewer instructions (a prompt: 86 -> 82 us)
           const char* from = qsrc + 2 * pq.off;
           const int left = it.rows - pq.r;
 #pragma unroll 4
@@ -602,8 +603,8 @@ cudaError_t mass_of(const Kv8Attn& a, int ctas, cudaStream_t s) {
   // Two accumulators up to 512 query rows, where the weight of a row can come from
   // a few queries and with it all their logits' error: 3.2e-6 of the weights in
   // one, 1.3e-6 in rounded fp32 sums (90 tokens of 2 heads on 120721 rows); the time
-  // is the same, 837 us against 853 us.  With more the errors average, 0.3e-6 for a
-  // prompt of 4096 in one, and tiles of 256 queries are faster: 89 against 110 us.
+  // is not longer, 849 us against 938 us.  With more the errors average, 0.3e-6 for a
+  // prompt of 4096 in one, and tiles of 256 queries are faster: 82 against 105 us.
   return a.T * a.G <= 512 ? mass_as<128, 2, FMT>(a, ctas, s) : mass_as<128, 1, FMT>(a, ctas, s);
 }
 

@@ -25,7 +25,7 @@
 // none per cached row, is left for the softmax.  A block whose scale is 2^12
 // below the largest still keeps every bit; below that a value is off by at most
 // 2^-25 of that largest scale, i.e. by 2^-31 of the range's largest value.
-// The running maximum is raised only when a logit exceeds it by 2^8 (the rare
+// The running maximum is raised only when a base-2 logit exceeds it by 8 (the rare
 // rescaling of O stays off the common path), and P is taken times 2^7: at most
 // 2^15, with f16's full precision down to 2^-21.  l is summed in fp32 from the
 // unrounded weights.

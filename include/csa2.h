@@ -346,9 +346,9 @@ csa2_status csa2_attn_prefill(const csa2_cache *cache, const uint16_t *q, int32_
                               float *out, void *ws, void *stream);
 
 /* ------------------------------------------------------------------------
- * A K/V cache of grouped heads in 8 bits, for the layers with ordinary (dense)
- * attention beside the CSA2 layers.  Hkv heads of K and of V rows of D
- * channels each; H = Hkv * G query heads, query head h reads K/V head h / G.
+ * A K/V cache of grouped heads in 8 bits, for models with ordinary (dense)
+ * grouped-head attention.  Hkv heads of K and of V rows of D channels each;
+ * H = Hkv * G query heads, query head h reads K/V head h / G.
  *
  * Storage.  Row r of page g and head h is at row index (g * Hkv + h) * P + r
  * with P = page_size (paged) or max_len (page_size 0: page g is sequence g):
@@ -364,8 +364,22 @@ csa2_status csa2_attn_prefill(const csa2_cache *cache, const uint16_t *q, int32_
  * for E4M3, 127 for INT8), and 0 for amax = 0 (all codes 0).  A value's code is
  * the format's nearest to value / scale, ties to even.
  *
- * Sequences whose page-table rows name a common page may share it for reading.
- * A page that csa2_kv8_append or csa2_kv8_evict writes must be in one row only.
+ * Sequences whose page-table rows name a common page may share it for reading
+ * (csa2_kv8_attn).  A page that csa2_kv8_append, csa2_kv8_evict or csa2_kv8_mass
+ * writes must be in one row only, and there once: mass is read, changed and
+ * written without an order between sequences, so on a shared page updates are
+ * lost.  Weights of sequences with a common prefix need pages of their own for it.
+ *
+ * Precision.  Sums, maxima, normalisers and weights are fp32; outputs are rounded
+ * to their type once.  Weights are rounded to f16 for the product with V, and where
+ * scales differ, K and V are held relative to the largest scale among the rows that
+ * a CTA works on, seen by the query or not: with many query rows a value is off by
+ * at most 2^-31 of the largest there, and with any a weight times its value by 2^-31
+ * of the largest weight times it.  csa2_kv8_mass with many query rows takes the
+ * queries as they are, and K, for f16 queries, to within 2^-24 of the largest value
+ * of 128 rows: sums of |q k| beyond fp32's range overflow there.  Which kernel runs, and with it the last bits of a result, depends on
+ * shapes and on max_len, never on contents or on earlier calls: the same call gives
+ * the same bits, a cache of another capacity may not.
  */
 typedef struct csa2_kv8_cache {
   int32_t batch;              /* B sequences */

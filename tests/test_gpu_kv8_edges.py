@@ -193,3 +193,38 @@ def test_attention_takes_every_output_without_overlap(T):
     for shape in ((1, T, H, D), (B, T, 1, D)) + (((B, 1, H, D),) if T > 1 else ()):
         with pytest.raises(K.Csa2Error):
             K.kv8_attn(p.c, q, full(*shape).expand(B, T, H, D), ws)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("T,G,D", [(3, 2, 128), (9, 3, 64), (60, 4, 128), (60, 4, 64), (150, 4, 128)])
+def test_weights_of_logits_whose_products_share_a_sign(T, G, D, sign, dtype):
+    """Sums that grow steadily lose more to an accumulator that cuts off than sums
+    that cancel.  Each product may lose a step of the sum, 2^-23 of it: D 2^-23 of
+    the logit, and 4 more for its factor; lse times log2 e, exp2 and the additions
+    of T G weights as in any other weight."""
+    Hkv, n = 2, 900
+    p = Pair(1, Hkv, D, 960, 64, 64, O.E4M3, seed=99)
+    ws = p.c.workspace(T, Hkv * G)
+    p.append(*(p.rows(n, Hkv, "f32").abs() for _ in "kv"), ws)
+    q = sign * p.rows(T, Hkv * G, dtype).abs()
+    k = [p.seq[0, h, "k"].values() for h in range(Hkv)]
+    lse = np.zeros((T, Hkv * G))
+    scale = 25 / max((np.abs(q[0].double().numpy()) @ k[0].T).mean(), 1e-9)
+    qn = q[0].double().numpy()
+    for h in range(Hkv):
+        hs = slice(h * G, (h + 1) * G)
+        lse[:, hs] = O.attention(qn[:, hs], k[h], k[h], scale)[1]
+    lse = lse.astype(np.float32)
+    K.kv8_mass(p.c, q.cuda(), torch.from_numpy(lse)[None].cuda(), ws, softmax_scale=scale, decay=0.0)
+    assert K.get_status(ws) == 0
+    scale = float(np.float32(scale))
+    for h in range(Hkv):
+        hs = slice(h * G, (h + 1) * G)
+        want = O.mass(qn[:, hs], lse[:, hs].astype(np.float64), k[h], scale)
+        big = scale * (np.abs(qn[:, hs]).reshape(-1, D) @ k[h].T).max()
+        rel = ((D + 4) * 2.0 ** -23 * big + 2.0 ** -22 * np.abs(lse).max() + 2.0 ** -20
+               + (T * G + 2) * 2.0 ** -23)
+        got = p.at("mass", 0, h)[:n].astype(np.float64)
+        assert (np.abs(got - want) <= rel * want + 1e-36).all(), np.max(np.abs(got - want) / (want + 1e-36)) / rel
+
