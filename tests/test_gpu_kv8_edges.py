@@ -14,7 +14,7 @@ if not torch.cuda.is_available():
 
 import fp4_kv_cache_rope_gb300 as K  # noqa: E402
 from oracle import kv8 as O  # noqa: E402
-from kv8_tools import Pair  # noqa: E402
+from kv8_tools import Pair, attention_bounds  # noqa: E402
 
 
 @pytest.mark.parametrize("into", ["place", "cache"])
@@ -228,3 +228,98 @@ def test_weights_of_logits_whose_products_share_a_sign(T, G, D, sign, dtype):
         got = p.at("mass", 0, h)[:n].astype(np.float64)
         assert (np.abs(got - want) <= rel * want + 1e-36).all(), np.max(np.abs(got - want) / (want + 1e-36)) / rel
 
+
+def test_lengths_out_of_range_are_clamped():
+    """q_len and new_len below 0 and above T, seq_len below 0 and above the capacity."""
+    B, Hkv, G, D, cap = 4, 2, 2, 64, 96
+    H = Hkv * G
+    p = Pair(B, Hkv, D, cap, 16, 16, O.INT8, seed=101)
+    ws = p.c.workspace(40, H)
+    p.append(p.rows(cap, Hkv, "bf16"), p.rows(cap, Hkv, "bf16"), ws)
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    for T in (3, 40):
+        q = p.rows(T, H, "f16", 0.7).cuda()
+        got = []
+        for lens, q_len in (([96, 96, 0, 50], [0, T, T, 1]), ([2 ** 30, 97, -7, 50], [-2 ** 31, 2 ** 31 - 1, T + 1, 1])):
+            p.c.seq_len.copy_(ints(lens))
+            out, lse = torch.full_like(q, 7.0), torch.full((B, T, H), 7.0, device="cuda")
+            K.kv8_attn(p.c, q, out, ws, lse=lse, q_len=ints(q_len))
+            p.c.mass.fill_(0.5)
+            K.kv8_mass(p.c, q, lse, ws, q_len=ints(q_len), decay=0.5)
+            assert p.c.seq_len.tolist() == lens
+            got.append((out, lse, p.c.mass.clone()))
+        assert all(torch.equal(x, y) for x, y in zip(*got))
+        assert (got[0][0][0] == 7.0).all() and (got[0][0][2] == 0).all()
+        k = p.rows(T, Hkv, "f16").cuda()
+        start = ints([10, 20, 30, 40])
+        stored = []
+        for new in ([0, T, T, 1], [-5, 2 ** 31 - 1, T + 9, 1]):
+            K.kv8_append(p.c, k, k, ws, new_len=ints(new), start=start)
+            assert p.c.seq_len.tolist() == [10, 20 + T, 30 + T, 41]
+            # (bits: unused pages' scales are NaN)
+            stored.append([t.view(torch.uint8).clone()
+                           for t in (p.c.k_codes, p.c.v_codes, p.c.k_scales, p.c.v_scales)])
+        assert all(torch.equal(x, y) for x, y in zip(*stored))
+    assert K.get_status(ws) == 0
+
+
+def test_weights_of_no_queries_decay():
+    p = Pair(2, 2, 64, 200, 16, 16, O.E4M3, seed=102)
+    ws = p.c.workspace(1, 4)
+    p.append(p.rows(130, 2, "bf16"), p.rows(130, 2, "bf16"), ws, lens=[130, 7])
+    p.c.mass.fill_(3.0)
+    q, lse = torch.zeros(2, 0, 4, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, 0, 4, device="cuda")
+    K.kv8_mass(p.c, q, lse, ws, decay=0.5)
+    for b, n in ((0, 130), (1, 7)):
+        for h in range(2):
+            m = p.at("mass", b, h)
+            assert (m[:n] == 1.5).all() and (m[n:] == 3.0).all()
+    assert K.get_status(ws) == 0
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("T,G", [(3, 4), (40, 2)])
+def test_storage_beyond_4_gib(T, G, paged):
+    """K and V of 5 GiB each, of which the last rows are used."""
+    B, Hkv, D, block = (40, 8, 128, 64) if not paged else (3, 8, 128, 64)
+    H, page = Hkv * G, 64
+    cap = 131072 if not paged else 4096
+    if paged:
+        pages = 5 * 2 ** 30 // (Hkv * page * D)
+        table = torch.arange(pages - 1, pages - 1 - B * cap // page, -1, dtype=torch.int32).view(B, -1)
+    p = Pair(1 if paged else B, Hkv, D, block, block, 0, O.E4M3, seed=103)
+    p.B, p.table = B, table if paged else None
+    p.c = K.Cache8(B, Hkv, D, cap, block=block, page_size=page if paged else 0,
+                   page_table=table if paged else None, num_pages=pages if paged else 0, fmt=O.E4M3, mass=True)
+    assert p.c.k_codes.numel() > 2 ** 32
+    p.seq = {(b, h, s): O.Seq(block, O.E4M3, D) for b in range(B) for h in range(Hkv) for s in "kv"}
+    lens = [0] * (B - 2) + [300, 131]
+    p.len = [0] * B
+    ws = p.c.workspace(T, H)
+    p.append(p.rows(300, Hkv, "bf16"), p.rows(300, Hkv, "bf16"), ws, lens=lens)
+    p.append(p.rows(2, Hkv, "bf16"), p.rows(2, Hkv, "bf16"), ws, lens=[0] * (B - 1) + [2])
+    p.check()
+    q = p.rows(T, H, "bf16", 0.7)
+    out, lse = torch.empty(B, T, H, D, dtype=q.dtype, device="cuda"), torch.empty(B, T, H, device="cuda")
+    K.kv8_attn(p.c, q.cuda(), out, ws, lse=lse)
+    K.kv8_mass(p.c, q.cuda(), lse, ws, decay=0.0)
+    for b in (B - 2, B - 1):
+        for h in range(Hkv):
+            hs = slice(h * G, (h + 1) * G)
+            ro, rl, tol, ltol = attention_bounds(q[b, :, hs].double().numpy(), p, b, h, G, T, 1 / math.sqrt(D),
+                                                 2.0 ** -8)
+            assert (np.abs(out[b, :, hs].cpu().double().numpy() - ro) <= tol).all()
+            assert (np.abs(lse[b, :, hs].cpu().double().numpy() - rl) <= ltol).all()
+            m = p.at("mass", b, h)[: p.len[b]].astype(np.float64)
+            assert abs(m.sum() - T * G) < 1e-4 * T * G
+    kept = torch.empty(B, Hkv, 100, dtype=torch.int32, device="cuda")
+    w = {(b, h): p.at("mass", b, h) for b in (B - 2, B - 1) for h in range(Hkv)}
+    K.kv8_evict(p.c, 100, 4, 16, kept, ws)
+    for (b, h), x in w.items():
+        rows = O.evict(x, p.len[b], 100, 4, 16)
+        assert kept[b, h].tolist() == rows.tolist()
+        for s in "kv":
+            p.seq[b, h, s] = p.seq[b, h, s].keep(rows)
+    p.len[B - 2:] = [100, 100]
+    p.check()
+    assert K.get_status(ws) == 0
