@@ -24,7 +24,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 CSA2_OK, CSA2_ERR_INVALID, CSA2_ERR_CUDA, CSA2_ERR_UNSUPPORTED, CSA2_ERR_TIMEOUT, CSA2_ERR_DEVICE = range(6)
 DEV_BAD_INDEX, DEV_BAD_PAGE, DEV_OVERFLOW, DEV_TIMEOUT, DEV_BAD_POOL, DEV_BAD_ALIGN = (
     0x1, 0x2, 0x4, 0x8, 0x10, 0x20)
-DEV_NONFINITE = 0x40
+DEV_NONFINITE, DEV_BAD_TREE = 0x40, 0x80
 MAX_TOPK = 2048
 POOL_BLOCKS = 2048
 BLOCK = 8
@@ -64,7 +64,19 @@ class Csa2Rows(ctypes.Structure):
                 ("type", _i32)]
 
 
+class Csa2Rope(ctypes.Structure):
+    _fields_ = [("cos", _p), ("sin", _p), ("positions", _i32), ("dim", _i32), ("first", _i32),
+                ("style", _i32)]
+
+
+class Csa2Scores(ctypes.Structure):
+    _fields_ = [("cap", ctypes.c_float), ("window", _i32), ("sink", _i32), ("slopes", _p),
+                ("prefix", _p)]
+
+
 KV8_E4M3, KV8_INT8 = 0, 1
+ROPE_HALVES, ROPE_PAIRS = 0, 1
+KV8_MAX_TREE = 256
 BF16, F16, F32 = 0, 1, 2
 
 
@@ -106,6 +118,16 @@ _kv8_attn = _sig("csa2_kv8_attn", [_C8P, _RP, _i32, _i32, _p, ctypes.c_float, _R
 _kv8_mass = _sig("csa2_kv8_mass", [_C8P, _RP, _i32, _i32, _p, _p, ctypes.c_float, ctypes.c_float,
                                    _p, _p])
 _kv8_evict = _sig("csa2_kv8_evict", [_C8P, _C8P, _i32, _i32, _i32, _p, _p, _p])
+_OP, _SP = ctypes.POINTER(Csa2Rope), ctypes.POINTER(Csa2Scores)
+_kv8_rope = _sig("csa2_kv8_rope", [_C8P, _OP, _RP, _i32, _RP, _RP, _RP, _i32, _p, _p, _p, _p, _p])
+_kv8_append_rope = _sig("csa2_kv8_append_rope", [_C8P, _OP, _RP, _RP, _i32, _RP, _i32, _RP, _p, _p,
+                                                 _p, _p, _p])
+_kv8_append_path = _sig("csa2_kv8_append_path", [_C8P, _RP, _RP, _i32, _p, _i32, _p, _p, _p, _p])
+_kv8_attn_scored = _sig("csa2_kv8_attn_scored", [_C8P, _RP, _i32, _i32, _p, ctypes.c_float, _SP, _RP,
+                                                 _p, _p, _p])
+_kv8_tree_workspace_size = _sig("csa2_kv8_tree_workspace_size", [_C8P, _i32, _i32], ctypes.c_size_t)
+_kv8_attn_tree = _sig("csa2_kv8_attn_tree", [_C8P, _RP, _i32, _RP, _RP, _p, _i32, _p, ctypes.c_float,
+                                             _SP, _RP, _p, _p, _p])
 KERNEL_QUANT, KERNEL_INDEXER, KERNEL_SELECT, KERNEL_ATTENTION = 0, 1, 2, 3
 
 EXPORTED = ["csa2_workspace_size", "csa2_entry_bytes", "csa2_fp8_quant", "csa2_quant_append",
@@ -113,7 +135,9 @@ EXPORTED = ["csa2_workspace_size", "csa2_entry_bytes", "csa2_fp8_quant", "csa2_q
             "csa2_get_status", "csa2_reset_status", "csa2_status_string",
             "csa2_set_launch_events", "csa2_index_full_noalloc", "csa2_quant_append_pairs",
             "csa2_set_wait_limit", "csa2_attn_decode_layers", "csa2_kv8_workspace_size",
-            "csa2_kv8_append", "csa2_kv8_attn", "csa2_kv8_mass", "csa2_kv8_evict"]
+            "csa2_kv8_append", "csa2_kv8_attn", "csa2_kv8_mass", "csa2_kv8_evict", "csa2_kv8_rope",
+            "csa2_kv8_append_rope", "csa2_kv8_append_path", "csa2_kv8_attn_scored",
+            "csa2_kv8_tree_workspace_size", "csa2_kv8_attn_tree"]
 
 
 class Csa2Error(RuntimeError):
@@ -336,6 +360,11 @@ def kv8_workspace_size(cache: "Cache8 | Csa2Kv8Cache", T: int, heads: int) -> in
     return int(_kv8_workspace_size(ctypes.byref(c), T, heads))
 
 
+def kv8_tree_workspace_size(cache: "Cache8 | Csa2Kv8Cache", T: int, heads: int) -> int:
+    c = cache.struct if isinstance(cache, Cache8) else cache
+    return int(_kv8_tree_workspace_size(ctypes.byref(c), T, heads))
+
+
 class Cache8:
     """Device storage of a K/V cache of grouped heads in 8 bits plus its C
     description (csa2_kv8_cache): codes with one power-of-two scale for each
@@ -408,6 +437,50 @@ class Cache8:
             raise Csa2Error("invalid cache description")
         return torch.zeros(n, dtype=torch.uint8, device=self.device)
 
+    def tree_workspace(self, T, heads):
+        """Workspace for kv8_attn_tree with at most T drafted tokens per sequence and `heads`
+        heads, and for the other calls too."""
+        import torch
+        n = kv8_tree_workspace_size(self, T, heads)
+        if n == 0:
+            raise Csa2Error("invalid cache description, or more drafted tokens than KV8_MAX_TREE")
+        return torch.zeros(n, dtype=torch.uint8, device=self.device)
+
+
+class Rope:
+    """Cosines and sines [positions, dim / 2] of the position rotation of `dim` channels
+    from channel `first` on; pair j is the channels first + j and first + dim / 2 + j
+    (ROPE_HALVES) or first + 2 j and first + 2 j + 1 (ROPE_PAIRS).  Kept as fp32 on
+    `device` (default: where `cos` is)."""
+
+    def __init__(self, cos, sin, first=0, style=ROPE_HALVES, device=None):
+        import torch
+        device = torch.device(cos.device if device is None else device)
+        if cos.dim() != 2 or cos.shape != sin.shape or cos.shape[0] < 1:
+            raise Csa2Error("Rope: cos and sin are [positions, dim / 2]")
+        self.cos = cos.to(device=device, dtype=torch.float32).contiguous()
+        self.sin = sin.to(device=device, dtype=torch.float32).contiguous()
+        if (self.cos.data_ptr() | self.sin.data_ptr()) & 15:
+            self.cos, self.sin = self.cos.clone(), self.sin.clone()
+        self.device = self.cos.device
+        self.struct = Csa2Rope(_ptr(self.cos), _ptr(self.sin), cos.shape[0], 2 * cos.shape[1], first,
+                               style)
+
+
+class Scores:
+    """What a model does to its attention's scores, for a query at position p and a row
+    at position j: x = cap * tanh(x / cap) (cap > 0), x = x - slopes[head] * |p - j|
+    (slopes: fp32 [heads]); and which rows a query sees: j <= p or j < prefix[b]
+    (prefix: int32 [batch]), and, with window > 0, j > p - window or j < sink."""
+
+    def __init__(self, cap=0.0, window=0, sink=0, slopes=None, prefix=None):
+        import torch
+        for name, x, dt in (("slopes", slopes, torch.float32), ("prefix", prefix, torch.int32)):
+            if x is not None and (x.dtype != dt or x.dim() != 1 or not x.is_contiguous()):
+                raise Csa2Error(f"Scores: {name} is a contiguous {dt} vector")
+        self.slopes, self.prefix = slopes, prefix
+        self.struct = Csa2Scores(cap, window, sink, _ptr(slopes), _ptr(prefix))
+
 
 # The calls below are made once per layer and token, so their checks are kept to
 # a few attribute reads, and a refusal's text is put together only when it is raised.
@@ -448,16 +521,16 @@ def _kv8_arg(cache, x, name, dtype, shape):
     return x.data_ptr()
 
 
-def _kv8_ws(cache, ws, T=0, heads=None):
+def _kv8_ws(cache, ws, T=0, heads=None, tree=False):
     heads = cache.kv_heads if heads is None else heads
-    need = cache.needs.get((T, heads))
+    need = cache.needs.get((T, heads, tree))
     if need is None:
-        need = kv8_workspace_size(cache, T, heads)
+        need = (kv8_tree_workspace_size if tree else kv8_workspace_size)(cache, T, heads)
         if need == 0:
             raise Csa2Error(f"the cache does not take a call of {T} query rows and {heads} heads")
         if len(cache.needs) > 256:
             cache.needs.clear()
-        cache.needs[T, heads] = need
+        cache.needs[T, heads, tree] = need
     if ws.device != cache.device or ws.numel() * ws.element_size() < need or not ws.is_contiguous():
         raise Csa2Error(f"workspace: it takes {need} contiguous bytes on {cache.device}")
     return ws.data_ptr()
@@ -537,3 +610,139 @@ def kv8_evict(cache, keep, sink, recent, kept, ws, dst=None, stream=None):
     _kv8_run(cache, "csa2_kv8_evict", _kv8_evict, stream, ctypes.byref(cache.struct),
              None if dst is None else ctypes.byref(dst.struct), keep, sink, recent, kp,
              _kv8_ws(cache, ws))
+
+
+def _kv8_alike(x, of, name, T, kind):
+    """(struct) of rows that have the T and the type of others."""
+    r, Tx = x
+    if Tx != T or r.type != kind:
+        raise Csa2Error(f"{name}: T and type of {of}")
+    return r
+
+
+def _kv8_table(cache, rope):
+    if rope.device != cache.device:
+        raise Csa2Error(f"rope: on {rope.device}, the cache on {cache.device}")
+    return ctypes.byref(rope.struct)
+
+
+def _kv8_scores(cache, scores, H):
+    if scores.slopes is not None:
+        _kv8_arg(cache, scores.slopes, "slopes", "float32", (H,))
+    if scores.prefix is not None:
+        _kv8_arg(cache, scores.prefix, "prefix", "int32", (cache.batch,))
+    return ctypes.byref(scores.struct)
+
+
+def kv8_rope(cache, q, q_out, rope, ws, k=None, k_out=None, q_len=None, pos=None, parent=None,
+             stream=None):
+    """Rotate the first q_len[b] rows (int32 [batch], default T) of q [batch, T, heads, dim]
+    into q_out and, if given, of k [batch, T, kv_heads, dim] into k_out (bf16, f16 or fp32,
+    one type; an output may be its input).  Their positions: pos[b, i] (int32 [batch, T]), or
+    seq_len[b] + the depth of drafted token i in the tree parent[b] (int32 [batch, T]), or
+    seq_len[b] + i."""
+    rq, T = _kv8_rows(cache, q, "q", None, True)
+    H = q.shape[2]
+    ro = _kv8_alike(_kv8_rows(cache, q_out, "q_out", H, True), "q", "q_out", T, rq.type)
+    if (k is None) != (k_out is None):
+        raise Csa2Error("k and k_out go together")
+    rk = rko = None
+    if k is not None:
+        rk = ctypes.byref(_kv8_alike(_kv8_rows(cache, k, "k", cache.kv_heads, True), "q", "k", T,
+                                     rq.type))
+        rko = ctypes.byref(_kv8_alike(_kv8_rows(cache, k_out, "k_out", cache.kv_heads, True), "q",
+                                      "k_out", T, rq.type))
+    if pos is not None and parent is not None:
+        raise Csa2Error("pos or parent, not both")
+    if parent is not None and T > KV8_MAX_TREE:
+        raise Csa2Error(f"a tree has at most {KV8_MAX_TREE} drafted tokens")
+    ql = _kv8_arg(cache, q_len, "q_len", "int32", (cache.batch,))
+    ps = _kv8_arg(cache, pos, "pos", "int32", (cache.batch, T))
+    pa = _kv8_arg(cache, parent, "parent", "int32", (cache.batch, T))
+    _kv8_run(cache, "csa2_kv8_rope", _kv8_rope, stream, ctypes.byref(cache.struct),
+             _kv8_table(cache, rope), ctypes.byref(rq), H, ctypes.byref(ro), rk, rko, T, ql, ps, pa,
+             _kv8_ws(cache, ws))
+
+
+def kv8_append_rope(cache, k, v, rope, ws, q=None, q_out=None, new_len=None, start=None, pos=None,
+                    stream=None):
+    """kv8_append of the rows k, rotated at the positions pos (int32 [batch, T], default
+    start[b] + i), and v; with q [batch, T, heads, dim] (bf16, f16 or fp32) the step's
+    queries are rotated at the same positions into q_out, which may be q."""
+    rk, T = _kv8_rows(cache, k, "k", cache.kv_heads, True)
+    rv = _kv8_alike(_kv8_rows(cache, v, "v", cache.kv_heads, True), "k", "v", T, rk.type)
+    if (q is None) != (q_out is None):
+        raise Csa2Error("q and q_out go together")
+    rq = ro = None
+    H = 0
+    if q is not None:
+        x, Tq = _kv8_rows(cache, q, "q", None, True)
+        H = q.shape[2]
+        if Tq != T:
+            raise Csa2Error("q: the T of k and v")
+        rq = ctypes.byref(x)
+        ro = ctypes.byref(_kv8_alike(_kv8_rows(cache, q_out, "q_out", H, True), "q", "q_out", T, x.type))
+    nl = _kv8_arg(cache, new_len, "new_len", "int32", (cache.batch,))
+    sp = _kv8_arg(cache, start, "start", "int32", (cache.batch,))
+    ps = _kv8_arg(cache, pos, "pos", "int32", (cache.batch, T))
+    _kv8_run(cache, "csa2_kv8_append_rope", _kv8_append_rope, stream, ctypes.byref(cache.struct),
+             _kv8_table(cache, rope), ctypes.byref(rk), ctypes.byref(rv), T, rq, H, ro, nl, sp, ps,
+             _kv8_ws(cache, ws))
+
+
+def kv8_append_path(cache, k, v, path, ws, new_len=None, start=None, stream=None):
+    """kv8_append of chosen rows of k, v [batch, T, kv_heads, dim]: the i-th new row of a
+    sequence is row path[b, i] (int32 [batch, M]); new_len[b] of them (default M).  The drafted
+    tokens on an accepted path, with the keys that kv8_attn_tree took."""
+    rk, T = _kv8_rows(cache, k, "k", cache.kv_heads, True)
+    rv = _kv8_alike(_kv8_rows(cache, v, "v", cache.kv_heads, True), "k", "v", T, rk.type)
+    if len(path.shape) != 2:
+        raise Csa2Error("path: it takes [batch, M]")
+    M = path.shape[1]
+    if T == 0 and M > 0:
+        raise Csa2Error("path: there are no rows to choose from")
+    pt = _kv8_arg(cache, path, "path", "int32", (cache.batch, M))
+    nl = _kv8_arg(cache, new_len, "new_len", "int32", (cache.batch,))
+    sp = _kv8_arg(cache, start, "start", "int32", (cache.batch,))
+    _kv8_run(cache, "csa2_kv8_append_path", _kv8_append_path, stream, ctypes.byref(cache.struct),
+             ctypes.byref(rk), ctypes.byref(rv), T, pt, M, nl, sp, _kv8_ws(cache, ws))
+
+
+def kv8_attn_scored(cache, q, out, ws, scores, lse=None, q_len=None, softmax_scale=0.0, stream=None):
+    """kv8_attn with what `scores` (Scores) does to the scores and to which rows count; query
+    i of a sequence is at position seq_len[b] - q_len[b] + i.  kv8_mass does not take its lse."""
+    rq, T = _kv8_rows(cache, q, "q")
+    H = q.shape[2]
+    ro = _kv8_alike(_kv8_rows(cache, out, "out", H), "q", "out", T, rq.type)
+    ls = _kv8_arg(cache, lse, "lse", "float32", (cache.batch, T, H))
+    ql = _kv8_arg(cache, q_len, "q_len", "int32", (cache.batch,))
+    _kv8_run(cache, "csa2_kv8_attn_scored", _kv8_attn_scored, stream, ctypes.byref(cache.struct),
+             ctypes.byref(rq), H, T, ql, softmax_scale, _kv8_scores(cache, scores, H),
+             ctypes.byref(ro), ls, _kv8_ws(cache, ws, T, H))
+
+
+def kv8_attn_tree(cache, q, k, v, parent, out, ws, lse=None, q_len=None, softmax_scale=0.0,
+                  scores=None, stream=None):
+    """Attention of drafted tokens, which are not in the cache: token i of a sequence's first
+    q_len[b] (default T <= KV8_MAX_TREE) sees all rows of the cache, itself and the tokens that
+    it follows, parent[b, i] (int32 [batch, T]; an earlier token, or -1) and so on.  q [batch,
+    T, heads, dim], k and v [batch, T, kv_heads, dim] (bf16 or f16, rotated as kv8_rope with
+    `parent` does); out, lse as kv8_attn; scores without a prefix; ws: cache.tree_workspace."""
+    rq, T = _kv8_rows(cache, q, "q")
+    H = q.shape[2]
+    rk = _kv8_alike(_kv8_rows(cache, k, "k", cache.kv_heads), "q", "k", T, rq.type)
+    rv = _kv8_alike(_kv8_rows(cache, v, "v", cache.kv_heads), "q", "v", T, rq.type)
+    ro = _kv8_alike(_kv8_rows(cache, out, "out", H), "q", "out", T, rq.type)
+    if T > KV8_MAX_TREE:
+        raise Csa2Error(f"a tree has at most {KV8_MAX_TREE} drafted tokens")
+    if parent is None:
+        raise Csa2Error("csa2_kv8_attn_tree: it takes `parent`")
+    if scores is not None and scores.prefix is not None:
+        raise Csa2Error("csa2_kv8_attn_tree: scores without a prefix")
+    pa = _kv8_arg(cache, parent, "parent", "int32", (cache.batch, T))
+    ls = _kv8_arg(cache, lse, "lse", "float32", (cache.batch, T, H))
+    ql = _kv8_arg(cache, q_len, "q_len", "int32", (cache.batch,))
+    _kv8_run(cache, "csa2_kv8_attn_tree", _kv8_attn_tree, stream, ctypes.byref(cache.struct),
+             ctypes.byref(rq), H, ctypes.byref(rk), ctypes.byref(rv), pa, T, ql, softmax_scale,
+             None if scores is None else _kv8_scores(cache, scores, H), ctypes.byref(ro), ls,
+             _kv8_ws(cache, ws, T, H, tree=True))

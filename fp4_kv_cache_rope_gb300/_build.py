@@ -20,7 +20,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-v"]
 SOURCES = ["api.cu", "quant.cu", "indexer.cu", "select.cu", "attention.cu",
-           "kv8_api.cu", "kv8_rows.cu", "kv8_attn.cu", "kv8_prefill.cu", "kv8_mass.cu"]
+           "kv8_api.cu", "kv8_rows.cu", "kv8_attn.cu", "kv8_prefill.cu", "kv8_mass.cu",
+           "kv8_rope.cu", "kv8_scored.cu", "kv8_scored_prefill.cu", "kv8_tree.cu"]
 
 
 def nvcc() -> str:

@@ -106,6 +106,7 @@ csa2_status csa2_set_wait_limit(uint64_t ns) {
   if (e == cudaSuccess) e = set_wait_limit_quant(v);
   if (e == cudaSuccess) e = set_wait_limit_kv8_prefill(v);
   if (e == cudaSuccess) e = set_wait_limit_kv8_mass(v);
+  if (e == cudaSuccess) e = set_wait_limit_kv8_scored(v);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   return from_cuda(e);
 }

@@ -384,6 +384,27 @@ cudaError_t launch_kv8_append(const Kv8& c, int D, const Kv8Rows& k, const Kv8Ro
 cudaError_t launch_kv8_attn(const Kv8Attn& a, int num_sms, cudaStream_t s);
 cudaError_t launch_kv8_mass_few(const Kv8Attn& a, int num_sms, cudaStream_t s);
 cudaError_t launch_kv8_mass_many(const Kv8Attn& a, int num_sms, cudaStream_t s);
+cudaError_t launch_kv8_rope(const Kv8& c, int D, const csa2_rope& rope, const Kv8Rows& q, int H,
+                            const Kv8Rows& q_out, const Kv8Rows& k, const Kv8Rows& k_out, int T,
+                            const int32_t* q_len, const int32_t* pos, const int32_t* parent,
+                            uint32_t* status, cudaStream_t s);
+cudaError_t launch_kv8_append_rope(const Kv8& c, int D, const csa2_rope& rope, const Kv8Rows& k,
+                                   const Kv8Rows& v, int T, const Kv8Rows& q, int H,
+                                   const Kv8Rows& q_out, const int32_t* new_len,
+                                   const int32_t* start, const int32_t* pos, uint32_t* status,
+                                   cudaStream_t s);
+cudaError_t launch_kv8_append_path(const Kv8& c, int D, const Kv8Rows& k, const Kv8Rows& v, int T,
+                                   const int32_t* path, int M, const int32_t* new_len,
+                                   const int32_t* start, uint32_t* status, cudaStream_t s);
+struct Kv8Scores;         // kv8_scores.cuh
+struct Kv8Left;
+// left null: the outputs; else where the drafted rows' join finds the results
+cudaError_t launch_kv8_scored_few(const Kv8Attn& a, const Kv8Scores& sc, int num_sms, Kv8Left* left,
+                                  cudaStream_t s);
+cudaError_t launch_kv8_scored_many(const Kv8Attn& a, const Kv8Scores& sc, int num_sms, Kv8Left* left,
+                                   cudaStream_t s);
+cudaError_t launch_kv8_tree_join(const Kv8Attn& a, const Kv8Scores& sc, const Kv8Left& left,
+                                 const Kv8Rows& k, const Kv8Rows& v, int num_sms, cudaStream_t s);
 cudaError_t launch_kv8_evict(const Kv8& src, const Kv8& dst, bool in_place, int D, int keep,
                              int sink, int recent, int32_t* kept, int32_t* old_len,
                              uint32_t* status, int num_sms, cudaStream_t s);

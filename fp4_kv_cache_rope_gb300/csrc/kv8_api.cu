@@ -4,7 +4,7 @@
 
 #include <atomic>
 
-#include "kv8.cuh"
+#include "kv8_scores.cuh"
 
 using namespace csa2;
 
@@ -108,10 +108,12 @@ csa2_status done(cudaError_t e) {
   return CSA2_ERR_CUDA;
 }
 
-bool overlap(const int32_t* a, const int32_t* b, int64_t n) {
+// Whether the na numbers from a on and the nb from b on have one in common.
+bool overlap(const int32_t* a, const int32_t* b, int64_t na, int64_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && x < y + 4 * n && y < x + 4 * n;
+  return a && x < y + 4 * nb && y < x + 4 * na;
 }
+bool overlap(const int32_t* a, const int32_t* b, int64_t n) { return overlap(a, b, n, n); }
 
 // Whether two caches whose places the host knows (at least one is contiguous)
 // have storage in common.  Two paged ones may lie in one pool of pages.
@@ -152,6 +154,22 @@ Kv8Ws kv8_ws(const csa2_kv8_cache* c) {
   return w;
 }
 
+// The results of drafted tokens' queries before their own rows: one fp32 row each.
+size_t kv8_tree_bytes(const csa2_kv8_cache* c, int32_t T, int32_t H) {
+  return align256((size_t)c->batch * T * H * kv8_row_floats(c->dim) * 4);
+}
+
+bool rope_ok(const csa2_rope* r, int32_t D) {
+  return r && r->cos && r->sin && aligned(r->cos, 16) && aligned(r->sin, 16) && r->positions > 0 &&
+         r->positions <= CSA2_MAX_LEN && r->dim >= 16 && r->dim % 16 == 0 && r->first >= 0 &&
+         r->first % 8 == 0 && r->dim <= D && r->first <= D - r->dim &&
+         (r->style == CSA2_ROPE_HALVES || r->style == CSA2_ROPE_PAIRS);
+}
+bool scores_ok(const csa2_scores* s) {
+  return s && (s->cap == 0.0f || (s->cap >= 0x1p-10f && s->cap <= 0x1p20f)) && s->window >= 0 &&
+         s->sink >= 0 && aligned(s->slopes, 4) && aligned(s->prefix, 4);
+}
+
 bool heads_ok(const csa2_kv8_cache* c, int32_t T, int32_t H) {
   return H > 0 && H % c->kv_heads == 0 && H <= 65536 && T >= 0 && T <= CSA2_MAX_LEN &&
          (int64_t)c->batch * H * (T + 1) < (int64_t)1 << 31;
@@ -161,6 +179,17 @@ bool heads_ok(const csa2_kv8_cache* c, int32_t T, int32_t H) {
 // where it would lose bits, there is none.
 bool scale_ok(float scale) {
   return scale <= 0.0f || (scale >= 0x1p-100f && scale <= 0x1p100f);
+}
+
+// What every append wants of its rows and integer arguments (T above 0).
+bool append_ok(const csa2_kv8_cache* c, const csa2_rows* k, const csa2_rows* v,
+               const int32_t* new_len, const int32_t* start) {
+  if (!aligned(new_len, 4) || !aligned(start, 4)) return false;
+  // seq_len is written while these are read
+  if (overlap(new_len, c->seq_len, c->batch) ||
+      (start != c->seq_len && overlap(start, c->seq_len, c->batch)))
+    return false;
+  return rows_ok(k, true) && rows_ok(v, true) && k->type == v->type;
 }
 
 Kv8Attn attn_of(const csa2_kv8_cache* c, const csa2_rows* q, int32_t H, int32_t T,
@@ -180,6 +209,26 @@ Kv8Attn attn_of(const csa2_kv8_cache* c, const csa2_rows* q, int32_t H, int32_t 
   a.part = reinterpret_cast<float*>(w + kv8_ws(c).part);
   a.status = reinterpret_cast<uint32_t*>(w);
   return a;
+}
+
+Kv8Scores scores_of(const csa2_scores& s, const Kv8Attn& a) {
+  Kv8Scores k{};
+  // the softmax scale's double is in its two floats
+  const double to2 = (double)a.scale_log2 + (double)a.scale_low;
+  k.factor = s.cap > 0.0f ? (float)(to2 / 1.4426950408889634 / (double)s.cap) : a.scale_log2;
+  k.cap2 = (float)((double)s.cap * 1.4426950408889634);
+  k.window = s.window < kKv8MaxWindow ? s.window : kKv8MaxWindow;
+  k.sink = s.window > 0 ? (s.sink < kKv8MaxWindow ? s.sink : kKv8MaxWindow) : 0;
+  k.slopes = s.slopes;
+  k.prefix = s.prefix;
+  return k;
+}
+
+// Up to 64 query rows per (sequence, K/V head) go to the kernel that is bound by
+// the cache's bytes, more to the tensor cores', as in csa2_kv8_attn.
+cudaError_t scored(const Kv8Attn& a, const Kv8Scores& sc, Kv8Left* left, cudaStream_t s) {
+  return a.T * a.G <= 64 ? launch_kv8_scored_few(a, sc, sms(), left, s)
+                         : launch_kv8_scored_many(a, sc, sms(), left, s);
 }
 
 }  // namespace
@@ -269,6 +318,119 @@ csa2_status csa2_kv8_evict(const csa2_kv8_cache* cache, const csa2_kv8_cache* ds
   return done(launch_kv8_evict(kv8_of(*cache), kv8_of(*d), dst == nullptr, cache->dim, keep, sink,
                                recent, kept, reinterpret_cast<int32_t*>(w + kv8_ws(cache).old_len),
                                reinterpret_cast<uint32_t*>(w), sms(), (cudaStream_t)stream));
+}
+
+csa2_status csa2_kv8_rope(const csa2_kv8_cache *cache, const csa2_rope *rope, const csa2_rows *q,
+                          int32_t H, const csa2_rows *q_out, const csa2_rows *k,
+                          const csa2_rows *k_out, int32_t T, const int32_t *q_len,
+                          const int32_t *pos, const int32_t *parent, void *ws, void *stream) {
+  if (!kv8_ok(cache) || !rope_ok(rope, cache->dim) || !ws || !aligned(ws, 256) || !heads_ok(cache, T, H))
+    return CSA2_ERR_INVALID;
+  if (!aligned(q_len, 4) || !aligned(pos, 4) || !aligned(parent, 4) || (pos && parent) ||
+      (parent && T > CSA2_KV8_MAX_TREE) || !k != !k_out)
+    return CSA2_ERR_INVALID;
+  if (T == 0) return CSA2_OK;
+  if (!rows_ok(q, true) || !rows_ok(q_out, true) || q->type != q_out->type ||
+      !rows_apart(*q_out, cache->batch, T, H, cache->dim))
+    return CSA2_ERR_INVALID;
+  if (k && (!rows_ok(k, true) || !rows_ok(k_out, true) || k->type != q->type ||
+            k_out->type != q->type ||
+            !rows_apart(*k_out, cache->batch, T, cache->kv_heads, cache->dim)))
+    return CSA2_ERR_INVALID;
+  const csa2_rows none = {nullptr, 0, 0, 0, CSA2_BF16};
+  return done(launch_kv8_rope(kv8_of(*cache), cache->dim, *rope, rows_of(*q), H, rows_of(*q_out),
+                              rows_of(k ? *k : none), rows_of(k ? *k_out : none), T, q_len, pos,
+                              parent, static_cast<uint32_t*>(ws), (cudaStream_t)stream));
+}
+
+csa2_status csa2_kv8_append_rope(const csa2_kv8_cache* cache, const csa2_rope* rope,
+                                 const csa2_rows* k, const csa2_rows* v, int32_t T,
+                                 const csa2_rows* q, int32_t H, const csa2_rows* q_out,
+                                 const int32_t* new_len, const int32_t* start, const int32_t* pos,
+                                 void* ws, void* stream) {
+  if (!kv8_ok(cache) || !rope_ok(rope, cache->dim) || !ws || !aligned(ws, 256) || T < 0 ||
+      T > CSA2_MAX_LEN || H < 0 || !q != !q_out || !q != !H || (q && !heads_ok(cache, T, H)))
+    return CSA2_ERR_INVALID;
+  if (!aligned(pos, 4)) return CSA2_ERR_INVALID;
+  if (T == 0) return csa2_kv8_append(cache, nullptr, nullptr, 0, new_len, start, ws, stream);
+  if (!append_ok(cache, k, v, new_len, start) ||
+      overlap(pos, cache->seq_len, (int64_t)cache->batch * T, cache->batch))
+    return CSA2_ERR_INVALID;
+  if (q && (!rows_ok(q, true) || !rows_ok(q_out, true) || q->type != q_out->type ||
+            !rows_apart(*q_out, cache->batch, T, H, cache->dim)))
+    return CSA2_ERR_INVALID;
+  const csa2_rows none = {nullptr, 0, 0, 0, CSA2_BF16};
+  return done(launch_kv8_append_rope(kv8_of(*cache), cache->dim, *rope, rows_of(*k), rows_of(*v), T,
+                                     rows_of(q ? *q : none), H, rows_of(q ? *q_out : none), new_len,
+                                     start, pos, static_cast<uint32_t*>(ws), (cudaStream_t)stream));
+}
+
+csa2_status csa2_kv8_append_path(const csa2_kv8_cache* cache, const csa2_rows* k,
+                                 const csa2_rows* v, int32_t T, const int32_t* path, int32_t M,
+                                 const int32_t* new_len, const int32_t* start, void* ws,
+                                 void* stream) {
+  if (!kv8_ok(cache) || !ws || !aligned(ws, 256) || T < 0 || T > CSA2_MAX_LEN || M < 0 ||
+      M > CSA2_MAX_LEN)
+    return CSA2_ERR_INVALID;
+  if (M == 0) return csa2_kv8_append(cache, nullptr, nullptr, 0, new_len, start, ws, stream);
+  if (!path || !aligned(path, 4) || T == 0 || !append_ok(cache, k, v, new_len, start) ||
+      overlap(path, cache->seq_len, (int64_t)cache->batch * M, cache->batch))
+    return CSA2_ERR_INVALID;
+  return done(launch_kv8_append_path(kv8_of(*cache), cache->dim, rows_of(*k), rows_of(*v), T, path, M,
+                                     new_len, start, static_cast<uint32_t*>(ws),
+                                     (cudaStream_t)stream));
+}
+
+csa2_status csa2_kv8_attn_scored(const csa2_kv8_cache* cache, const csa2_rows* q, int32_t H,
+                                 int32_t T, const int32_t* q_len, float softmax_scale,
+                                 const csa2_scores* scores, const csa2_rows* out, float* lse,
+                                 void* ws, void* stream) {
+  if (!kv8_ok(cache) || !ws || !aligned(ws, 256) || !heads_ok(cache, T, H) ||
+      !scale_ok(softmax_scale) || !scores_ok(scores))
+    return CSA2_ERR_INVALID;
+  if (!aligned(q_len, 4) || !aligned(lse, 4)) return CSA2_ERR_INVALID;
+  if (T == 0) return CSA2_OK;
+  if (!rows_ok(q, false) || !rows_ok(out, false) || q->type != out->type ||
+      !rows_apart(*out, cache->batch, T, H, cache->dim))
+    return CSA2_ERR_INVALID;
+  Kv8Attn a = attn_of(cache, q, H, T, q_len, softmax_scale, ws);
+  a.out = rows_of(*out);
+  a.lse = lse;
+  return done(scored(a, scores_of(*scores, a), nullptr, (cudaStream_t)stream));
+}
+
+size_t csa2_kv8_tree_workspace_size(const csa2_kv8_cache* cache, int32_t T, int32_t H) {
+  if (!kv8_ok(cache) || !heads_ok(cache, T, H) || T > CSA2_KV8_MAX_TREE) return 0;
+  return kv8_ws(cache).total + kv8_tree_bytes(cache, T, H);
+}
+
+csa2_status csa2_kv8_attn_tree(const csa2_kv8_cache* cache, const csa2_rows* q, int32_t H,
+                               const csa2_rows* k, const csa2_rows* v, const int32_t* parent,
+                               int32_t T, const int32_t* q_len, float softmax_scale,
+                               const csa2_scores* scores, const csa2_rows* out, float* lse,
+                               void* ws, void* stream) {
+  const csa2_scores plain = {0.0f, 0, 0, nullptr, nullptr};
+  if (!scores) scores = &plain;
+  if (!kv8_ok(cache) || !ws || !aligned(ws, 256) || !heads_ok(cache, T, H) ||
+      T > CSA2_KV8_MAX_TREE || !scale_ok(softmax_scale) || !scores_ok(scores) || scores->prefix)
+    return CSA2_ERR_INVALID;
+  if (!aligned(q_len, 4) || !aligned(lse, 4) || !aligned(parent, 4)) return CSA2_ERR_INVALID;
+  if (T == 0) return CSA2_OK;
+  if (!parent || !rows_ok(q, false) || !rows_ok(k, false) || !rows_ok(v, false) ||
+      !rows_ok(out, false) || q->type != out->type || k->type != q->type || v->type != q->type ||
+      !rows_apart(*out, cache->batch, T, H, cache->dim))
+    return CSA2_ERR_INVALID;
+  Kv8Attn a = attn_of(cache, q, H, T, q_len, softmax_scale, ws);
+  a.out = rows_of(*out);
+  a.lse = lse;
+  Kv8Scores sc = scores_of(*scores, a);
+  sc.parent = parent;
+  sc.rows_out = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kv8_ws(cache).total);
+  Kv8Left left{};
+  const cudaError_t e = scored(a, sc, &left, (cudaStream_t)stream);
+  return done(e != cudaSuccess ? e
+                               : launch_kv8_tree_join(a, sc, left, rows_of(*k), rows_of(*v), sms(),
+                                                      (cudaStream_t)stream));
 }
 
 }  // extern "C"

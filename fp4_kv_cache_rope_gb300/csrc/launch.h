@@ -58,6 +58,7 @@ cudaError_t set_wait_limit_attention(unsigned long long ns);
 cudaError_t set_wait_limit_quant(unsigned long long ns);
 cudaError_t set_wait_limit_kv8_prefill(unsigned long long ns);
 cudaError_t set_wait_limit_kv8_mass(unsigned long long ns);
+cudaError_t set_wait_limit_kv8_scored(unsigned long long ns);
 
 // Benchmark instrumentation (api.cu): records the family's begin/end events
 // on stream s when they are set.

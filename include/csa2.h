@@ -69,7 +69,8 @@ typedef enum csa2_status {
 #define CSA2_DEV_TIMEOUT 0x8u     /* a bounded on-chip wait gave up */
 #define CSA2_DEV_BAD_POOL 0x10u   /* pool block id outside the visible blocks */
 #define CSA2_DEV_BAD_ALIGN 0x20u  /* on-chip buffer misaligned (kernel skipped work) */
-#define CSA2_DEV_NONFINITE 0x40u  /* csa2_kv8_append met an infinity or a NaN */
+#define CSA2_DEV_NONFINITE 0x40u  /* csa2_kv8_append* met an infinity or a NaN */
+#define CSA2_DEV_BAD_TREE 0x80u   /* a drafted token's parent is not an earlier token */
 
 /* Largest k and the pool capacity (blocks of 8 positions). */
 #define CSA2_MAX_TOPK 2048
@@ -473,6 +474,124 @@ csa2_status csa2_kv8_attn(const csa2_kv8_cache *cache, const csa2_rows *q, int32
 csa2_status csa2_kv8_mass(const csa2_kv8_cache *cache, const csa2_rows *q, int32_t H, int32_t T,
                           const int32_t *q_len, const float *lse, float softmax_scale, float decay,
                           void *ws, void *stream);
+
+/*
+ * Rotated, scored and drafted tokens over the same cache.
+ *
+ * csa2_rope: the position rotation.  Of a row's `dim` channels from `first`
+ * on, pair j (0 .. dim/2 - 1) is rotated by (c, s) = (cos, sin)[p][j] as
+ *   (x0, x1) -> (x0 c - x1 s, x0 s + x1 c),
+ * each product and sum rounded once in fp32.  Pair j is the channels
+ * first + j and first + dim/2 + j (CSA2_ROPE_HALVES) or first + 2j and
+ * first + 2j + 1 (CSA2_ROPE_PAIRS); the other channels stay as they are.  A
+ * position outside [0, positions) leaves the row unrotated and sets
+ * CSA2_DEV_BAD_INDEX.
+ */
+typedef struct csa2_rope {
+  const float *cos, *sin;     /* [positions, dim / 2], 16-byte aligned */
+  int32_t positions;          /* 1 .. CSA2_MAX_LEN */
+  int32_t dim;                /* a multiple of 16, 16 .. D */
+  int32_t first;              /* a multiple of 8, first + dim <= D */
+  int32_t style;              /* CSA2_ROPE_HALVES or CSA2_ROPE_PAIRS */
+} csa2_rope;
+
+#define CSA2_ROPE_HALVES 0
+#define CSA2_ROPE_PAIRS 1
+
+/*
+ * What a model does to its scores, for a query at position p and a row at
+ * position j (positions count rows: after csa2_kv8_evict they are not the tokens'):
+ *   x = softmax_scale * q . k_j
+ *   x = cap tanh(x / cap)                     where cap > 0
+ *   x = x - slopes[h] |p - j|                 where slopes are given
+ * and the query sees row j when j <= p or j < prefix[b], and, where window > 0,
+ * j > p - window or j < sink.
+ */
+typedef struct csa2_scores {
+  float cap;                  /* 0, or 2^-10 .. 2^20 */
+  int32_t window;             /* 0: every row; else >= 1 */
+  int32_t sink;               /* first rows that a window does not hide, >= 0 */
+  const float *slopes;        /* [H] (device) or NULL */
+  const int32_t *prefix;      /* [B] (device) or NULL; csa2_kv8_attn_tree takes none */
+} csa2_scores;
+
+/*
+ * Rotation of rows that stay outside the cache: of sequence b the first
+ * q_len[b] rows (device int32 [B], clamped to 0..T; NULL: T) of q [B, T, H, D]
+ * go to q_out, and of k [B, T, Hkv, D] to k_out (k and k_out NULL: none).  The
+ * types are one for all four, of any kind; results are rounded to it once.  Row i's position is
+ *   pos[b, i]                  where pos (device int32 [B, T]) is given;
+ *   seq_len[b] + depth(i)      where parent (device int32 [B, T]) is given: the
+ *                              drafted tokens of csa2_kv8_attn_tree, T <=
+ *                              CSA2_KV8_MAX_TREE;
+ *   seq_len[b] + i             otherwise.
+ * Rows behind q_len[b] are left as they were.  An output may be its input itself
+ * (the same rows at the same places); otherwise no rows share memory.
+ */
+csa2_status csa2_kv8_rope(const csa2_kv8_cache *cache, const csa2_rope *rope,
+                            const csa2_rows *q, int32_t H, const csa2_rows *q_out,
+                            const csa2_rows *k, const csa2_rows *k_out, int32_t T,
+                            const int32_t *q_len, const int32_t *pos, const int32_t *parent,
+                            void *ws, void *stream);
+
+/*
+ * Append with rotation: csa2_kv8_append of k's rows rotated (in fp32, not rounded
+ * before they are quantised) and of v's as they are.  Row i's position is
+ * pos[b, i] (device int32 [B, T]) or, pos NULL, start[b] + i.  With q (rows
+ * [B, T, H, D] of the same T) the step's queries are rotated into q_out at the
+ * same positions (q_out may be q itself; otherwise it shares no memory with any
+ * of the inputs); q and q_out NULL, H 0: none.  q and q_out have one type, k and
+ * v one.  pos shares no memory with seq_len.
+ */
+csa2_status csa2_kv8_append_rope(const csa2_kv8_cache *cache, const csa2_rope *rope,
+                                 const csa2_rows *k, const csa2_rows *v, int32_t T,
+                                 const csa2_rows *q, int32_t H, const csa2_rows *q_out,
+                                 const int32_t *new_len, const int32_t *start,
+                                 const int32_t *pos, void *ws, void *stream);
+
+/*
+ * Append of chosen rows: csa2_kv8_append where the i-th new row of sequence b is
+ * row path[b, i] of k and v (rows [B, T, Hkv, D]; path: device int32 [B, M];
+ * new_len is clamped to 0..M, NULL: M).  The drafted tokens on an accepted path,
+ * with the keys that csa2_kv8_attn_tree took: the i-th then stands at the position
+ * that its depth gave it.  An index outside [0, T) appends a row of zeros and sets
+ * CSA2_DEV_BAD_INDEX.
+ */
+csa2_status csa2_kv8_append_path(const csa2_kv8_cache *cache, const csa2_rows *k,
+                                 const csa2_rows *v, int32_t T, const int32_t *path, int32_t M,
+                                 const int32_t *new_len, const int32_t *start, void *ws,
+                                 void *stream);
+
+/* csa2_kv8_attn with scores: query i's position is seq_len[b] - q_len[b] + i.
+ * Slopes are finite.  lse is the logarithm of the changed scores' sum, so
+ * csa2_kv8_mass, which has no scores, does not take it. */
+csa2_status csa2_kv8_attn_scored(const csa2_kv8_cache *cache, const csa2_rows *q, int32_t H,
+                                 int32_t T, const int32_t *q_len, float softmax_scale,
+                                 const csa2_scores *scores, const csa2_rows *out, float *lse,
+                                 void *ws, void *stream);
+
+/*
+ * Attention of drafted tokens, none of which is in the cache.  Of sequence b the
+ * first q_len[b] tokens count (device int32 [B], clamped to 0..T; NULL: T).
+ * parent (device int32 [B, T]): the token that token i follows, an earlier one, or
+ * -1 (any negative) for one that follows the cache's last row; a parent that is not
+ * earlier counts as -1 and sets CSA2_DEV_BAD_TREE.  Token i sees the rows 0 ..
+ * seq_len[b] - 1 of the cache and, in k and v (rows [B, T, Hkv, D] of q's type), the
+ * rows of itself and of the tokens that it follows, directly or not.  Its position
+ * is seq_len[b] plus how many tokens it follows; `scores` (NULL: none), which may
+ * hold no prefix, goes by these.  out, lse, softmax_scale and what is left as it
+ * was: as csa2_kv8_attn; out shares no memory with k and v.
+ * ws: csa2_kv8_tree_workspace_size bytes (more than the other calls take, which it
+ * serves too).  T is at most CSA2_KV8_MAX_TREE.
+ */
+#define CSA2_KV8_MAX_TREE 256
+csa2_status csa2_kv8_attn_tree(const csa2_kv8_cache *cache, const csa2_rows *q, int32_t H,
+                               const csa2_rows *k, const csa2_rows *v, const int32_t *parent,
+                               int32_t T, const int32_t *q_len, float softmax_scale,
+                               const csa2_scores *scores, const csa2_rows *out, float *lse,
+                               void *ws, void *stream);
+/* 0 when the description is invalid or T is above CSA2_KV8_MAX_TREE. */
+size_t csa2_kv8_tree_workspace_size(const csa2_kv8_cache *cache, int32_t T, int32_t H);
 
 /*
  * Eviction.  Of a sequence with more than `keep` rows every K/V head keeps, in

@@ -144,3 +144,95 @@ def evict(weight, n: int, keep: int, sink: int, recent: int):
     order = sorted(mid, key=lambda j: (not nan_first[j], -w[j], j))
     take = order[: keep - sink - recent]
     return np.array(sorted(set(range(sink)) | set(range(n - recent, n)) | set(take)), dtype=np.int64)
+
+
+# ------------------------------------------- rotated, scored and drafted tokens
+HALVES, PAIRS = 0, 1
+
+
+def rotate(x, pos, cos, sin, first: int = 0, style: int = HALVES):
+    """Rows x [n, ..., D] (fp32 values) rotated at positions pos [n] with the tables
+    [positions, R / 2]; each product and sum rounded once in fp32.  A position outside
+    the tables leaves its row as it is."""
+    x = np.asarray(x, np.float32)
+    y = x.copy()
+    half = cos.shape[1]
+    at = first + np.arange(half)
+    a, b = (at, at + half) if style == HALVES else (first + 2 * np.arange(half),
+                                                    first + 2 * np.arange(half) + 1)
+    pos = np.asarray(pos)
+    ok = (pos >= 0) & (pos < len(cos))
+    shape = (-1,) + (1,) * (x.ndim - 2) + (half,)
+    c = np.asarray(cos, np.float32)[pos[ok]].reshape(shape)
+    s = np.asarray(sin, np.float32)[pos[ok]].reshape(shape)
+    with np.errstate(invalid="ignore", over="ignore"):
+        u, v = x[ok][..., a], x[ok][..., b]
+        yo = y[ok]
+        yo[..., a] = u * c - v * s
+        yo[..., b] = u * s + v * c
+    y[ok] = yo
+    return y
+
+
+def path_to(parent, i: int):
+    """Token i and the ones that it follows, itself first; a parent that is no earlier
+    token is none."""
+    path = [i]
+    while 0 <= parent[path[-1]] < path[-1]:
+        path.append(int(parent[path[-1]]))
+    return path
+
+
+def sees(p, j, n: int, window: int = 0, sink: int = 0, prefix: int = 0):
+    """Whether queries at positions p [T] see the cached rows j [n]: bool [T, n]."""
+    p = np.asarray(p)[:, None]
+    ok = ((j <= p) | (j < prefix)) & (j < n)
+    return ok & ((j > p - window) | (j < sink)) if window else ok
+
+
+def attend(q, k, v, scale: float, see, dist, cap: float = 0.0, slopes=None, half: float = 2.0 ** -11):
+    """q [T, G, D] over rows k, v [n, D] that see [T, n] shows, at distances dist [T, n].
+    Returns (o, lse, tol, ltol): the values and bounds of what fp32 arithmetic makes of
+    them.
+
+    A logit L = scale sum |q k| of D exact products, summed in fp32 by an accumulator
+    that may cut off, is off by (D + 2) 2^-23 L; the cap (slope at most 1) hands that
+    on and adds 2^-20 of its result (the quotient's fit and roundings, 4e-7, a
+    reciprocal's 2^-23 and three products); a slope's product and sum add 2^-22 of their
+    sizes.  A weight is the exponential of that, 2^-20 for its argument's rounding
+    and the function, rounded once to f16 (2^-11); the sums of n terms add 2^-23 n.  Weights are held in steps
+    of 2^-31 of the largest, and V in steps of 2^-30 of its own largest value.
+    half: half a step of the output's type, relative.
+    """
+    T, G, D = q.shape
+    n = len(k)
+    o, tol = np.zeros((T, G, v.shape[1])), np.zeros((T, G, v.shape[1]))
+    lse, ltol = np.full((T, G), -np.inf), np.zeros((T, G))
+    vmax = np.abs(v).max() if n else 0.0
+    for i in range(T):
+        on = see[i]
+        if not on.any():
+            continue
+        kk, vv = k[on], v[on]
+        x = scale * (q[i] @ kk.T)
+        e = (D + 2) * 2.0 ** -23 * scale * (np.abs(q[i]) @ np.abs(kk).T)
+        if cap:
+            x = cap * np.tanh(x / cap)
+            e = e + 2.0 ** -20 * np.abs(x)
+        if slopes is not None:
+            bias = np.asarray(slopes, np.float64)[:, None] * np.abs(dist[i][on])
+            e = e + 2.0 ** -22 * (np.abs(bias) + np.abs(x))
+            x = x - bias
+        top = x.max(1, keepdims=True)
+        w = np.exp(x - top)
+        z = w.sum(1, keepdims=True)
+        lse[i] = (top + np.log(z))[:, 0]
+        w = w / z
+        o[i] = w @ vv
+        mean = (w * e).sum(1, keepdims=True)
+        a = w @ np.abs(vv)
+        tol[i] = (w * e) @ np.abs(vv) + a * (mean + 2.0 ** -20 + 2.0 ** -11 + 2 * n * 2.0 ** -23)
+        ltol[i] = mean[:, 0] + 2.0 ** -20 + n * 2.0 ** -23 + 2.0 ** -22 * np.abs(lse[i])
+    tol = tol + (n * 2.0 ** -32 + 2.0 ** -30) * vmax
+    tol = tol + half * (np.abs(o) + tol) + (2.0 ** -25 if half == 2.0 ** -11 else 1e-30)
+    return o, lse, tol, ltol
