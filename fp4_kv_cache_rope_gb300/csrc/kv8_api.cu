@@ -154,9 +154,14 @@ Kv8Ws kv8_ws(const csa2_kv8_cache* c) {
   return w;
 }
 
-// The results of drafted tokens' queries before their own rows: one fp32 row each.
+// The results of drafted tokens' queries before their own rows: one fp32 row each, or
+// the many-row kernel's parts in their place.
 size_t kv8_tree_bytes(const csa2_kv8_cache* c, int32_t T, int32_t H) {
-  return align256((size_t)c->batch * T * H * kv8_row_floats(c->dim) * 4);
+  const size_t rows = (size_t)c->batch * T * H * kv8_row_floats(c->dim) * 4;
+  const int64_t base = (int64_t)c->batch * c->kv_heads * (((int64_t)T * (H / c->kv_heads) + 255) / 256);
+  const int splits = base > 0 ? kv8_tree_splits(base, c->max_len) : 1;
+  const size_t parts = splits > 1 ? (size_t)base * splits * 256 * (c->dim + 2) * 4 : 0;
+  return align256(rows > parts ? rows : parts);
 }
 
 bool rope_ok(const csa2_rope* r, int32_t D) {
@@ -426,6 +431,7 @@ csa2_status csa2_kv8_attn_tree(const csa2_kv8_cache* cache, const csa2_rows* q, 
   Kv8Scores sc = scores_of(*scores, a);
   sc.parent = parent;
   sc.rows_out = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kv8_ws(cache).total);
+  if (a.T * a.G > 64) a.part = sc.rows_out;   // the one or the other
   Kv8Left left{};
   const cudaError_t e = scored(a, sc, &left, (cudaStream_t)stream);
   return done(e != cudaSuccess ? e

@@ -69,15 +69,20 @@ struct PreSmem {
   static constexpr int kBytes = kMisc + 512 < 120 * 1024 ? 120 * 1024 : kMisc + 512;
 };
 
+// What changes the logits: nothing; nothing but which rows count; a cap; a slope;
+// both.
+enum Kind { kPlain, kMasked, kCapped, kSloped, kBoth };
+
 struct PreParams {
   Kv8Attn a;
   int32_t rows, row_tiles, splits;
   Kv8Scores sc;                                      // what changes the scores (SCORED)
 };
 
-template <int D, int FMT, bool SCORED>
+template <int D, int FMT, int KIND>
 __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
   using L = PreSmem<D>;
+  constexpr bool SCORED = KIND != kPlain;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Kv8& c = p.a.c;
@@ -179,9 +184,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
       lim = p.sc.sees(pos, n, prefix);
       low = p.sc.from(pos);
       at = (float)pos;
-      if (p.sc.slopes) slope = p.sc.slopes[hd] * kLog2e;
+      if (KIND == kSloped || KIND == kBoth) slope = p.sc.slopes[hd] * kLog2e;
     }
-    const bool changed = SCORED && (p.sc.cap2 > 0.0f || p.sc.slopes);
     float mul = 0.0f;
     constexpr int kPer = D / 8;                            // 16-byte chunks of a row
     constexpr int kAt = 32 / kPer;                         // rows of a warp's access
@@ -265,17 +269,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
             if (j < to && j >= from) s[j] = 0xFF800000u;
         }
       };
-      // SCORED: the logits as the model changes them, in base 2
-      auto change = [&](uint32_t (&s)[16], int u) {
+      // kSloped: logits in base 2, plus `add`; a row's bias is linear in the column
+      // but where a prefix lets rows behind the query count
+      bool mirrored = false;
+      if (KIND == kSloped && p.sc.prefix)
+        mirrored = __any_sync(0xffffffffu, at < (float)(key0 + kTileKeys - 1));
+      auto sloped = [&](uint32_t (&s)[16], int u, float add) {
+        const uint64_t f = pack2(mul, mul);
+        const float d0 = (float)(key0 + 16 * u) - at;
+        const uint64_t by = pack2(slope, slope), more = pack2(add, add);
+        uint64_t d = pack2(d0, d0 + 1.0f);                 // exact, like every step
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          uint64_t bias = d;
+          if (mirrored) {
+            float x, y;
+            unpack2(d, x, y);
+            bias = pack2(-fabsf(x), -fabsf(y));
+          }
+          bias = fma2(bias, by, more);
+          d = add2(d, pack2(2.0f, 2.0f));
+          float x, y;
+          unpack2(fma2(pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), f, bias), x, y);
+          s[j] = __float_as_uint(x);
+          s[j + 1] = __float_as_uint(y);
+        }
+      };
+      // kCapped, kBoth: capped logits in base 2
+      auto capped = [&](uint32_t (&s)[16]) {
         const uint64_t f = pack2(mul, mul);
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
           float x, y;
           unpack2(mul2(pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), f), x, y);
-          if (p.sc.cap2 > 0.0f) kv8_cap2(x, y, p.sc.cap2);
-          const float d = at - (float)(key0 + 16 * u + j);
-          s[j] = __float_as_uint(fmaf(-slope, fabsf(d), x));
-          s[j + 1] = __float_as_uint(fmaf(-slope, fabsf(d - 1.0f), y));
+          kv8_cap2(x, y, p.sc.cap2);
+          s[j] = __float_as_uint(x);
+          s[j + 1] = __float_as_uint(y);
         }
       };
       // f(columns 16 u .., u) for u = 0 .. 7, the next ones on their way meanwhile
@@ -303,24 +332,52 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
           tops[(j >> 1) & 1] =
               fmaxf(tops[(j >> 1) & 1], fmaxf(__uint_as_float(s[j]), __uint_as_float(s[j + 1])));
       };
-      if (SCORED && changed) {
+      float size = 0.0f;                                   // kCapped: the largest |logit|
+      if constexpr (KIND == kBoth) {
+        // (taken once, and kept in tensor memory)
         each([&](uint32_t (&s)[16], int u) {
-          change(s, u);
+          capped(s);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            s[j] = __float_as_uint(fmaf(-slope, fabsf(at - (float)(key0 + 16 * u + j)), __uint_as_float(s[j])));
           if (masked) hide(s, u);
           largest(s, u);
           tmem_st16(tS + 16 * u, s);
         });
         tmem_st_wait();
-      } else if (masked) {
+      } else if constexpr (KIND == kSloped) {
         each([&](uint32_t (&s)[16], int u) {
-          hide(s, u);
+          sloped(s, u, 0.0f);
+          if (masked) hide(s, u);
           largest(s, u);
         });
       } else {
-        each(largest);
+        if constexpr (KIND == kCapped) {
+          each([&](uint32_t (&s)[16], int u) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 2)
+              size = fmaxf(size, fmaxf(fabsf(__uint_as_float(s[j])), fabsf(__uint_as_float(s[j + 1]))));
+            if (masked) hide(s, u);
+            largest(s, u);
+          });
+        } else if (masked) {
+          each([&](uint32_t (&s)[16], int u) {
+            hide(s, u);
+            largest(s, u);
+          });
+        } else {
+          each(largest);
+        }
       }
-      const float by = SCORED && changed ? 1.0f : mul;     // what the logits lack
-      const float top = fmaxf(tops[0], tops[1]) * by;
+      // what the logits in tensor memory lack to base 2
+      const float by = KIND == kSloped || KIND == kBoth ? 1.0f : mul;
+      float top = fmaxf(tops[0], tops[1]) * by;
+      if constexpr (KIND == kCapped) {                     // (the cap keeps their order)
+        float same = top;
+        const bool none = top == -INFINITY;
+        kv8_cap2(top, same, p.sc.cap2);
+        if (none) top = -INFINITY;
+      }
       // (a row without a visible key so far waits for one; no row's result
       // depends on another's)
       const bool raise = top > m + 8.0f;
@@ -352,7 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
       // it would carry P out of range (ulp(2^16) = 2^-7), the logits are rounded
       // like m, which makes the largest difference 0 again.
       const float mm = m == -INFINITY ? 0.0f : m;
-      const uint64_t f2 = pack2(by, by), u2 = pack2(7.0f - mm, 7.0f - mm);
+      const float less = 7.0f - mm;
+      const uint64_t f2 = pack2(by, by), u2 = pack2(less, less);
       auto weights = [&](uint32_t (&s)[16], int u) {        // exponents -> P
         uint32_t w[8];
 #pragma unroll
@@ -372,19 +430,49 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
           s[j + 1] = __float_as_uint(y);
         }
       };
-      if (__any_sync(0xffffffffu, fabsf(mm) > 65536.0f)) {
+      if (KIND != kCapped && __any_sync(0xffffffffu, fabsf(mm) > 65536.0f)) {
 #pragma unroll 1
         for (int u = 0; u < 8; ++u) {
           uint32_t s[16];
           tmem_ld16(tS + 16 * u, s);
           tmem_ld_wait();
           reg_fence(s);
+          if constexpr (KIND == kSloped) sloped(s, u, 0.0f);
           hide(s, u);
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             s[j] = __float_as_uint((__fmul_rn(__uint_as_float(s[j]), by) - mm) + 7.0f);
           weights(s, u);
         }
+      } else if constexpr (KIND == kCapped) {
+        if (__any_sync(0xffffffffu, !(size * mul <= kTanhNear))) {
+          each([&](uint32_t (&s)[16], int u) {
+            capped(s);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) + less);
+            if (masked) hide(s, u);
+            weights(s, u);
+          });
+        } else {
+          each([&](uint32_t (&s)[16], int u) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              const uint64_t x = mul2(pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), f2);
+              float e0, e1;
+              unpack2(kv8_cap_near(x, p.sc.cap2, u2), e0, e1);
+              s[j] = __float_as_uint(e0);
+              s[j + 1] = __float_as_uint(e1);
+            }
+            if (masked) hide(s, u);
+            weights(s, u);
+          });
+        }
+      } else if constexpr (KIND == kSloped) {
+        each([&](uint32_t (&s)[16], int u) {
+          sloped(s, u, less);
+          if (masked) hide(s, u);
+          weights(s, u);
+        });
       } else if (masked) {
         each([&](uint32_t (&s)[16], int u) {
           hide(s, u);
@@ -756,9 +844,9 @@ __global__ void __launch_bounds__(256) kv8_prefill_combine_kernel(PreParams p) {
 }
 
 // left: where the rows outside the cache are joined to the results.
-template <int D, int FMT, bool SCORED>
+template <int D, int FMT, int KIND>
 cudaError_t prefill_as(const PreParams& p, cudaStream_t s, Kv8Left* left) {
-  auto kern = kv8_prefill_kernel<D, FMT, SCORED>;
+  auto kern = kv8_prefill_kernel<D, FMT, KIND>;
   static std::atomic<uint64_t> seen;
   cudaError_t e = kv8_prepare(kern, PreSmem<D>::kBytes, seen);
   if (e != cudaSuccess) return e;
@@ -770,23 +858,25 @@ cudaError_t prefill_as(const PreParams& p, cudaStream_t s, Kv8Left* left) {
                     dim3((p.rows + 7) / 8, p.a.c.heads * p.a.c.batch), 256, 0, s, p);
 }
 
-template <bool SCORED>
+template <int KIND>
 cudaError_t prefill_any(const Kv8Attn& a, const Kv8Scores& sc, int num_sms, cudaStream_t s,
                         Kv8Left* left) {
   PreParams p{a, a.T * a.G, (a.T * a.G + kTileRows - 1) / kTileRows, 1, sc};
   // Fewer CTAs than SMs: the cached rows are split, into parts of at least 8 tiles.
   const int64_t base = (int64_t)a.c.heads * a.c.batch * p.row_tiles;
   const int limit = num_sms < kKv8SplitCtas ? num_sms : kKv8SplitCtas;
-  if (2 * base <= limit) {
-    const int64_t seen = SCORED ? kv8_most_rows(a, sc) : a.c.max_len;
+  const int64_t seen = KIND != kPlain ? kv8_most_rows(a, sc) : a.c.max_len;
+  if (KIND != kPlain && left) {
+    p.splits = kv8_tree_splits(base, seen);
+  } else if (2 * base <= limit) {
     const int most = (int)((seen + 8 * kTileKeys - 1) / (8 * kTileKeys));
     p.splits = (int)(limit / base) < most ? (int)(limit / base) : most;
   }
   if (a.c.format == CSA2_KV8_E4M3)
-    return a.D == 64 ? prefill_as<64, CSA2_KV8_E4M3, SCORED>(p, s, left)
-                     : prefill_as<128, CSA2_KV8_E4M3, SCORED>(p, s, left);
-  return a.D == 64 ? prefill_as<64, CSA2_KV8_INT8, SCORED>(p, s, left)
-                   : prefill_as<128, CSA2_KV8_INT8, SCORED>(p, s, left);
+    return a.D == 64 ? prefill_as<64, CSA2_KV8_E4M3, KIND>(p, s, left)
+                     : prefill_as<128, CSA2_KV8_E4M3, KIND>(p, s, left);
+  return a.D == 64 ? prefill_as<64, CSA2_KV8_INT8, KIND>(p, s, left)
+                   : prefill_as<128, CSA2_KV8_INT8, KIND>(p, s, left);
 }
 
 }  // namespace

@@ -146,7 +146,7 @@ __device__ __forceinline__ char* row_at(const Kv8Rows& r, int es, int b, int tok
 // thread's cosines and sines serve all heads of the token.
 constexpr int kRopeThreads = 256, kRopePass = 3;
 template <int D, int TYPE>
-__global__ void __launch_bounds__(kRopeThreads) kv8_rope_kernel(RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, TYPE == CSA2_F32 ? 2 : 4) kv8_rope_kernel(RopeParams p) {
   griddep_wait();
   griddep_launch_dependents();
   constexpr int kLanes = D / 16, kSize = TYPE == CSA2_F32 ? 4 : 2;
@@ -154,6 +154,22 @@ __global__ void __launch_bounds__(kRopeThreads) kv8_rope_kernel(RopeParams p) {
   int t = p.len ? p.len[b] : p.T;
   t = t < 0 ? 0 : (t > p.T ? p.T : t);
   if (tok >= t) return;
+  const int u = threadIdx.x % kLanes, sub = threadIdx.x / kLanes, rows = blockDim.x / kLanes;
+  const int all = p.heads[0] + p.heads[1];
+  Chunks k = chunks_of<D>(p.r, u);
+  Eight<TYPE> x[kRopePass], y[kRopePass];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < kRopePass; ++i) {
+      const int h = h0 + i * rows;
+      if (h >= all) break;
+      const int set = h >= p.heads[0];
+      const char* from = row_at(p.in[set], kSize, b, tok, set ? h - p.heads[0] : h);
+      x[i].load(from, k.a);
+      y[i].load(from, k.b);
+    }
+  };
+  load(sub);               // on their way while the position is looked up
   int at;
   if (p.pos) {
     at = p.pos[(int64_t)b * p.T + tok];
@@ -169,22 +185,10 @@ __global__ void __launch_bounds__(kRopeThreads) kv8_rope_kernel(RopeParams p) {
   }
   const bool inside = at >= 0 && at < p.r.positions;
   if (!inside && threadIdx.x == 0) set_status(p.status, CSA2_DEV_BAD_INDEX);
-  const int u = threadIdx.x % kLanes, sub = threadIdx.x / kLanes, rows = blockDim.x / kLanes;
-  Chunks k = chunks_of<D>(p.r, u);
   k.on &= inside;
   const Turn turn = turn_at(p.r, k, u, at);
-  const int all = p.heads[0] + p.heads[1];
   for (int h0 = sub; h0 < all; h0 += kRopePass * rows) {
-    Eight<TYPE> x[kRopePass], y[kRopePass];
-#pragma unroll
-    for (int i = 0; i < kRopePass; ++i) {
-      const int h = h0 + i * rows;
-      if (h >= all) break;
-      const int set = h >= p.heads[0];
-      const char* from = row_at(p.in[set], kSize, b, tok, set ? h - p.heads[0] : h);
-      x[i].load(from, k.a);
-      y[i].load(from, k.b);
-    }
+    if (h0 > sub) load(h0);
 #pragma unroll
     for (int i = 0; i < kRopePass; ++i) {
       const int h = h0 + i * rows;
@@ -207,8 +211,10 @@ __global__ void __launch_bounds__(kRopeThreads) kv8_rope_kernel(RopeParams p) {
 
 template <int D>
 cudaError_t rope_of(const RopeParams& p, cudaStream_t s) {
-  const int rows = p.heads[0] + p.heads[1], lanes = D / 16;
-  const int threads = rows * lanes >= kRopeThreads ? kRopeThreads : (rows * lanes + 31) / 32 * 32;
+  // as few threads as need no more passes
+  const int items = (p.heads[0] + p.heads[1]) * (D / 16);
+  const int passes = (items + kRopeThreads - 1) / kRopeThreads;
+  const int threads = ((items + passes - 1) / passes + 31) / 32 * 32;
   const dim3 grid(p.T, p.c.batch);
   const int type = p.in[0].type;
   auto kern = type == CSA2_F32    ? kv8_rope_kernel<D, CSA2_F32>

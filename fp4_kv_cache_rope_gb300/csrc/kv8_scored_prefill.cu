@@ -6,7 +6,11 @@ namespace csa2 {
 
 cudaError_t launch_kv8_scored_many(const Kv8Attn& a, const Kv8Scores& sc, int num_sms, Kv8Left* left,
                                    cudaStream_t s) {
-  return prefill_any<true>(a, sc, num_sms, s, left);
+  if (sc.cap2 > 0.0f)
+    return sc.slopes ? prefill_any<kBoth>(a, sc, num_sms, s, left)
+                     : prefill_any<kCapped>(a, sc, num_sms, s, left);
+  return sc.slopes ? prefill_any<kSloped>(a, sc, num_sms, s, left)
+                   : prefill_any<kMasked>(a, sc, num_sms, s, left);
 }
 
 cudaError_t set_wait_limit_kv8_scored(unsigned long long ns) { return set_wait_limit_here(ns); }

@@ -12,6 +12,7 @@ namespace csa2 {
 
 constexpr float kLog2e = 1.44269504f;
 constexpr int kNoQuery = 0x40000000;      // the "position" of a row without a query
+constexpr int kKv8TreeCtas = 304;         // of the many-row kernel's parts for drafted tokens
 constexpr int kKv8MaxWindow = 1 << 23;    // beyond any difference of two positions
 
 struct Kv8Scores {
@@ -76,6 +77,16 @@ inline int64_t kv8_most_rows(const Kv8Attn& a, const Kv8Scores& sc) {
   return seen < a.c.max_len ? seen : a.c.max_len;
 }
 
+// Splits of the cached rows for drafted tokens' queries in the many-row kernel (base
+// CTAs without), into parts of at least 1024 rows.  Their results are joined with
+// the drafted rows' in any case, so the CTAs may be cut to even out the sequences'
+// lengths.
+inline int kv8_tree_splits(int64_t base, int64_t most_rows) {
+  const int64_t most = (most_rows + 1023) / 1024, fit = kKv8TreeCtas / base;
+  const int64_t n = fit < most ? fit : most;
+  return n < 1 ? 1 : (int)n;
+}
+
 // Where the results of the cached rows are once the drafted ones are joined to them
 // (rows_out holds those that no entry here says otherwise of).
 struct Kv8Left {
@@ -124,6 +135,33 @@ __device__ __forceinline__ void kv8_cap2(float& x, float& y, float cap2) {
   const float r = kv8_rcp(qx * qy) * cap2;
   x = px * (qy * r);
   y = py * (qx * r);
+}
+
+// The same for |score / cap| <= kTanhNear from polynomials of degree 2 (8.4e-8; 3e-7 with
+// fp32's roundings), two scores of one query at a time: cap2 tanh(x) + add.
+constexpr float kTanhNear = 2.0f;
+__device__ __forceinline__ uint64_t kv8_pair(float x) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t kv8_cap_near(uint64_t x, float cap2, uint64_t add) {
+  uint64_t u, n, q, w, e;
+  asm("mul.rn.f32x2 %0, %1, %1;" : "=l"(u) : "l"(x));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(n) : "l"(u), "l"(kv8_pair(9.667574195191264e-4f)), "l"(kv8_pair(0.1096152737736702f)));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(n) : "l"(n), "l"(u), "l"(kv8_pair(1.0f)));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(q) : "l"(u), "l"(kv8_pair(1.5285835601389408e-2f)), "l"(kv8_pair(0.4429476857185364f)));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(q), "l"(u), "l"(kv8_pair(1.0f)));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(n) : "l"(n), "l"(x));
+  float q0, q1;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(q0), "=f"(q1) : "l"(q));
+  const float r = kv8_rcp(q0 * q1) * cap2;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(w) : "f"(q1), "f"(q0));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(w) : "l"(w), "l"(kv8_pair(r)));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(n), "l"(w), "l"(add));
+  return e;
 }
 
 // ------------------------------------- split of rows over the CTAs, as kv8_share
