@@ -247,15 +247,15 @@ __global__ void __launch_bounds__(32 * WARPS, decode_ctas(D, NT, WARPS))
     st0 = 0;
     x1 = steps;
   } else if (SCORED) {
-    const Kv8Share at = kv8_share_by(c, lane, units, p.ctas, blockIdx.x, [&](int i) {
-      return kv8_span<kStep>(p.a, p.sc, i).steps;
+    const Kv8SpanShare at = kv8_share_by(c, lane, units, p.ctas, blockIdx.x, [&](int i) {
+      return kv8_span<kStep>(p.a, p.sc, i);
     });
     if ((int)blockIdx.x >= at.ctas) return;
     x = at.x;
     x1 = at.x1;
     b = at.b;
-    span = kv8_span<kStep>(p.a, p.sc, b);
-    n = span.n;
+    span = at.span;
+    n = at.n;
     steps = at.steps;
     unit = at.unit;
     st0 = at.step;
@@ -759,7 +759,8 @@ cudaError_t decode_as(DecodeParams p, int num_sms, cudaStream_t s, Kv8Left* left
   // Short caches in one launch: 1000 rows take as long on the GPU as shared out
   // and joined (10.5 us), 2000 rows of few units longer (14.5 us against 10.4 us),
   // and the host, which bounds such calls, issues one launch less.
-  if ((SCORED ? kv8_most_rows(p.a, p.sc) : p.a.c.max_len) <= kShort) {
+  // (Drafted tokens' results are joined with their rows anyway: few units are shared.)
+  if ((SCORED ? kv8_most_rows(p.a, p.sc) : p.a.c.max_len) <= kShort && !(left && units < num_sms)) {
     using L = DecodeSmem<D, kShortWarps>;
     auto kern = kv8_decode_kernel<D, NT, FMT, kShortWarps, SCORED>;
     static std::atomic<uint64_t> seen;

@@ -278,21 +278,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
         const uint64_t f = pack2(mul, mul);
         const float d0 = (float)(key0 + 16 * u) - at;
         const uint64_t by = pack2(slope, slope), more = pack2(add, add);
-        uint64_t d = pack2(d0, d0 + 1.0f);                 // exact, like every step
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          uint64_t bias = d;
-          if (mirrored) {
-            float x, y;
-            unpack2(d, x, y);
-            bias = pack2(-fabsf(x), -fabsf(y));
-          }
-          bias = fma2(bias, by, more);
-          d = add2(d, pack2(2.0f, 2.0f));
+        auto row = [&](uint64_t d, int j) {
           float x, y;
-          unpack2(fma2(pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), f, bias), x, y);
+          unpack2(fma2(pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), f, fma2(d, by, more)), x, y);
           s[j] = __float_as_uint(x);
           s[j + 1] = __float_as_uint(y);
+        };
+        if (mirrored) {
+#pragma unroll
+          for (int j = 0; j < 16; j += 2)
+            row(pack2(-fabsf(d0 + (float)j), -fabsf(d0 + (float)(j + 1))), j);
+        } else {
+          uint64_t d = pack2(d0, d0 + 1.0f);               // exact, like every step
+          const uint64_t two = pack2(2.0f, 2.0f);
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            row(d, j);
+            d = add2(d, two);
+          }
         }
       };
       // kCapped, kBoth: capped logits in base 2
@@ -313,7 +316,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
         tmem_ld16(tS, sa);
         tmem_ld_wait();
         reg_fence(sa);
-#pragma unroll
+// (what changes the scores takes so many instructions that eight copies of
+        // them would be fetched anew each time)
+#pragma unroll KIND == kPlain || KIND == kMasked ? 4 : 1
         for (int u = 0; u < 8; u += 2) {
           tmem_ld16(tS + 16 * (u + 1), sb);
           f(sa, u);
@@ -329,8 +334,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
       auto largest = [&](uint32_t (&s)[16], int) {
 #pragma unroll
         for (int j = 0; j < 16; j += 2)
-          tops[(j >> 1) & 1] =
-              fmaxf(tops[(j >> 1) & 1], fmaxf(__uint_as_float(s[j]), __uint_as_float(s[j + 1])));
+          tops[(j >> 1) & 1] = KIND == kPlain
+                                   ? fmaxf(tops[(j >> 1) & 1],
+                                           fmaxf(__uint_as_float(s[j]), __uint_as_float(s[j + 1])))
+                                   : max3(tops[(j >> 1) & 1], __uint_as_float(s[j]),
+                                          __uint_as_float(s[j + 1]));
       };
       float size = 0.0f;                                   // kCapped: the largest |logit|
       if constexpr (KIND == kBoth) {
@@ -356,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
           each([&](uint32_t (&s)[16], int u) {
 #pragma unroll
             for (int j = 0; j < 16; j += 2)
-              size = fmaxf(size, fmaxf(fabsf(__uint_as_float(s[j])), fabsf(__uint_as_float(s[j + 1]))));
+              size = max3_abs(size, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
             if (masked) hide(s, u);
             largest(s, u);
           });
@@ -445,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
           weights(s, u);
         }
       } else if constexpr (KIND == kCapped) {
-        if (__any_sync(0xffffffffu, !(size * mul <= kTanhNear))) {
+        if (__any_sync(0xffffffffu, !(size * mul <= kTanhNear && mul <= kNearMul))) {
           each([&](uint32_t (&s)[16], int u) {
             capped(s);
 #pragma unroll
@@ -454,14 +462,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
             weights(s, u);
           });
         } else {
+          const NearCap near(mul, p.sc.cap2);
           each([&](uint32_t (&s)[16], int u) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              const uint64_t x = mul2(pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), f2);
-              float e0, e1;
-              unpack2(kv8_cap_near(x, p.sc.cap2, u2), e0, e1);
-              s[j] = __float_as_uint(e0);
-              s[j + 1] = __float_as_uint(e1);
+            for (int j = 0; j < 16; j += 4) {
+              uint64_t a = pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+              uint64_t c = pack2(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
+              near(a, c, u2);
+              float x, y;
+              unpack2(a, x, y);
+              s[j] = __float_as_uint(x);
+              s[j + 1] = __float_as_uint(y);
+              unpack2(c, x, y);
+              s[j + 2] = __float_as_uint(x);
+              s[j + 3] = __float_as_uint(y);
             }
             if (masked) hide(s, u);
             weights(s, u);

@@ -138,69 +138,114 @@ __device__ __forceinline__ void kv8_cap2(float& x, float& y, float cap2) {
 }
 
 // The same for |score / cap| <= kTanhNear from polynomials of degree 2 (8.4e-8; 3e-7 with
-// fp32's roundings), two scores of one query at a time: cap2 tanh(x) + add.
-constexpr float kTanhNear = 2.0f;
-__device__ __forceinline__ uint64_t kv8_pair(float x) {
+// fp32's roundings), for logits s that `mul` takes to scores over the cap: the
+// polynomials take s itself, their coefficients the factor.  Four logits of a query at a
+// time, packed, two to a reciprocal.  (Beyond kNearMul a coefficient could be infinite;
+// one that is lost to 0 belongs to a term that is, too.)
+constexpr float kTanhNear = 2.0f, kNearMul = 1e6f;
+__device__ __forceinline__ uint64_t kv8_pair(float x, float y) {
   uint64_t r;
-  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
   return r;
 }
-__device__ __forceinline__ uint64_t kv8_cap_near(uint64_t x, float cap2, uint64_t add) {
-  uint64_t u, n, q, w, e;
-  asm("mul.rn.f32x2 %0, %1, %1;" : "=l"(u) : "l"(x));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(n) : "l"(u), "l"(kv8_pair(9.667574195191264e-4f)), "l"(kv8_pair(0.1096152737736702f)));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(n) : "l"(n), "l"(u), "l"(kv8_pair(1.0f)));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(q) : "l"(u), "l"(kv8_pair(1.5285835601389408e-2f)), "l"(kv8_pair(0.4429476857185364f)));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(q), "l"(u), "l"(kv8_pair(1.0f)));
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(n) : "l"(n), "l"(x));
-  float q0, q1;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(q0), "=f"(q1) : "l"(q));
-  const float r = kv8_rcp(q0 * q1) * cap2;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(w) : "f"(q1), "f"(q0));
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(w) : "l"(w), "l"(kv8_pair(r)));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(n), "l"(w), "l"(add));
-  return e;
+__device__ __forceinline__ uint64_t kv8_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t kv8_mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+struct NearCap {
+  uint64_t p0, p1, p2, q1, q2, one;
+  __device__ __forceinline__ NearCap(float mul, float cap2) {
+    const float m2 = mul * mul, c = cap2 * mul;
+    p0 = kv8_pair(c, c);
+    p1 = kv8_pair(c * (m2 * 0.1096152737736702f), c * (m2 * 0.1096152737736702f));
+    p2 = kv8_pair(c * (m2 * (m2 * 9.667574195191264e-4f)), c * (m2 * (m2 * 9.667574195191264e-4f)));
+    q1 = kv8_pair(m2 * 0.4429476857185364f, m2 * 0.4429476857185364f);
+    q2 = kv8_pair(m2 * (m2 * 1.5285835601389408e-2f), m2 * (m2 * 1.5285835601389408e-2f));
+    one = kv8_pair(1.0f, 1.0f);
+  }
+  // a, b: two logits each -> capped, plus `add`
+  __device__ __forceinline__ void operator()(uint64_t& a, uint64_t& b, uint64_t add) const {
+    const uint64_t ta = kv8_mul2(a, a), tb = kv8_mul2(b, b);
+    const uint64_t na = kv8_mul2(a, kv8_fma2(kv8_fma2(p2, ta, p1), ta, p0));
+    const uint64_t nb = kv8_mul2(b, kv8_fma2(kv8_fma2(p2, tb, p1), tb, p0));
+    const uint64_t qa = kv8_fma2(kv8_fma2(q2, ta, q1), ta, one);
+    const uint64_t qb = kv8_fma2(kv8_fma2(q2, tb, q1), tb, one);
+    const uint64_t q = kv8_mul2(qa, qb);
+    float x, y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(q));
+    const uint64_t r = kv8_pair(kv8_rcp(x), kv8_rcp(y));
+    a = kv8_fma2(na, kv8_mul2(qb, r), add);
+    b = kv8_fma2(nb, kv8_mul2(qa, r), add);
+  }
+};
+// Larger of three; of three magnitudes.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float d;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // ------------------------------------- split of rows over the CTAs, as kv8_share
-// kv8_share and kv8_sharers_of for steps that `steps_of` counts.
+// kv8_share and kv8_sharers_of for the steps of the spans that `span_of` gives.
+struct Kv8SpanShare : Kv8Share {
+  Kv8Span span;           // the first step's sequence's
+};
 template <class F>
-__device__ __forceinline__ Kv8Share kv8_share_by(const Kv8& c, int lane, int units, int max_ctas,
-                                                 int cta, F steps_of) {
-  Kv8Share r;
-  int64_t all = 0;
-  for (int b = lane; b < c.batch; b += 32) all += steps_of(b);
+__device__ __forceinline__ Kv8SpanShare kv8_share_by(const Kv8& c, int lane, int units, int max_ctas,
+                                                     int cta, F span_of) {
+  Kv8SpanShare r;
+  int64_t total = 0;
+  if (c.batch > 32) {
+    int64_t all = 0;
+    for (int b = lane; b < c.batch; b += 32) all += span_of(b).steps;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-  const int64_t total = all * units;
-  r.ctas = kv8_sharers(total, max_ctas);
-  r.x = kv8_muldiv(total, cta, r.ctas);
-  r.x1 = kv8_muldiv(total, cta + 1, r.ctas);
-  const int64_t x = r.x < total ? r.x : total - 1;
-  int64_t before = 0, first = 0;
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    total = all * units;
+  }
+  int64_t x = 0, before = 0, first = 0;
   for (int base = 0;; base += 32) {
-    const int b = base + lane;
-    const int steps = b < c.batch ? steps_of(b) : 0;
-    const int64_t mine = (int64_t)steps * units;
-    int64_t incl = mine;
+    Kv8Span mine{};
+    if (base + lane < c.batch) mine = span_of(base + lane);
+    int incl = mine.steps;  // at most 32 * 2^14 steps
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
-    const uint32_t hit = __ballot_sync(0xffffffffu, before + incl > x);
+    const int sum = __shfl_sync(0xffffffffu, incl, 31);
+    if (base == 0) {
+      if (c.batch <= 32) total = (int64_t)sum * units;
+      r.ctas = kv8_sharers(total, max_ctas);
+      r.x = kv8_muldiv(total, cta, r.ctas);
+      r.x1 = kv8_muldiv(total, cta + 1, r.ctas);
+      x = r.x < total ? r.x : total - 1;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, before + (int64_t)incl * units > x);
     if (hit || base + 32 >= c.batch) {
       const int l = hit ? __ffs(hit) - 1 : (c.batch - 1) & 31;
-      first = before + __shfl_sync(0xffffffffu, incl - mine, l);
+      first = before + (int64_t)__shfl_sync(0xffffffffu, incl - mine.steps, l) * units;
       r.b = base + l;
-      r.steps = __shfl_sync(0xffffffffu, steps, l);
+      r.span.n = __shfl_sync(0xffffffffu, mine.n, l);
+      r.span.steps = __shfl_sync(0xffffffffu, mine.steps, l);
+      r.span.sinks = __shfl_sync(0xffffffffu, mine.sinks, l);
+      r.span.first = __shfl_sync(0xffffffffu, mine.first, l);
       break;
     }
-    before += __shfl_sync(0xffffffffu, incl, 31);
+    before += (int64_t)sum * units;
   }
-  r.n = kv8_len(c, r.b);
+  r.n = r.span.n;
+  r.steps = r.span.steps;
   r.unit = (int)kv8_muldiv(x - first, 1, r.steps);
   r.step = (int)(x - first - (int64_t)r.unit * r.steps);
   return r;

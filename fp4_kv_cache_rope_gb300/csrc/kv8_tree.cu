@@ -28,23 +28,28 @@ template <int D>
 struct Share {
   static constexpr int kCh = D / 8;
   float v[kCh];
-  __device__ __forceinline__ void load(const Kv8Rows& r, int64_t at, int l8) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(r.data) + 2 * at) + l8;
+  __device__ __forceinline__ void take(const uint4 (&raw)[D / 64], int type) {
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
-      const uint4 w = p[8 * c];
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+      const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (r.type == CSA2_BF16) {
-          bf16x2_to_f32(ww[i], v[8 * c + 2 * i], v[8 * c + 2 * i + 1]);
+        if (type == CSA2_BF16) {
+          bf16x2_to_f32(w[i], v[8 * c + 2 * i], v[8 * c + 2 * i + 1]);
         } else {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&ww[i]));
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
           v[8 * c + 2 * i] = f.x;
           v[8 * c + 2 * i + 1] = f.y;
         }
       }
     }
+  }
+  __device__ __forceinline__ void load(const Kv8Rows& r, int64_t at, int l8) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(r.data) + 2 * at) + l8;
+    uint4 raw[D / 64];
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) raw[c] = p[8 * c];
+    take(raw, r.type);
   }
   __device__ __forceinline__ void load(const float* row, int l8) {
 #pragma unroll
@@ -71,48 +76,49 @@ struct Running {
   }
 };
 
-// WARPS: warps of a query row.  Each group of eight lanes takes every 4 WARPS-th of
-// the parts, then of the path's rows.
-template <int D, int WARPS>
+// WIDE: a CTA's eight warps for one query row, whose parts and path their 32 groups of
+// eight lanes take in turn.  Otherwise a group for a row: a token's heads lie next to
+// each other, so the four groups of a warp read the same drafted rows, and nothing is
+// left to put together.
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(kJoinThreads) kv8_tree_join_kernel(JoinParams p) {
-  constexpr int kRows = kJoinWarps / WARPS;
+  constexpr int kRows = WIDE ? 1 : 4 * kJoinWarps;
   __shared__ uint8_t path[kRows][CSA2_KV8_MAX_TREE];
   __shared__ float stat[2][kJoinWarps];
-  __shared__ float outs[WARPS > 1 ? kJoinWarps : 1][D];
+  __shared__ float outs[WIDE ? kJoinWarps : 1][D];
   griddep_wait();
   griddep_launch_dependents();
   const Kv8& c = p.a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l8 = lane & 7;
-  const int64_t row = (int64_t)blockIdx.x * kRows + warp / WARPS;    // of [B, T, H]
-  const int hd = (int)(row % p.a.H), tok = (int)(row / p.a.H % p.a.T);
-  const int64_t b64 = row / p.a.H / p.a.T;
-  if (b64 >= c.batch) return;                // a whole warp; WARPS > 1: the whole CTA
-  const int b = (int)b64;
+  const int grp = warp * 4 + (lane >> 3);
+  const int64_t rows = (int64_t)c.batch * p.a.T * p.a.H;
+  int64_t row = WIDE ? blockIdx.x : (int64_t)blockIdx.x * kRows + grp;   // of [B, T, H]
+  bool real = row < rows;
+  if (!real) row = rows - 1;
+  const int hd = (int)(row % p.a.H), tok = (int)(row / p.a.H % p.a.T), b = (int)(row / p.a.H / p.a.T);
   int ql = p.a.q_len ? p.a.q_len[b] : p.a.T;
   ql = ql < 0 ? 0 : (ql > p.a.T ? p.a.T : ql);
-  if (tok >= ql) return;                     // alike
+  real &= tok < ql;
+  if (WIDE && !real) return;                 // (the whole CTA)
   const int n = kv8_len(c, b), h = hd / p.a.G;
 
   // ---- the path: itself, its parent, ..
-  const int32_t* parent = p.sc.parent + (int64_t)b * p.a.T;
-  uint8_t* mine = path[warp / WARPS];
-  int depth = 0;
-  {
+  uint8_t* mine = path[WIDE ? 0 : grp];
+  int depth = -1;
+  if (real) {
+    const int32_t* parent = p.sc.parent + (int64_t)b * p.a.T;
     bool bad = false;
-    int at = tok;
-    for (;; ++depth) {
-      if (lane == 0 && warp % WARPS == 0) mine[depth] = (uint8_t)at;
+    for (int at = tok;;) {
+      ++depth;
+      if (l8 == 0) mine[depth] = (uint8_t)at;
       const int up = parent[at];
-      if (up < 0) break;
-      if (up >= at) {
-        bad = true;
-        break;
-      }
+      bad = up >= at;
+      if (up < 0 || bad) break;
       at = up;
     }
-    if (bad && lane == 0) set_status(p.a.status, CSA2_DEV_BAD_TREE);
+    if (bad && l8 == 0) set_status(p.a.status, CSA2_DEV_BAD_TREE);
   }
-  if (WARPS > 1)
+  if (WIDE)
     __syncthreads();
   else
     __syncwarp();
@@ -120,26 +126,37 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_tree_join_kernel(JoinParams 
   Share<D> q;
   q.load(p.a.q, b * p.a.q.sb + (int64_t)tok * p.a.q.st + (int64_t)hd * p.a.q.sh, l8);
   Running<D> all;
-  const int grp = warp % WARPS * 4 + (lane >> 3);
-  constexpr int kGroups = 4 * WARPS;
+  const int from = WIDE ? grp : 0;
+  constexpr int kStride = WIDE ? 4 * kJoinWarps : 1;
 
   // ---- the cached rows' parts
   int parts = 1, c0 = 0, gr = tok * p.a.G + hd % p.a.G;
   if (p.left.kind == 1) {
-    int c1;
-    kv8_sharers_by(c, lane, c.heads * p.left.tiles, p.left.ctas, b,
-                   h * p.left.tiles + gr / p.left.tile_rows, c0, c1,
-                   [&](int i) { return kv8_span<kKv8Step>(p.a, p.sc, i).steps; });
-    parts = c1 - c0 + 1;
+    // (a whole warp's work: a row of each group after another)
+    const int unit = h * p.left.tiles + gr / p.left.tile_rows;
+#pragma unroll 1
+    for (int g = 0; g < 32; g += 8) {
+      int first, last;
+      kv8_sharers_by(c, lane, c.heads * p.left.tiles, p.left.ctas, __shfl_sync(0xffffffffu, b, g),
+                     __shfl_sync(0xffffffffu, unit, g), first, last,
+                     [&](int i) { return kv8_span<kKv8Step>(p.a, p.sc, i).steps; });
+      if (WIDE || (lane & 24) == g) {
+        c0 = first;
+        parts = last - first + 1;
+      }
+      if (WIDE) break;
+    }
   } else if (p.left.kind == 2) {
     parts = p.left.ctas;
   }
+  if (!real) parts = 0;
   const int in = gr % max(p.left.tile_rows, 1);
-  for (int i = grp; i < parts; i += kGroups) {
+#pragma unroll 2
+  for (int i = from; i < parts; i += kStride) {
     const float *o, *m, *s;
     if (p.left.kind == 2) {
-      const int64_t id =
-          (((int64_t)(p.left.tiles - 1 - gr / kPreRows) * c.batch + b) * parts + i) * c.heads + h;
+      const int64_t id = (((int64_t)(p.left.tiles - 1 - gr / kPreRows) * c.batch + b) * p.left.ctas + i) *
+                             c.heads + h;
       const float* part = p.a.part + id * kPreRows * (D + 2);
       o = part + in * D;
       m = part + kPreRows * D + in;
@@ -161,15 +178,32 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_tree_join_kernel(JoinParams 
     all.join(p.left.kind == 2 ? *m - 7.0f : *m, *s, y.v);
   }
 
-  // ---- the path's rows
+  // ---- the path's rows, the next one on its way while one is worked on
   const float slope = p.sc.slopes ? p.sc.slopes[hd] * kLog2e : 0.0f;
-  for (int i0 = 0; i0 <= depth; i0 += kGroups) {   // (whole warps: the dot's shuffles)
-    const int i = i0 + grp;
-    const bool ok = i <= depth && (!p.sc.window || i < p.sc.window || n + depth - i < p.sc.sink);
-    const int64_t at = ok ? mine[i] : tok;
+  const char* kp = static_cast<const char*>(p.k.data) + 2 * (b * p.k.sb + (int64_t)h * p.k.sh);
+  const char* vp = static_cast<const char*>(p.v.data) + 2 * (b * p.v.sb + (int64_t)h * p.v.sh);
+  constexpr int kC = D / 64;
+  uint4 rk[kC], rv[kC];
+  auto fetch = [&](int i) {
+    const int64_t at = i <= depth ? mine[i] : 0;   // (a row that is there)
+    const uint4* k = reinterpret_cast<const uint4*>(kp + 2 * at * p.k.st) + l8;
+    const uint4* v = reinterpret_cast<const uint4*>(vp + 2 * at * p.v.st) + l8;
+#pragma unroll
+    for (int cc = 0; cc < kC; ++cc) {
+      rk[cc] = k[8 * cc];
+      rv[cc] = v[8 * cc];
+    }
+  };
+  // (whole warps: the dot's shuffles)
+  const int longest = __reduce_max_sync(0xffffffffu, depth);
+  fetch(from);
+#pragma unroll 1
+  for (int i0 = 0; i0 <= longest; i0 += kStride) {
+    const int i = i0 + from;
     Share<D> k, v;
-    k.load(p.k, b * p.k.sb + at * p.k.st + (int64_t)h * p.k.sh, l8);
-    v.load(p.v, b * p.v.sb + at * p.v.st + (int64_t)h * p.v.sh, l8);
+    k.take(rk, p.a.q.type);
+    v.take(rv, p.a.q.type);
+    if (i0 + kStride <= longest) fetch(i + kStride);
     float dot = 0.0f;
 #pragma unroll
     for (int e = 0; e < Share<D>::kCh; ++e) dot = fmaf(q.v[e], k.v[e], dot);
@@ -182,23 +216,24 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_tree_join_kernel(JoinParams 
       kv8_cap2(x, y, p.sc.cap2);
     }
     x = fmaf(-slope, (float)i, x);
+    const bool ok = i <= depth && (!p.sc.window || i < p.sc.window || n + depth - i < p.sc.sink);
     if (ok && x != -INFINITY) all.join(x, 1.0f, v.v);
   }
 
   // ---- the groups together
+  if (WIDE) {
 #pragma unroll
-  for (int d = 8; d < 32; d *= 2) {
-    float y[D / 8];
+    for (int d = 8; d < 32; d *= 2) {
+      float y[D / 8];
 #pragma unroll
-    for (int e = 0; e < D / 8; ++e) y[e] = __shfl_xor_sync(0xffffffffu, all.o[e], d);
-    const float m = __shfl_xor_sync(0xffffffffu, all.top, d);
-    const float s = __shfl_xor_sync(0xffffffffu, all.sum, d);
-    all.join(m, s, y);
-  }
-  if (WARPS > 1) {
+      for (int e = 0; e < D / 8; ++e) y[e] = __shfl_xor_sync(0xffffffffu, all.o[e], d);
+      const float m = __shfl_xor_sync(0xffffffffu, all.top, d);
+      const float s = __shfl_xor_sync(0xffffffffu, all.sum, d);
+      all.join(m, s, y);
+    }
     if (lane < 8) {
 #pragma unroll
-      for (int cc = 0; cc < D / 64; ++cc)
+      for (int cc = 0; cc < kC; ++cc)
 #pragma unroll
         for (int e = 0; e < 8; ++e) outs[warp][64 * cc + 8 * l8 + e] = all.o[8 * cc + e];
       if (lane == 0) {
@@ -209,25 +244,26 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_tree_join_kernel(JoinParams 
     __syncthreads();
     if (warp > 0) return;
 #pragma unroll
-    for (int w = 1; w < WARPS; ++w) {
+    for (int w = 1; w < kJoinWarps; ++w) {
       Share<D> y;
       y.load(outs[w], l8);
       all.join(stat[0][w], stat[1][w], y.v);
     }
+    real = lane < 8;
   }
-  if (lane < 8) {
+  if (real) {
     const float inv = all.sum == 0.0f ? 0.0f : 1.0f / all.sum;
     uint16_t* out = static_cast<uint16_t*>(const_cast<void*>(p.a.out.data)) + b * p.a.out.sb +
                     (int64_t)tok * p.a.out.st + (int64_t)hd * p.a.out.sh;
 #pragma unroll
-    for (int cc = 0; cc < D / 64; ++cc) {
+    for (int cc = 0; cc < kC; ++cc) {
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         w[e] = pack16(all.o[8 * cc + 2 * e] * inv, all.o[8 * cc + 2 * e + 1] * inv, p.a.out.type);
       *reinterpret_cast<uint4*>(out + 64 * cc + 8 * l8) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    if (p.a.lse && lane == 0)
+    if (p.a.lse && l8 == 0)
       p.a.lse[row] = all.sum == 0.0f ? -INFINITY : (all.top + log2f(all.sum)) * 0.6931471805599453f;
   }
 }
@@ -237,8 +273,9 @@ cudaError_t join_as(const JoinParams& p, int num_sms, cudaStream_t s) {
   const int64_t rows = (int64_t)p.a.c.batch * p.a.T * p.a.H;
   // Few query rows: eight warps each, for the parts of a unit that many CTAs shared.
   if (rows <= 16 * num_sms)
-    return kv8_launch(kv8_tree_join_kernel<D, kJoinWarps>, dim3((unsigned)rows), kJoinThreads, 0, s, p);
-  return kv8_launch(kv8_tree_join_kernel<D, 1>, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)),
+    return kv8_launch(kv8_tree_join_kernel<D, true>, dim3((unsigned)rows), kJoinThreads, 0, s, p);
+  constexpr int kRows = 4 * kJoinWarps;
+  return kv8_launch(kv8_tree_join_kernel<D, false>, dim3((unsigned)((rows + kRows - 1) / kRows)),
                     kJoinThreads, 0, s, p);
 }
 
