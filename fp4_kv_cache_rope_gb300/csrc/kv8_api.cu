@@ -230,7 +230,12 @@ Kv8Scores scores_of(const csa2_scores& s, const Kv8Attn& a) {
 }
 
 // Up to 64 query rows per (sequence, K/V head) go to the kernel that is bound by
-// the cache's bytes, more to the tensor cores', as in csa2_kv8_attn.
+// the cache's bytes, more to the tensor cores' (16 sequences of 9000 rows, 4 heads,
+// D 128: 62 us against 80 us for 48 rows, 78 against 80 for 64, 92 against 82 for 80).
+cudaError_t plain(const Kv8Attn& a, cudaStream_t s) {
+  return a.T * a.G <= 64 ? launch_kv8_attn(a, sms(), s) : launch_kv8_prefill(a, sms(), s);
+}
+// The same with changed scores.
 cudaError_t scored(const Kv8Attn& a, const Kv8Scores& sc, Kv8Left* left, cudaStream_t s) {
   return a.T * a.G <= 64 ? launch_kv8_scored_few(a, sc, sms(), left, s)
                          : launch_kv8_scored_many(a, sc, sms(), left, s);
@@ -277,11 +282,7 @@ csa2_status csa2_kv8_attn(const csa2_kv8_cache* cache, const csa2_rows* q, int32
   Kv8Attn a = attn_of(cache, q, H, T, q_len, softmax_scale, ws);
   a.out = rows_of(*out);
   a.lse = lse;
-  // Up to 64 query rows per (sequence, K/V head) go to the kernel that is bound by
-  // the cache's bytes, more to the tensor cores' (16 sequences of 9000 rows, 4 heads,
-  // D 128: 62 us against 80 us for 48 rows, 78 against 80 for 64, 92 against 82 for 80).
-  return done(a.T * a.G <= 64 ? launch_kv8_attn(a, sms(), (cudaStream_t)stream)
-                              : launch_kv8_prefill(a, sms(), (cudaStream_t)stream));
+  return done(plain(a, (cudaStream_t)stream));
 }
 
 csa2_status csa2_kv8_mass(const csa2_kv8_cache* cache, const csa2_rows* q, int32_t H, int32_t T,
@@ -401,7 +402,10 @@ csa2_status csa2_kv8_attn_scored(const csa2_kv8_cache* cache, const csa2_rows* q
   Kv8Attn a = attn_of(cache, q, H, T, q_len, softmax_scale, ws);
   a.out = rows_of(*out);
   a.lse = lse;
-  return done(scored(a, scores_of(*scores, a), nullptr, (cudaStream_t)stream));
+  const Kv8Scores sc = scores_of(*scores, a);
+  if (!(sc.cap2 > 0.0f) && !sc.window && !sc.slopes && !sc.prefix)   // nothing changes
+    return done(plain(a, (cudaStream_t)stream));
+  return done(scored(a, sc, nullptr, (cudaStream_t)stream));
 }
 
 size_t csa2_kv8_tree_workspace_size(const csa2_kv8_cache* cache, int32_t T, int32_t H) {

@@ -106,6 +106,7 @@ __device__ __forceinline__ Turn turn_at(const RopeTable& r, const Chunks& k, int
   }
   return t;
 }
+// (Single operations: the packed product and sum are contracted into one that rounds once.)
 __device__ __forceinline__ void turn_pair(float& x, float& y, float c, float s) {
   const float a = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
   y = __fadd_rn(__fmul_rn(x, s), __fmul_rn(y, c));
@@ -144,9 +145,9 @@ __device__ __forceinline__ char* row_at(const Kv8Rows& r, int es, int b, int tok
 
 // One CTA per token, D / 16 threads a row, PASS rows of each thread in flight.  A
 // thread's cosines and sines serve all heads of the token.
-constexpr int kRopeThreads = 256, kRopePass = 3;
+constexpr int kRopeThreads = 256, kRopePass = 1;
 template <int D, int TYPE>
-__global__ void __launch_bounds__(kRopeThreads, TYPE == CSA2_F32 ? 2 : 4) kv8_rope_kernel(RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, TYPE == CSA2_F32 ? 4 : 6) kv8_rope_kernel(RopeParams p) {
   griddep_wait();
   griddep_launch_dependents();
   constexpr int kLanes = D / 16, kSize = TYPE == CSA2_F32 ? 4 : 2;
@@ -250,7 +251,23 @@ struct TurnedRows {
     const int u = tid % kLanes, sub = tid / kLanes;
     k = chunks_of<D>(p.r, u);
     s0 = had ? *scale : 0.0f;
+    // Everything is asked for before anything is used, up to two rows' tables at a time.
+    constexpr int kAhead = PASSES < 2 ? PASSES : 2;
     Eight<TYPE> x[PASSES], y[PASSES];
+    Turn turn[kAhead];
+    bool on[kAhead];
+    auto look_up = [&](int i) {
+      const int at = lo + i * kRows + sub;
+      on[i % kAhead] = false;
+      if (i >= PASSES || at >= hi) return;
+      const int pos = rope_position(p, sp, b, at - sp.start);
+      if (pos < 0 || pos >= p.r.positions) {
+        if (u == 0) set_status(p.a.status, CSA2_DEV_BAD_INDEX);
+        return;
+      }
+      on[i % kAhead] = k.on;
+      turn[i % kAhead] = turn_at(p.r, k, u, pos);
+    };
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
       const int at = lo + i * kRows + sub;
@@ -263,18 +280,13 @@ struct TurnedRows {
       }
     }
 #pragma unroll
+    for (int i = 0; i < kAhead; ++i) look_up(i);
+#pragma unroll
     for (int i = 0; i < PASSES; ++i) {
-      const int at = lo + i * kRows + sub;
       x[i].to(v[i][0]);
       y[i].to(v[i][1]);
-      if (at >= hi) continue;
-      const int pos = rope_position(p, sp, b, at - sp.start);
-      if (pos < 0 || pos >= p.r.positions) {
-        if (u == 0) set_status(p.a.status, CSA2_DEV_BAD_INDEX);
-      } else if (k.on) {
-        const Turn t = turn_at(p.r, k, u, pos);
-        turn_rows(v[i][0], v[i][1], t, p.r.style);
-      }
+      if (on[i % kAhead]) turn_rows(v[i][0], v[i][1], turn[i % kAhead], p.r.style);
+      if (i + kAhead < PASSES) look_up(i + kAhead);
     }
   }
 
@@ -284,12 +296,12 @@ struct TurnedRows {
                                         const Chunks& k) {
     const int sub = tid / kLanes;
     constexpr uint32_t kInf = 0x7F800000u;
-    uint32_t bits = 0;
+    float top = 0.0f;                      // a NaN stays one
 #pragma unroll
     for (int i = 0; i < PASSES; ++i)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) bits = max(bits, __float_as_uint(v[i][e >> 3][e & 7]) & 0x7FFFFFFFu);
-    bits = group_max<NT>(bits, red, tid);
+      for (int e = 0; e < 16; e += 2) top = max3_abs_nan(top, v[i][e >> 3][e & 7], v[i][e >> 3][(e & 7) + 1]);
+    uint32_t bits = group_max<NT>(__float_as_uint(top), red, tid);
     const bool odd = bits >= kInf;         // uniform over the group
     if (odd) {                             // the maximum of the finite values then
       if (tid == 0) set_status(p.a.status, CSA2_DEV_NONFINITE);
@@ -306,20 +318,20 @@ struct TurnedRows {
     __syncwarp();                          // every thread of the group has read s0
     const float s1 = fmaxf(s0, kv8_scale_of<FMT>(__uint_as_float(bits)));
     const float inv = kv8_inverse(s1);
-    const float big = s1 > 0.0f ? (FMT == CSA2_KV8_E4M3 ? 448.0f : 127.0f) : 0.0f;
     uint8_t* dst = codes + (row0 + (lo - b0) + sub) * D;
+    const uint64_t by = kv8_pair(inv, inv);
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
       if (lo + i * kRows + sub >= hi) continue;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float (&x)[8] = v[i][c];
+        float x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (odd)
-            x[e] = fabsf(x[e]) <= 3.402823466e38f ? x[e] * inv : x[e] != x[e] ? 0.0f : copysignf(big, x[e]);
-          else
-            x[e] *= inv;
+        for (int e = 0; e < 8; e += 2) kv8_split(kv8_mul2(kv8_pair(v[i][c][e], v[i][c][e + 1]), by), x[e], x[e + 1]);
+        if (odd) {                         // infinities to the largest code, NaN to 0
+          constexpr float kBig = FMT == CSA2_KV8_E4M3 ? 448.0f : 127.0f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = x[e] != x[e] ? 0.0f : fminf(fmaxf(x[e], -kBig), kBig);
         }
         *reinterpret_cast<uint2*>(dst + (int64_t)i * kRows * D + 8 * (c ? k.b : k.a)) =
             make_uint2(kv8_encode4<FMT>(x[0], x[1], x[2], x[3]), kv8_encode4<FMT>(x[4], x[5], x[6], x[7]));

@@ -143,21 +143,6 @@ __device__ __forceinline__ void kv8_cap2(float& x, float& y, float cap2) {
 // time, packed, two to a reciprocal.  (Beyond kNearMul a coefficient could be infinite;
 // one that is lost to 0 belongs to a term that is, too.)
 constexpr float kTanhNear = 2.0f, kNearMul = 1e6f;
-__device__ __forceinline__ uint64_t kv8_pair(float x, float y) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ uint64_t kv8_fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t kv8_mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 struct NearCap {
   uint64_t p0, p1, p2, q1, q2, one;
   __device__ __forceinline__ NearCap(float mul, float cap2) {
@@ -184,18 +169,6 @@ struct NearCap {
     b = kv8_fma2(nb, kv8_mul2(qa, r), add);
   }
 };
-// Larger of three; of three magnitudes.
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ float max3_abs(float a, float b, float c) {
-  float d;
-  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
 // ------------------------------------- split of rows over the CTAs, as kv8_share
 // kv8_share and kv8_sharers_of for the steps of the spans that `span_of` gives.
 struct Kv8SpanShare : Kv8Share {

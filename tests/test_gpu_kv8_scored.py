@@ -295,3 +295,26 @@ def test_trees_of_many_sequences_and_strides():
     K.kv8_attn_tree(p.c, *(fused[:, :, a:b].contiguous().cuda() for a, b in ((0, 4), (4, 6), (6, 8))),
                     ints(parent), y, ws)
     assert torch.equal(x[:, :, :4], y) and torch.equal(x[:, :, 4:].cpu(), fused[:, :, 4:])
+
+
+@pytest.mark.parametrize("T,G", [(1, 8), (5, 8), (40, 4)])
+@pytest.mark.parametrize("what", ["window", "cap", "far", "slopes", "both", "tree"])
+def test_scores_that_grow_along_the_rows(T, G, what):
+    """Every few rows raise the running maximum, inside tiles too; a cap that few, many
+    or all scores reach; and a row in front that stays the largest."""
+    for case in range(3):
+        p = Pair(2, 1, 64, 900, 32, 32, O.E4M3, seed=41 + case, mass=False)
+        ws = p.c.workspace(1, 1)
+        k, v = p.rows(900, 1, "f32"), p.rows(900, 1, "f32")
+        j = torch.arange(900.0)
+        size = [torch.exp(j / 170), torch.exp(2 * torch.sin(j / 9)) * (1 + j / 90), torch.ones(900)][case]
+        if case == 2:
+            size[3] = 60.0
+        p.append(k * size.view(1, -1, 1, 1), v, ws, lens=[900, 517])
+        args = {"window": dict(window=700, sink=10), "cap": dict(cap=40.0), "far": dict(cap=3.0),
+                "slopes": dict(slopes=slopes_of(G)), "both": dict(cap=25.0, slopes=slopes_of(G)),
+                "tree": dict()}[what]
+        if what == "tree":
+            run_tree(p, G, T, "bf16", size=2.0, chain=0.8)
+        else:
+            run_scored(p, G, T, "bf16", size=2.0, **args)
