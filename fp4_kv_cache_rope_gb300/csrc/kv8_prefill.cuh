@@ -41,6 +41,8 @@
 // L2, because L1 is left little beside the tiles.
 #pragma once
 
+#include <type_traits>
+
 #include "kv8_mma.cuh"
 #include "kv8_scores.cuh"
 
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
       bool mirrored = false;
       if (KIND == kSloped && p.sc.prefix)
         mirrored = __any_sync(0xffffffffu, at < (float)(key0 + kTileKeys - 1));
-      auto sloped = [&](uint32_t (&s)[16], int u, float add) {
+      auto sloped = [&](uint32_t (&s)[16], int u, float add, auto both) {
         const uint64_t f = pack2(mul, mul);
         const float d0 = (float)(key0 + 16 * u) - at;
         const uint64_t by = pack2(slope, slope), more = pack2(add, add);
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
           s[j] = __float_as_uint(x);
           s[j + 1] = __float_as_uint(y);
         };
-        if (mirrored) {
+        if constexpr (decltype(both)::value) {
 #pragma unroll
           for (int j = 0; j < 16; j += 2)
             row(pack2(-fabsf(d0 + (float)j), -fabsf(d0 + (float)(j + 1))), j);
@@ -298,6 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
           }
         }
       };
+      using Yes = std::integral_constant<bool, true>;
+      using No = std::integral_constant<bool, false>;
       // kCapped, kBoth: capped logits in base 2
       auto capped = [&](uint32_t (&s)[16]) {
         const uint64_t f = pack2(mul, mul);
@@ -316,9 +320,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
         tmem_ld16(tS, sa);
         tmem_ld_wait();
         reg_fence(sa);
-// (what changes the scores takes so many instructions that eight copies of
-        // them would be fetched anew each time)
-#pragma unroll KIND == kPlain || KIND == kMasked ? 4 : 1
+        // (what changes the scores takes so many instructions that eight copies of
+        // them would be fetched anew each time: two of them for prompts of 64 channels
+        // with slopes 46 us, four times two 53 us)
+#pragma unroll KIND == kPlain || KIND == kMasked ? 4 : KIND == kBoth ? 1 : 2
         for (int u = 0; u < 8; u += 2) {
           tmem_ld16(tS + 16 * (u + 1), sb);
           f(sa, u);
@@ -329,6 +334,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
           tmem_ld_wait();
           reg_fence(sa);
         }
+      };
+      // change, hide where some row does not see all, use: a loop of its own each way, for
+      // a branch in every step costs more than the code
+      auto pass = [&](auto change, auto use) {
+        if (masked)
+          each([&](uint32_t (&s)[16], int u) {
+            change(s, u);
+            hide(s, u);
+            use(s, u);
+          });
+        else
+          each([&](uint32_t (&s)[16], int u) {
+            change(s, u);
+            use(s, u);
+          });
       };
       float tops[2] = {-INFINITY, -INFINITY};
       auto largest = [&](uint32_t (&s)[16], int) {
@@ -343,31 +363,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
       float size = 0.0f;                                   // kCapped: the largest |logit|
       if constexpr (KIND == kBoth) {
         // (taken once, and kept in tensor memory)
-        each([&](uint32_t (&s)[16], int u) {
-          capped(s);
+        pass(
+            [&](uint32_t (&s)[16], int u) {
+              capped(s);
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            s[j] = __float_as_uint(fmaf(-slope, fabsf(at - (float)(key0 + 16 * u + j)), __uint_as_float(s[j])));
-          if (masked) hide(s, u);
-          largest(s, u);
-          tmem_st16(tS + 16 * u, s);
-        });
+              for (int j = 0; j < 16; ++j)
+                s[j] = __float_as_uint(fmaf(-slope, fabsf(at - (float)(key0 + 16 * u + j)), __uint_as_float(s[j])));
+            },
+            [&](uint32_t (&s)[16], int u) {
+              largest(s, u);
+              tmem_st16(tS + 16 * u, s);
+            });
         tmem_st_wait();
       } else if constexpr (KIND == kSloped) {
-        each([&](uint32_t (&s)[16], int u) {
-          sloped(s, u, 0.0f);
-          if (masked) hide(s, u);
-          largest(s, u);
-        });
+        if (mirrored)
+          pass([&](uint32_t (&s)[16], int u) { sloped(s, u, 0.0f, Yes{}); }, largest);
+        else
+          pass([&](uint32_t (&s)[16], int u) { sloped(s, u, 0.0f, No{}); }, largest);
       } else {
         if constexpr (KIND == kCapped) {
-          each([&](uint32_t (&s)[16], int u) {
+          pass(
+              [&](uint32_t (&s)[16], int) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 2)
-              size = max3_abs(size, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
-            if (masked) hide(s, u);
-            largest(s, u);
-          });
+                for (int j = 0; j < 16; j += 2)
+                  size = max3_abs(size, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+              },
+              largest);
         } else if (masked) {
           each([&](uint32_t (&s)[16], int u) {
             hide(s, u);
@@ -445,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
           tmem_ld16(tS + 16 * u, s);
           tmem_ld_wait();
           reg_fence(s);
-          if constexpr (KIND == kSloped) sloped(s, u, 0.0f);
+          if constexpr (KIND == kSloped) sloped(s, u, 0.0f, Yes{});
           hide(s, u);
 #pragma unroll
           for (int j = 0; j < 16; ++j)
@@ -454,39 +475,38 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
         }
       } else if constexpr (KIND == kCapped) {
         if (__any_sync(0xffffffffu, !(size * mul <= kTanhNear && mul <= kNearMul))) {
-          each([&](uint32_t (&s)[16], int u) {
-            capped(s);
+          pass(
+              [&](uint32_t (&s)[16], int) {
+                capped(s);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) + less);
-            if (masked) hide(s, u);
-            weights(s, u);
-          });
+                for (int j = 0; j < 16; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) + less);
+              },
+              weights);
         } else {
           const NearCap near(mul, p.sc.cap2);
-          each([&](uint32_t (&s)[16], int u) {
+          pass(
+              [&](uint32_t (&s)[16], int) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              uint64_t a = pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1]));
-              uint64_t c = pack2(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
-              near(a, c, u2);
-              float x, y;
-              unpack2(a, x, y);
-              s[j] = __float_as_uint(x);
-              s[j + 1] = __float_as_uint(y);
-              unpack2(c, x, y);
-              s[j + 2] = __float_as_uint(x);
-              s[j + 3] = __float_as_uint(y);
-            }
-            if (masked) hide(s, u);
-            weights(s, u);
-          });
+                for (int j = 0; j < 16; j += 4) {
+                  uint64_t a = pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+                  uint64_t c = pack2(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
+                  near(a, c, u2);
+                  float x, y;
+                  unpack2(a, x, y);
+                  s[j] = __float_as_uint(x);
+                  s[j + 1] = __float_as_uint(y);
+                  unpack2(c, x, y);
+                  s[j + 2] = __float_as_uint(x);
+                  s[j + 3] = __float_as_uint(y);
+                }
+              },
+              weights);
         }
       } else if constexpr (KIND == kSloped) {
-        each([&](uint32_t (&s)[16], int u) {
-          sloped(s, u, less);
-          if (masked) hide(s, u);
-          weights(s, u);
-        });
+        if (mirrored)
+          pass([&](uint32_t (&s)[16], int u) { sloped(s, u, less, Yes{}); }, weights);
+        else
+          pass([&](uint32_t (&s)[16], int u) { sloped(s, u, less, No{}); }, weights);
       } else if (masked) {
         each([&](uint32_t (&s)[16], int u) {
           hide(s, u);
