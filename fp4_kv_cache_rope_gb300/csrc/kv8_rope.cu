@@ -434,7 +434,8 @@ __global__ void __launch_bounds__(512) kv8_append_rope_few_kernel(AppendRopePara
 
 // Longer ones: one CTA per (block, head, side, sequence).  ROWS: of a block.
 template <int D, int TYPE, int FMT, int ROWS>
-__global__ void __launch_bounds__(kAppendThreads) kv8_append_rope_kernel(AppendRopeParams p) {
+__global__ void __launch_bounds__(kAppendThreads, ROWS <= 64 ? 4 : 2)
+    kv8_append_rope_kernel(AppendRopeParams p) {
   __shared__ uint32_t red[kAppendThreads / 32];
   griddep_wait();
   griddep_launch_dependents();
