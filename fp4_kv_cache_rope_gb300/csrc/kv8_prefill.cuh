@@ -39,6 +39,17 @@
 // exponentials.  That
 // keeps every role within its registers: a spilled register is read back from
 // L2, because L1 is left little beside the tiles.
+//
+// Changed scores (KIND).  A window or a prefix changes which tiles a CTA walks and what is
+// hidden in them.  A slope is a multiply-add in both readings of S, exact in the
+// distance.  A cap keeps the order of a row's logits, so the maximum is taken of the
+// plain ones and capped once; the second reading takes four logits at a time through a
+// quotient of polynomials in packed arithmetic (two operations in two cycles of the
+// FMA pipe, but one issue).  Both together are taken once and kept in tensor memory.
+// 4096 tokens of 64 heads at the end of 16384 rows, D 128: 2.69 ms with a cap, 2.57 ms with
+// slopes, 1.72 ms with a window that hides nothing, against 1.69 ms.  The two softmax
+// warps of an SM partition run chains of dependent instructions and leave half of its
+// issue slots unused.
 #pragma once
 
 #include <type_traits>

@@ -6,6 +6,10 @@
 // A path holds a handful of rows, so they are taken one by one: eight lanes a row,
 // fp32 throughout.  The cached rows' part, which is where the bytes are, comes from
 // the kernels that attend over the cache.
+//
+// Latency bounds it: lengths, the walk to the root, the parts, then a path row after
+// another.  Trees of 60 tokens of 16 sequences, 32 heads, D 128 (up to 30,720 query
+// rows): 24 us on cold caches, of 137 us for the call.
 #include "kv8_tree.cuh"
 #include "kv8_scores.cuh"
 

@@ -505,7 +505,8 @@ typedef struct csa2_rope {
  *   x = cap tanh(x / cap)                     where cap > 0
  *   x = x - slopes[h] |p - j|                 where slopes are given
  * and the query sees row j when j <= p or j < prefix[b], and, where window > 0,
- * j > p - window or j < sink.
+ * j > p - window or j < sink.  A capped score is within 1e-6 of itself; distances are
+ * exact, and a slope's product and the sum with it round once each in fp32.
  */
 typedef struct csa2_scores {
   float cap;                  /* 0, or 2^-10 .. 2^20 */
