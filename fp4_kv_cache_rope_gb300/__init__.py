@@ -623,10 +623,16 @@ def _kv8_alike(x, of, name, T, kind):
 def _kv8_table(cache, rope):
     if rope.device != cache.device:
         raise Csa2Error(f"rope: on {rope.device}, the cache on {cache.device}")
-    return ctypes.byref(rope.struct)
+    r = rope.struct
+    if r.dim % 16 or r.first % 8 or r.first < 0 or r.first + r.dim > cache.dim:
+        raise Csa2Error(f"rope: {r.dim} channels from {r.first} on; it takes a multiple of 16 from a "
+                        f"multiple of 8 on, within dim {cache.dim}")
+    return ctypes.byref(r)
 
 
 def _kv8_scores(cache, scores, H):
+    if not isinstance(scores, Scores):
+        raise Csa2Error("scores: it takes a Scores")
     if scores.slopes is not None:
         _kv8_arg(cache, scores.slopes, "slopes", "float32", (H,))
     if scores.prefix is not None:
@@ -737,7 +743,7 @@ def kv8_attn_tree(cache, q, k, v, parent, out, ws, lse=None, q_len=None, softmax
         raise Csa2Error(f"a tree has at most {KV8_MAX_TREE} drafted tokens")
     if parent is None:
         raise Csa2Error("csa2_kv8_attn_tree: it takes `parent`")
-    if scores is not None and scores.prefix is not None:
+    if isinstance(scores, Scores) and scores.prefix is not None:
         raise Csa2Error("csa2_kv8_attn_tree: scores without a prefix")
     pa = _kv8_arg(cache, parent, "parent", "int32", (cache.batch, T))
     ls = _kv8_arg(cache, lse, "lse", "float32", (cache.batch, T, H))

@@ -184,6 +184,10 @@ def test_the_binding_names_what_it_refuses():
         ("no rows", lambda: K.kv8_append_path(c, f(0, 4), f(0, 4), i(2, 2), ws)),
         ("slopes", lambda: K.kv8_attn_scored(c, f(3, 8), f(3, 8), ws, K.Scores(slopes=torch.zeros(4)))),
         ("prefix", lambda: K.kv8_attn_scored(c, f(3, 8), f(3, 8), ws, K.Scores(prefix=i(3)))),
+        ("rope: 16 channels from 4", lambda: K.kv8_rope(c, f(3, 8), f(3, 8), K.Rope(torch.zeros(9, 8), torch.zeros(9, 8), first=4), ws)),
+        ("rope: 128 channels", lambda: K.kv8_append_rope(c, f(3, 4), f(3, 4), K.Rope(torch.zeros(9, 64), torch.zeros(9, 64)), ws)),
+        ("a Scores", lambda: K.kv8_attn_scored(c, f(3, 8), f(3, 8), ws, None)),
+        ("a Scores", lambda: K.kv8_attn_tree(c, f(3, 8), f(3, 4), f(3, 4), i(2, 3), f(3, 8), ws, scores=30.0)),
         ("out", lambda: K.kv8_attn_scored(c, f(3, 8), f(3, 4), ws, K.Scores())),
         ("at most 256", lambda: K.kv8_attn_tree(c, f(257, 8), f(257, 4), f(257, 4), i(2, 257), f(257, 8), ws)),
         ("parent", lambda: K.kv8_attn_tree(c, f(3, 8), f(3, 4), f(3, 4), None, f(3, 8), ws)),
