@@ -23,6 +23,7 @@ constexpr int kKv8Ctas = 640;      // upper bound of the split kernels' CTAs
 constexpr int kKv8SplitCtas = 256; // upper bound of the CTAs of a split prefill
 constexpr int kKv8SlotRows = 24;   // query rows of one partial result
 constexpr int kKv8Step = 128;      // cached rows of one step of a CTA
+constexpr int kKv8FewRows = 64;    // query rows per (sequence, K/V head) of the few-row kernels
 
 struct Kv8 {
   uint8_t* codes[2];               // K, V

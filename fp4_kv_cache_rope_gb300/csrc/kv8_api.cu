@@ -155,13 +155,19 @@ Kv8Ws kv8_ws(const csa2_kv8_cache* c) {
 }
 
 // The results of drafted tokens' queries before their own rows: one fp32 row each, or
-// the many-row kernel's parts in their place.
+// the many-row kernel's parts in their place.  Enough for fewer tokens too, whose rows
+// may be split more often.
 size_t kv8_tree_bytes(const csa2_kv8_cache* c, int32_t T, int32_t H) {
-  const size_t rows = (size_t)c->batch * T * H * kv8_row_floats(c->dim) * 4;
-  const int64_t base = (int64_t)c->batch * c->kv_heads * (((int64_t)T * (H / c->kv_heads) + 255) / 256);
-  const int splits = base > 0 ? kv8_tree_splits(base, c->max_len) : 1;
-  const size_t parts = splits > 1 ? (size_t)base * splits * 256 * (c->dim + 2) * 4 : 0;
-  return align256(rows > parts ? rows : parts);
+  const int64_t rows = (int64_t)T * (H / c->kv_heads), units = (int64_t)c->batch * c->kv_heads;
+  size_t most = (size_t)units * rows * kv8_row_floats(c->dim) * 4;
+  for (int64_t tiles = 1; rows > kKv8FewRows && tiles <= (rows + 255) / 256; ++tiles) {
+    const int64_t base = units * tiles;
+    if (base > kKv8TreeCtas) break;
+    const int splits = kv8_tree_splits(base, c->max_len);
+    const size_t parts = splits > 1 ? (size_t)base * splits * 256 * (c->dim + 2) * 4 : 0;
+    if (parts > most) most = parts;
+  }
+  return align256(most);
 }
 
 bool rope_ok(const csa2_rope* r, int32_t D) {
@@ -229,15 +235,15 @@ Kv8Scores scores_of(const csa2_scores& s, const Kv8Attn& a) {
   return k;
 }
 
-// Up to 64 query rows per (sequence, K/V head) go to the kernel that is bound by
+// Up to kKv8FewRows query rows per (sequence, K/V head) go to the kernel that is bound by
 // the cache's bytes, more to the tensor cores' (16 sequences of 9000 rows, 4 heads,
 // D 128: 62 us against 80 us for 48 rows, 78 against 80 for 64, 92 against 82 for 80).
 cudaError_t plain(const Kv8Attn& a, cudaStream_t s) {
-  return a.T * a.G <= 64 ? launch_kv8_attn(a, sms(), s) : launch_kv8_prefill(a, sms(), s);
+  return a.T * a.G <= kKv8FewRows ? launch_kv8_attn(a, sms(), s) : launch_kv8_prefill(a, sms(), s);
 }
 // The same with changed scores.
 cudaError_t scored(const Kv8Attn& a, const Kv8Scores& sc, Kv8Left* left, cudaStream_t s) {
-  return a.T * a.G <= 64 ? launch_kv8_scored_few(a, sc, sms(), left, s)
+  return a.T * a.G <= kKv8FewRows ? launch_kv8_scored_few(a, sc, sms(), left, s)
                          : launch_kv8_scored_many(a, sc, sms(), left, s);
 }
 
@@ -326,10 +332,10 @@ csa2_status csa2_kv8_evict(const csa2_kv8_cache* cache, const csa2_kv8_cache* ds
                                reinterpret_cast<uint32_t*>(w), sms(), (cudaStream_t)stream));
 }
 
-csa2_status csa2_kv8_rope(const csa2_kv8_cache *cache, const csa2_rope *rope, const csa2_rows *q,
-                          int32_t H, const csa2_rows *q_out, const csa2_rows *k,
-                          const csa2_rows *k_out, int32_t T, const int32_t *q_len,
-                          const int32_t *pos, const int32_t *parent, void *ws, void *stream) {
+csa2_status csa2_kv8_rope(const csa2_kv8_cache* cache, const csa2_rope* rope, const csa2_rows* q,
+                          int32_t H, const csa2_rows* q_out, const csa2_rows* k,
+                          const csa2_rows* k_out, int32_t T, const int32_t* q_len,
+                          const int32_t* pos, const int32_t* parent, void* ws, void* stream) {
   if (!kv8_ok(cache) || !rope_ok(rope, cache->dim) || !ws || !aligned(ws, 256) || !heads_ok(cache, T, H))
     return CSA2_ERR_INVALID;
   if (!aligned(q_len, 4) || !aligned(pos, 4) || !aligned(parent, 4) || (pos && parent) ||
@@ -435,7 +441,7 @@ csa2_status csa2_kv8_attn_tree(const csa2_kv8_cache* cache, const csa2_rows* q, 
   Kv8Scores sc = scores_of(*scores, a);
   sc.parent = parent;
   sc.rows_out = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kv8_ws(cache).total);
-  if (a.T * a.G > 64) a.part = sc.rows_out;   // the one or the other
+  if (a.T * a.G > kKv8FewRows) a.part = sc.rows_out;   // the one or the other
   Kv8Left left{};
   const cudaError_t e = scored(a, sc, &left, (cudaStream_t)stream);
   return done(e != cudaSuccess ? e

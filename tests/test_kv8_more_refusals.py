@@ -144,6 +144,26 @@ def test_trees():
     assert size(ref(c), 3, 8) == (plain + 2 * 3 * 8 * 132 * 4 + 255) // 256 * 256
 
 
+@pytest.mark.parametrize("batch,heads,max_len", [(1, 1, 1 << 20), (2, 8, 131072), (16, 4, 9024), (40, 8, 4096),
+                                                 (152, 2, 65536), (3, 5, 50048)])
+def test_a_tree_workspace_serves_fewer_tokens(batch, heads, max_len):
+    """What a call of T tokens takes is enough for every call of fewer."""
+    c = contiguous(1 << 30, SEQ)
+    c.batch, c.kv_heads, c.max_len = batch, heads, max_len
+    for G in (1, 3, 8, 40):
+        sizes = [K._kv8_tree_workspace_size(ref(c), T, heads * G) for T in range(257)]
+        assert sizes[0] > 0 and sizes == sorted(sizes), G
+        # and it holds the rows, and the parts of the split that T itself gets
+        plain = K._kv8_workspace_size(ref(c), 1, heads * G)
+        for T in (1, 16, 64, 256):
+            parts = 0
+            if T * G > 64:
+                base = batch * heads * -(-T * G // 256)
+                splits = max(1, min(304 // base, -(-max_len // 1024)))
+                parts = base * splits * 256 * 130 * 4 if splits > 1 else 0
+            assert sizes[T] >= plain + max(batch * T * heads * G * 132 * 4, parts)
+
+
 # ------------------------------------------------------------------- the binding
 def test_handles():
     cos = torch.zeros(10, 8)
