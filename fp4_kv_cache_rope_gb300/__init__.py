@@ -612,9 +612,15 @@ def kv8_evict(cache, keep, sink, recent, kept, ws, dst=None, stream=None):
              _kv8_ws(cache, ws))
 
 
-def _kv8_alike(x, of, name, T, kind):
-    """(struct) of rows that have the T and the type of others."""
-    r, Tx = x
+def _kv8_alike(cache, x, name, heads, first, of, T, kind, wide=False):
+    """(struct) of rows of x, which has the T and the type of `first`, the operand called `of`."""
+    if x.dtype is first.dtype and x.shape == (cache.batch, T, heads, cache.dim) \
+            and x.device == cache.device and T:
+        sb, st, sh, sd = x.stride()
+        at = x.data_ptr()
+        if sd == 1 and not (at & 15 or (sb | st | sh) & (3 if kind == F32 else 7)):
+            return Csa2Rows(at, sb, st, sh, kind)
+    r, Tx = _kv8_rows(cache, x, name, heads, wide)
     if Tx != T or r.type != kind:
         raise Csa2Error(f"{name}: T and type of {of}")
     return r
@@ -649,15 +655,13 @@ def kv8_rope(cache, q, q_out, rope, ws, k=None, k_out=None, q_len=None, pos=None
     seq_len[b] + i."""
     rq, T = _kv8_rows(cache, q, "q", None, True)
     H = q.shape[2]
-    ro = _kv8_alike(_kv8_rows(cache, q_out, "q_out", H, True), "q", "q_out", T, rq.type)
+    ro = _kv8_alike(cache, q_out, "q_out", H, q, "q", T, rq.type, True)
     if (k is None) != (k_out is None):
         raise Csa2Error("k and k_out go together")
     rk = rko = None
     if k is not None:
-        rk = ctypes.byref(_kv8_alike(_kv8_rows(cache, k, "k", cache.kv_heads, True), "q", "k", T,
-                                     rq.type))
-        rko = ctypes.byref(_kv8_alike(_kv8_rows(cache, k_out, "k_out", cache.kv_heads, True), "q",
-                                      "k_out", T, rq.type))
+        rk = ctypes.byref(_kv8_alike(cache, k, "k", cache.kv_heads, q, "q", T, rq.type, True))
+        rko = ctypes.byref(_kv8_alike(cache, k_out, "k_out", cache.kv_heads, q, "q", T, rq.type, True))
     if pos is not None and parent is not None:
         raise Csa2Error("pos or parent, not both")
     if parent is not None and T > KV8_MAX_TREE:
@@ -676,7 +680,7 @@ def kv8_append_rope(cache, k, v, rope, ws, q=None, q_out=None, new_len=None, sta
     start[b] + i), and v; with q [batch, T, heads, dim] (bf16, f16 or fp32) the step's
     queries are rotated at the same positions into q_out, which may be q."""
     rk, T = _kv8_rows(cache, k, "k", cache.kv_heads, True)
-    rv = _kv8_alike(_kv8_rows(cache, v, "v", cache.kv_heads, True), "k", "v", T, rk.type)
+    rv = _kv8_alike(cache, v, "v", cache.kv_heads, k, "k", T, rk.type, True)
     if (q is None) != (q_out is None):
         raise Csa2Error("q and q_out go together")
     rq = ro = None
@@ -687,7 +691,7 @@ def kv8_append_rope(cache, k, v, rope, ws, q=None, q_out=None, new_len=None, sta
         if Tq != T:
             raise Csa2Error("q: the T of k and v")
         rq = ctypes.byref(x)
-        ro = ctypes.byref(_kv8_alike(_kv8_rows(cache, q_out, "q_out", H, True), "q", "q_out", T, x.type))
+        ro = ctypes.byref(_kv8_alike(cache, q_out, "q_out", H, q, "q", T, x.type, True))
     nl = _kv8_arg(cache, new_len, "new_len", "int32", (cache.batch,))
     sp = _kv8_arg(cache, start, "start", "int32", (cache.batch,))
     ps = _kv8_arg(cache, pos, "pos", "int32", (cache.batch, T))
@@ -701,7 +705,7 @@ def kv8_append_path(cache, k, v, path, ws, new_len=None, start=None, stream=None
     sequence is row path[b, i] (int32 [batch, M]); new_len[b] of them (default M).  The drafted
     tokens on an accepted path, with the keys that kv8_attn_tree took."""
     rk, T = _kv8_rows(cache, k, "k", cache.kv_heads, True)
-    rv = _kv8_alike(_kv8_rows(cache, v, "v", cache.kv_heads, True), "k", "v", T, rk.type)
+    rv = _kv8_alike(cache, v, "v", cache.kv_heads, k, "k", T, rk.type, True)
     if len(path.shape) != 2:
         raise Csa2Error("path: it takes [batch, M]")
     M = path.shape[1]
@@ -719,7 +723,7 @@ def kv8_attn_scored(cache, q, out, ws, scores, lse=None, q_len=None, softmax_sca
     i of a sequence is at position seq_len[b] - q_len[b] + i.  kv8_mass does not take its lse."""
     rq, T = _kv8_rows(cache, q, "q")
     H = q.shape[2]
-    ro = _kv8_alike(_kv8_rows(cache, out, "out", H), "q", "out", T, rq.type)
+    ro = _kv8_alike(cache, out, "out", H, q, "q", T, rq.type)
     ls = _kv8_arg(cache, lse, "lse", "float32", (cache.batch, T, H))
     ql = _kv8_arg(cache, q_len, "q_len", "int32", (cache.batch,))
     _kv8_run(cache, "csa2_kv8_attn_scored", _kv8_attn_scored, stream, ctypes.byref(cache.struct),
@@ -736,9 +740,9 @@ def kv8_attn_tree(cache, q, k, v, parent, out, ws, lse=None, q_len=None, softmax
     `parent` does); out, lse as kv8_attn; scores without a prefix; ws: cache.tree_workspace."""
     rq, T = _kv8_rows(cache, q, "q")
     H = q.shape[2]
-    rk = _kv8_alike(_kv8_rows(cache, k, "k", cache.kv_heads), "q", "k", T, rq.type)
-    rv = _kv8_alike(_kv8_rows(cache, v, "v", cache.kv_heads), "q", "v", T, rq.type)
-    ro = _kv8_alike(_kv8_rows(cache, out, "out", H), "q", "out", T, rq.type)
+    rk = _kv8_alike(cache, k, "k", cache.kv_heads, q, "q", T, rq.type)
+    rv = _kv8_alike(cache, v, "v", cache.kv_heads, q, "q", T, rq.type)
+    ro = _kv8_alike(cache, out, "out", H, q, "q", T, rq.type)
     if T > KV8_MAX_TREE:
         raise Csa2Error(f"a tree has at most {KV8_MAX_TREE} drafted tokens")
     if parent is None:
