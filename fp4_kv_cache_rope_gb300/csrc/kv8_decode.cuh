@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(32 * WARPS, decode_ctas(D, NT, WARPS))
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) kv8_cap2(s[u][i][e], s[u][i][2 + e], p.sc.cap2);
+              for (int e = 0; e < 4; ++e) s[u][i][e] = kv8_cap(s[u][i][e], p.sc.cap2);
         }
         if (p.sc.slopes) {
 #pragma unroll

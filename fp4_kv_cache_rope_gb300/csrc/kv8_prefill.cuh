@@ -320,9 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
         for (int j = 0; j < 16; j += 2) {
           float x, y;
           unpack2(mul2(pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), f), x, y);
-          kv8_cap2(x, y, p.sc.cap2);
-          s[j] = __float_as_uint(x);
-          s[j + 1] = __float_as_uint(y);
+          s[j] = __float_as_uint(kv8_cap(x, p.sc.cap2));
+          s[j + 1] = __float_as_uint(kv8_cap(y, p.sc.cap2));
         }
       };
       // f(columns 16 u .., u) for u = 0 .. 7, the next ones on their way meanwhile
@@ -412,11 +411,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
       // what the logits in tensor memory lack to base 2
       const float by = KIND == kSloped || KIND == kBoth ? 1.0f : mul;
       float top = fmaxf(tops[0], tops[1]) * by;
-      if constexpr (KIND == kCapped) {                     // (the cap keeps their order)
-        float same = top;
-        const bool none = top == -INFINITY;
-        kv8_cap2(top, same, p.sc.cap2);
-        if (none) top = -INFINITY;
+      if constexpr (KIND == kCapped) {
+        // (the cap keeps their order; a row that sees nothing starts from the least score
+        // that there is)
+        top = kv8_cap(top, p.sc.cap2);
       }
       // (a row without a visible key so far waits for one; no row's result
       // depends on another's)

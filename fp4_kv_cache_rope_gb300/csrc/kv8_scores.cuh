@@ -114,8 +114,7 @@ __device__ __forceinline__ float kv8_rcp(float x) {
 // tanh(y) / y as a quotient of two polynomials in u = y^2 of degree 4, fitted to
 // |y| <= 9.02 for the smallest relative error (2.1e-8; 4e-7 with fp32's roundings,
 // 6e-8 on average).  Beyond, tanh is 1 in fp32.  The quotient of the odd function
-// keeps small scores' relative precision, which 1 - 2 / (1 + e^2y) would not, and
-// takes one reciprocal for two of them in place of an exponential and a reciprocal each.
+// keeps small scores' relative precision, which 1 - 2 / (1 + e^2y) would not.
 constexpr float kTanhEnd = 9.02f;
 __device__ __forceinline__ void kv8_tanh_parts(float y, float& p, float& q) {
   const float u = y * y;
@@ -124,23 +123,19 @@ __device__ __forceinline__ void kv8_tanh_parts(float y, float& p, float& q) {
   q = fmaf(fmaf(fmaf(fmaf(7.761994424981822e-7f, u, 3.2830884447321296e-4f), u,
                      2.587106265127659e-2f), u, 0.46713030338287354f), u, 1.0f);
 }
-// x, y: scores of one query over the cap -> cap2 tanh of them.  A NaN stays one, and
-// makes the other one, too.
-__device__ __forceinline__ void kv8_cap2(float& x, float& y, float cap2) {
-  x = max_nan(min_nan(x, kTanhEnd), -kTanhEnd);
-  y = max_nan(min_nan(y, kTanhEnd), -kTanhEnd);
-  float px, qx, py, qy;
-  kv8_tanh_parts(x, px, qx);
-  kv8_tanh_parts(y, py, qy);
-  const float r = kv8_rcp(qx * qy) * cap2;
-  x = px * (qy * r);
-  y = py * (qx * r);
+// A score over the cap -> cap2 tanh of it.  A NaN stays one, and an infinity is the cap.
+// (A reciprocal of its own: one shared by two keys would let a hidden key's NaN, an
+// infinite query times a row that is not there, spoil a visible one.)
+__device__ __forceinline__ float kv8_cap(float x, float cap2) {
+  float p, q;
+  kv8_tanh_parts(max_nan(min_nan(x, kTanhEnd), -kTanhEnd), p, q);
+  return p * (kv8_rcp(q) * cap2);
 }
-
 // The same for |score / cap| <= kTanhNear from polynomials of degree 2 (8.4e-8; 3e-7 with
 // fp32's roundings), for logits s that `mul` takes to scores over the cap: the
 // polynomials take s itself, their coefficients the factor.  Four logits of a query at a
-// time, packed, two to a reciprocal.  (Beyond kNearMul a coefficient could be infinite;
+// time, packed, two to a reciprocal: a row's logits are all finite here, or all not.
+// (Beyond kNearMul a coefficient could be infinite;
 // one that is lost to 0 belongs to a term that is, too.)
 constexpr float kTanhNear = 2.0f, kNearMul = 1e6f;
 struct NearCap {

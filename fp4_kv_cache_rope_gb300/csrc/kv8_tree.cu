@@ -215,10 +215,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_tree_join_kernel(JoinParams 
     dot += __shfl_xor_sync(0xffffffffu, dot, 2);
     dot += __shfl_xor_sync(0xffffffffu, dot, 4);
     float x = dot * p.sc.factor;
-    if (p.sc.cap2 > 0.0f) {
-      float y = x;
-      kv8_cap2(x, y, p.sc.cap2);
-    }
+    if (p.sc.cap2 > 0.0f) x = kv8_cap(x, p.sc.cap2);
     x = fmaf(-slope, (float)i, x);
     const bool ok = i <= depth && (!p.sc.window || i < p.sc.window || n + depth - i < p.sc.sink);
     if (ok && x != -INFINITY) all.join(x, 1.0f, v.v);

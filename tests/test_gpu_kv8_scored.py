@@ -318,3 +318,41 @@ def test_scores_that_grow_along_the_rows(T, G, what):
             run_tree(p, G, T, "bf16", size=2.0, chain=0.8)
         else:
             run_scored(p, G, T, "bf16", size=2.0, **args)
+
+
+@pytest.mark.parametrize("T,G", [(1, 4), (40, 4)])
+@pytest.mark.parametrize("value,scale", [(math.inf, 0.0), (-math.inf, 0.0), (3e38, 2.0 ** 20), (-3e38, 2.0 ** 20)])
+def test_a_cap_makes_infinite_scores_finite(T, G, value, scale):
+    """Scores that are infinite, or beyond fp32, are the cap or its negative: alike for every
+    row, whose plain mean comes out."""
+    p = Pair(2, 1, 64, 300, 16, 16, O.E4M3, seed=71, mass=False)
+    k, v = p.rows(300, 1, "f32"), p.rows(300, 1, "f32")
+    k[..., 0] = 2.0
+    lens = [300, 171]
+    p.append(k, v, p.c.workspace(1, 1), lens=lens)
+    q = torch.zeros(2, T, G, 64, dtype=torch.bfloat16)
+    q[..., 0] = value
+    for drafted in (False, True):
+        ws = p.c.tree_workspace(T, G)
+        out, lse = torch.empty(q.shape, dtype=q.dtype, device="cuda"), torch.empty(2, T, G, device="cuda")
+        sc = K.Scores(cap=30.0)
+        if drafted:
+            kd = torch.full((2, T, 1, 64), 2.0, dtype=torch.bfloat16, device="cuda")
+            vd = torch.full_like(kd, 0.5)
+            K.kv8_attn_tree(p.c, q.cuda(), kd, vd, ints([[-1] * T] * 2), out, ws, lse=lse, softmax_scale=scale,
+                            scores=sc)
+        else:
+            K.kv8_attn_scored(p.c, q.cuda(), out, ws, sc, lse=lse, softmax_scale=scale)
+        for b in range(2):
+            vv = p.seq[b, 0, "v"].values()
+            for t in range(T):
+                n = lens[b] if drafted else lens[b] - T + t + 1
+                rows = np.concatenate([vv, np.full((1, 64), 0.5)]) if drafted else vv[:n]
+                mean, size = rows.mean(0), np.abs(rows).mean(0)
+                # the rounding of the output, of the weights (all one power of two but for the
+                # cap's own rounding) and of the sums
+                tol = 2.0 ** -8 * np.abs(mean) + size * (2.0 ** -10 + len(rows) * 2.0 ** -22)
+                got = out[b, t].double().cpu().numpy()
+                assert (np.abs(got - mean) <= tol).all(), (drafted, b, t)
+                want = math.copysign(30.0, value) + math.log(len(rows))
+                assert np.abs(lse[b, t].double().cpu().numpy() - want).max() < 30 * 2.0 ** -20 + 1e-5
