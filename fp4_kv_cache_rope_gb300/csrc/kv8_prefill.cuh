@@ -27,8 +27,8 @@
 // 2^-25 of that largest scale, i.e. by 2^-31 of the range's largest value.
 // The running maximum is raised only when a base-2 logit exceeds it by 8 (the rare
 // rescaling of O stays off the common path), and P is taken times 2^7: at most
-// 2^15, with f16's full precision down to 2^-21.  l is summed in fp32 from the
-// unrounded weights.
+// 2^15 (2^16 is f16's infinity), with f16's full precision down to 2^-21.  l is summed in
+// fp32 from the unrounded weights.
 //
 // Warps (640 threads): 0-3 and 4-7 softmax of query tile 0 and 1; 8-11 turn K's
 // codes into f16 tiles and 12-15 V's, from registers loaded one tile ahead (no
@@ -418,7 +418,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
       }
       // (a row without a visible key so far waits for one; no row's result
       // depends on another's)
-      const bool raise = top > m + 8.0f;
+      // A capped score and its row's largest are each off by up to 4e-7 of the cap: one power
+      // of two between them for a cap of 2^20.  So with large caps less of P's range is left
+      // to the maximum's lag.
+      const bool raise = top > m + (KIND == kCapped && p.sc.cap2 > 65536.0f ? 4.0f : 8.0f);
       if (__any_sync(0xffffffffu, raise)) {
         const float up = raise ? top : m;
         const float alpha = m == -INFINITY ? 0.0f : kv8_exp2(m - up);

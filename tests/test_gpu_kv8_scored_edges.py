@@ -1,0 +1,72 @@
+"""The attention with changed scores where its arithmetic is nearest to its limits."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+import fp4_kv_cache_rope_gb300 as K  # noqa: E402
+from oracle import kv8 as O  # noqa: E402
+from kv8_tools import Pair  # noqa: E402
+from kv8_more_tools import check_attention, ints, scored_want  # noqa: E402
+from test_gpu_kv8_scored import filled, run_scored  # noqa: E402
+
+
+def scored(p, q, k=None, v=None, scale=0.0, **args):
+    """(out, lse) on the host; with k and v of drafted tokens, each of which follows the one before."""
+    B, T, H, _ = q.shape
+    ws = p.c.tree_workspace(T, H)
+    out, lse = torch.empty(q.shape, dtype=q.dtype, device="cuda"), torch.empty(B, T, H, device="cuda")
+    if k is None:
+        K.kv8_attn_scored(p.c, q.cuda(), out, ws, K.Scores(**args), lse=lse, softmax_scale=scale)
+    else:
+        K.kv8_attn_tree(p.c, q.cuda(), k.cuda(), v.cuda(), ints([[t - 1 for t in range(T)]] * B), out, ws, lse=lse,
+                        softmax_scale=scale, scores=K.Scores(**args))
+    assert K.get_status(ws) == 0
+    return out.cpu(), lse.cpu()
+
+
+def digits(n):
+    """n in base 128 with digits from -64 to 63, the last one what is left."""
+    d = []
+    for _ in range(3):
+        low = (n + 64) % 128 - 64
+        d.append(low)
+        n = (n - low) // 128
+    return d + [n]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("drafted", [False, True])
+@pytest.mark.parametrize("T,G", [(1, 4), (40, 4)])
+def test_the_largest_cap(D, drafted, T, G):
+    """Scores over the cap in steps of 2^-18, held exactly: tile after tile of the first, whose
+    capped score the second's exceeds by 8 (base 2, the most that the many-row kernel leaves its
+    maximum behind), among them the third, a smaller score that comes out above the second by
+    1 for the quotient's roundings."""
+    first, second, third = 1666109, 2226092, 2218733
+    n, cap = 300, 2.0 ** 20
+    p = Pair(1, 1, D, n, 16, 16, O.INT8, seed=81, mass=False)
+    k = torch.zeros(1, n, 1, D)
+    for j in range(n):
+        k[0, j, 0, :4] = torch.tensor(digits(first if j < 128 else second if j % 2 else third), dtype=torch.float32)
+    k[..., 4] = 64.0                     # the blocks' scales are 1 then
+    p.append(k, p.rows(n, 1, "f32"), p.c.workspace(1, 1))
+    q = torch.zeros(1, T, G, D)
+    q[..., :4] = 128.0 ** torch.arange(4.0)
+    q = q.bfloat16()
+    kd, vd = (torch.zeros(1, T, 1, D, dtype=torch.bfloat16), p.rows(T, 1, "bf16")) if drafted else (None, None)
+    out, lse = scored(p, q, kd, vd, scale=cap * 2.0 ** -18, cap=cap)
+    more = {} if kd is None else dict(k=kd[0, :, 0].double().numpy(), v=vd[0, :, 0].double().numpy(),
+                                      parent=[t - 1 for t in range(T)])
+    check_attention(out[0], lse[0], scored_want(p, q, 0, 0, G, T, cap * 2.0 ** -18, "bf16", cap, **more))
+
+
+@pytest.mark.parametrize("T,G", [(1, 8), (40, 4)])
+@pytest.mark.parametrize("size", [0.1, 0.4, 1.0])
+def test_scores_about_and_beyond_the_largest_cap(T, G, size):
+    p = filled(2, 2, 128, [700, 130], 64, 64, O.E4M3, seed=82)
+    run_scored(p, G, T, "bf16", cap=2.0 ** 20, scale=2.0 ** 20, size=size)
