@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
     const bool real = r < rows;
     // (a row without a query is never written: it may see everything)
     int lim = real ? min(n, n - ql + tok + 1) : 0x7FFFFFFF;
-    int low = -0x7FFFFFFF;                                 // SCORED: from here on, or below the sink
+    int low = -kNoQuery;                                   // SCORED: from here on, or below the sink
     float at = 0.0f, slope = 0.0f;                         // the query's position; base 2
     if (SCORED && real) {
       const int pos = kv8_query_at(p.a, p.sc, b, n, ql, tok);
@@ -268,18 +268,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
         front = __any_sync(0xffffffffu, low > key0);
       const bool masked = groups != 0xFFu || front || __any_sync(0xffffffffu, lim < key0 + kTileKeys);
       const int seen = masked ? (int)__reduce_min_sync(0xffffffffu, max(lim - key0, 0)) : 0;
-      auto hide = [&](uint32_t (&s)[16], int u) {          // columns 16 u ..
+      // The columns 16 u .. that the row does not see, a bit each: kCapped hides them as 0,
+      // which neither its size nor a score beside them tells, and then as -inf.  (By
+      // comparisons twice, as below, a chunk of 4096 tokens took 2727 us, 2685 this way.)
+      auto hidden = [&](int u) -> uint32_t {
+        if (!((groups >> u) & 1u)) return 0xFFFFu;
+        if (seen >= 16 * u + 16 && !front) return 0u;      // every row sees them
+        const int x = key0 + 16 * u;
+        uint32_t bits = 0xFFFFu << min(max(lim - x, 0), 16);
+        if (front)
+          bits |= ((1u << min(max(low - x, 0), 16)) - 1u) & (0xFFFFu << min(max(p.sc.sink - x, 0), 16));
+        return bits;
+      };
+      auto put = [&](uint32_t (&s)[16], uint32_t bits, uint32_t with) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (bits >> j & 1u) s[j] = with;
+      };
+      constexpr uint32_t kMinusInf = 0xFF800000u;
+      auto hide = [&](uint32_t (&s)[16], int u) {
         const bool gone = !((groups >> u) & 1u);
         if (!gone && seen >= 16 * u + 16 && !front) return;   // every row sees them
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          if (gone || key0 + 16 * u + j >= lim) s[j] = 0xFF800000u;
+          if (gone || key0 + 16 * u + j >= lim) s[j] = kMinusInf;
         if constexpr (SCORED) {
           if (!front) return;
           const int to = low - (key0 + 16 * u), from = p.sc.sink - (key0 + 16 * u);
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            if (j < to && j >= from) s[j] = 0xFF800000u;
+            if (j < to && j >= from) s[j] = kMinusInf;
         }
       };
       // kSloped: logits in base 2, plus `add`; a row's bias is linear in the column
@@ -313,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
       };
       using Yes = std::integral_constant<bool, true>;
       using No = std::integral_constant<bool, false>;
-      // kCapped, kBoth: capped logits in base 2
+      // kBoth: capped logits in base 2
       auto capped = [&](uint32_t (&s)[16]) {
         const uint64_t f = pack2(mul, mul);
 #pragma unroll
@@ -350,8 +368,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
       auto pass = [&](auto change, auto use) {
         if (masked)
           each([&](uint32_t (&s)[16], int u) {
-            change(s, u);
-            hide(s, u);
+            if constexpr (KIND == kCapped) {
+              // (scores that share a reciprocal with hidden ones)
+              const uint32_t bits = hidden(u);
+              put(s, bits, 0u);
+              change(s, u);
+              put(s, bits, kMinusInf);
+            } else {
+              change(s, u);
+              hide(s, u);
+            }
             use(s, u);
           });
         else
@@ -370,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
                                    : max3(tops[(j >> 1) & 1], __uint_as_float(s[j]),
                                           __uint_as_float(s[j + 1]));
       };
-      float size = 0.0f;                                   // kCapped: the largest |logit|
+      float size = 0.0f;                                   // kCapped: the largest |logit| seen
       if constexpr (KIND == kBoth) {
         // (taken once, and kept in tensor memory)
         pass(
@@ -392,13 +418,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
           pass([&](uint32_t (&s)[16], int u) { sloped(s, u, 0.0f, No{}); }, largest);
       } else {
         if constexpr (KIND == kCapped) {
-          pass(
-              [&](uint32_t (&s)[16], int) {
+          auto measure = [&](const uint32_t (&s)[16]) {
 #pragma unroll
-                for (int j = 0; j < 16; j += 2)
-                  size = max3_abs(size, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
-              },
-              largest);
+            for (int j = 0; j < 16; j += 2)
+              size = max3_abs(size, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+          };
+          if (masked)
+            each([&](uint32_t (&s)[16], int u) {
+              const uint32_t bits = hidden(u);
+              put(s, bits, 0u);
+              measure(s);
+              put(s, bits, kMinusInf);
+              largest(s, u);
+            });
+          else
+            each([&](uint32_t (&s)[16], int u) {
+              measure(s);
+              largest(s, u);
+            });
         } else if (masked) {
           each([&](uint32_t (&s)[16], int u) {
             hide(s, u);
@@ -416,8 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
         // that there is)
         top = kv8_cap(top, p.sc.cap2);
       }
-      // (a row without a visible key so far waits for one; no row's result
-      // depends on another's)
+      // (a row without a visible key so far waits for one; rows share nothing but, by
+      // warp, which form of the arithmetic below takes their weights)
       // A capped score and its row's largest are each off by up to 4e-7 of the cap: one power
       // of two between them for a cap of 2^20.  So with large caps less of P's range is left
       // to the maximum's lag.
@@ -486,34 +523,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
           weights(s, u);
         }
       } else if constexpr (KIND == kCapped) {
-        if (__any_sync(0xffffffffu, !(size * mul <= kTanhNear && mul <= kNearMul))) {
-          pass(
-              [&](uint32_t (&s)[16], int) {
-                capped(s);
+        // By warp, so another row's scores may change a row's last bits; keys that none of
+        // the warp's rows sees do not.  (Both quotients where a warp's rows differ, each row by
+        // its own scores: 4096 tokens of 64 heads at the end of 16384 rows, D 128, scores around
+        // twice the cap 4844 -> 6374 us, of the cap 3729 -> 9570 us.)
+        const NearCap near(mul, p.sc.cap2);
+        auto near4 = [&](uint32_t (&s)[16], int j, float (&x)[4]) {
+          uint64_t a = pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+          uint64_t c = pack2(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
+          near(a, c, u2);
+          unpack2(a, x[0], x[1]);
+          unpack2(c, x[2], x[3]);
+        };
+        auto far4 = [&](uint32_t (&s)[16], int j, float (&x)[4]) {
+          const uint64_t f = pack2(mul, mul);
+          unpack2(mul2(pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), f), x[0], x[1]);
+          unpack2(mul2(pack2(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3])), f), x[2], x[3]);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) + less);
-              },
-              weights);
-        } else {
-          const NearCap near(mul, p.sc.cap2);
+          for (int k = 0; k < 4; ++k) x[k] = kv8_cap(x[k], p.sc.cap2, less);
+        };
+        auto by4 = [&](auto cap4) {
           pass(
               [&](uint32_t (&s)[16], int) {
 #pragma unroll
                 for (int j = 0; j < 16; j += 4) {
-                  uint64_t a = pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1]));
-                  uint64_t c = pack2(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
-                  near(a, c, u2);
-                  float x, y;
-                  unpack2(a, x, y);
-                  s[j] = __float_as_uint(x);
-                  s[j + 1] = __float_as_uint(y);
-                  unpack2(c, x, y);
-                  s[j + 2] = __float_as_uint(x);
-                  s[j + 3] = __float_as_uint(y);
+                  float x[4];
+                  cap4(s, j, x);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) s[j + k] = __float_as_uint(x[k]);
                 }
               },
               weights);
-        }
+        };
+        if (__all_sync(0xffffffffu, size * mul <= kTanhNear && mul <= kNearMul))
+          by4(near4);
+        else
+          by4(far4);
       } else if constexpr (KIND == kSloped) {
         if (mirrored)
           pass([&](uint32_t (&s)[16], int u) { sloped(s, u, less, Yes{}); }, weights);

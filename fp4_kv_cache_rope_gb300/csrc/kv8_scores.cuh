@@ -131,6 +131,12 @@ __device__ __forceinline__ float kv8_cap(float x, float cap2) {
   kv8_tanh_parts(max_nan(min_nan(x, kTanhEnd), -kTanhEnd), p, q);
   return p * (kv8_rcp(q) * cap2);
 }
+// Plus `add`, rounded once with the last product.
+__device__ __forceinline__ float kv8_cap(float x, float cap2, float add) {
+  float p, q;
+  kv8_tanh_parts(max_nan(min_nan(x, kTanhEnd), -kTanhEnd), p, q);
+  return fmaf(p, kv8_rcp(q) * cap2, add);
+}
 // The same for |score / cap| <= kTanhNear from polynomials of degree 2 (8.4e-8; 3e-7 with
 // fp32's roundings), for logits s that `mul` takes to scores over the cap: the
 // polynomials take s itself, their coefficients the factor.  Four logits of a query at a

@@ -506,7 +506,9 @@ typedef struct csa2_rope {
  *   x = x - slopes[h] |p - j|                 where slopes are given
  * and the query sees row j when j <= p or j < prefix[b], and, where window > 0,
  * j > p - window or j < sink.  A capped score is within 1e-6 of itself; distances are
- * exact, and a slope's product and the sum with it round once each in fp32.
+ * exact, and a slope's product and the sum with it round once each in fp32.  With more
+ * than 64 query rows per K/V head the last bits of a row's capped scores may depend on how
+ * large its neighbours' (32 rows) are; keys that none of these sees change none of them.
  */
 typedef struct csa2_scores {
   float cap;                  /* 0, or 2^-10 .. 2^20 */

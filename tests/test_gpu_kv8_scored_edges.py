@@ -70,3 +70,27 @@ def test_the_largest_cap(D, drafted, T, G):
 def test_scores_about_and_beyond_the_largest_cap(T, G, size):
     p = filled(2, 2, 128, [700, 130], 64, 64, O.E4M3, seed=82)
     run_scored(p, G, T, "bf16", cap=2.0 ** 20, scale=2.0 ** 20, size=size)
+
+
+@pytest.mark.parametrize("cap", [30.0, 300.0, 3000.0])
+@pytest.mark.parametrize("what", ["key", "query", "front key"])
+def test_far_larger_scores_that_are_not_seen_change_no_bits(cap, what):
+    """A key becomes 30 times as large, which comes later than some tokens or lies in front
+    of all windows, or the last token's query does.  The tokens that share none of the last
+    one's 32 query rows keep their bits."""
+    T, G, n = 48, 4, 97
+    res = []
+    for big in (1.0, 30.0):
+        p = Pair(1, 1, 128, n, 16, 16, O.E4M3, seed=83, mass=False)
+        k, v, q = p.rows(n, 1, "f32"), p.rows(n, 1, "f32"), p.rows(T, G, "f16", 0.02 * cap)
+        if what == "key":
+            k[0, n - 1] *= big           # alone in its block
+        elif what == "query":
+            q[0, T - 1] *= big
+        else:
+            k[0, :16] *= big
+        p.append(k, v, p.c.workspace(1, 1))
+        res.append(scored(p, q, cap=cap, window=30 if what == "front key" else 0))
+    last = T if what == "front key" else T - 32 // G
+    for a, b in zip(*res):
+        assert torch.equal(a[0, :last], b[0, :last])
