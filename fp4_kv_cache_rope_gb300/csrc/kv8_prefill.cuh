@@ -486,6 +486,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
       // same for the whole row and cancels in P / l.  Where m is so large that
       // it would carry P out of range (ulp(2^16) = 2^-7), the logits are rounded
       // like m, which makes the largest difference 0 again.
+      // kSloped rounds the bias with what is added to it, so the same goes for biases
+      // beyond 2^20 (ulp 2^-3), which only logits as large make up for.
       const float mm = m == -INFINITY ? 0.0f : m;
       const float less = 7.0f - mm;
       const uint64_t f2 = pack2(by, by), u2 = pack2(less, less);
@@ -508,7 +510,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(PreParams p) {
           s[j + 1] = __float_as_uint(y);
         }
       };
-      if (KIND != kCapped && __any_sync(0xffffffffu, fabsf(mm) > 65536.0f)) {
+      bool large = fabsf(mm) > 65536.0f;
+      if (KIND == kSloped)
+        large |= fabsf(slope) * fmaxf(fabsf((float)key0 - at), fabsf((float)(key0 + kTileKeys) - at)) > 0x1p20f;
+      if (KIND != kCapped && __any_sync(0xffffffffu, large)) {
 #pragma unroll 1
         for (int u = 0; u < 8; ++u) {
           uint32_t s[16];

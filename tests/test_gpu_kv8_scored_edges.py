@@ -94,3 +94,42 @@ def test_far_larger_scores_that_are_not_seen_change_no_bits(cap, what):
     last = T if what == "front key" else T - 32 // G
     for a, b in zip(*res):
         assert torch.equal(a[0, :last], b[0, :last])
+
+
+@pytest.mark.parametrize("T,G", [(1, 4), (40, 4)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("slope", [2.0 ** 24, 2.0 ** 20, 2.0 ** 14, 1.0])
+def test_slopes_that_cancel_huge_logits(T, G, D, slope):
+    """One row's score is q.k = slope * (p - j) less the slope's bias: 0, but for the roundings
+    of numbers up to 2^31, which are far above 1, and every other row's lies far below.
+    Whatever is left of that score, the row's V comes out."""
+    n, at = 160, 77
+    p = Pair(1, 1, D, n, 16, 16, O.INT8, seed=84, mass=False)
+    k = torch.zeros(1, n, 1, D)
+    k[..., 0] = (torch.arange(n) - 64.0).view(1, n, 1)
+    k[..., 1] = 1.0
+    k[..., 2] = 100.0
+    k[0, at, 0, 2] = 0.0
+    p.append(k, p.rows(n, 1, "f32"), p.c.workspace(1, 1))
+    slopes = slope * 2.0 ** -torch.arange(float(G))
+    i = torch.arange(float(T)).view(T, 1)
+
+    def queries(first):                  # at first, first + 1, ..
+        q = torch.zeros(1, T, G, D)
+        q[0, :, :, 0] = -slopes
+        q[0, :, :, 1] = slopes * (first + i - 64.0)
+        q[0, :, :, 2] = -max(1.0, 2.0 ** -7 * slope)
+        assert torch.equal(q, q.bfloat16().float())
+        return q.bfloat16()
+
+    for chain in (False, True):
+        q = queries(n if chain else n - T)
+        more, drafts = {}, {}
+        if chain:
+            drafts = dict(k=torch.zeros(1, T, 1, D, dtype=torch.bfloat16), v=p.rows(T, 1, "bf16"))
+            drafts["k"][..., 2] = 100.0
+            more = dict(k=drafts["k"][0, :, 0].double().numpy(), v=drafts["v"][0, :, 0].double().numpy(),
+                        parent=[t - 1 for t in range(T)])
+        out, lse = scored(p, q, scale=1.0, slopes=slopes.cuda(), **drafts)
+        want = scored_want(p, q, 0, 0, G, T, 1.0, "bf16", slopes=slopes.numpy(), **more)
+        check_attention(out[0], lse[0], want, chain)
