@@ -447,6 +447,13 @@ class Cache8:
         return torch.zeros(n, dtype=torch.uint8, device=self.device)
 
 
+def _int32(name, x):
+    """x, which a C structure would cut to 32 bits."""
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise Csa2Error(f"{name}: {x} is not a 32-bit number")
+    return x
+
+
 class Rope:
     """Cosines and sines [positions, dim / 2] of the position rotation of `dim` channels
     from channel `first` on; pair j is the channels first + j and first + dim / 2 + j
@@ -463,8 +470,9 @@ class Rope:
         if (self.cos.data_ptr() | self.sin.data_ptr()) & 15:
             self.cos, self.sin = self.cos.clone(), self.sin.clone()
         self.device = self.cos.device
-        self.struct = Csa2Rope(_ptr(self.cos), _ptr(self.sin), cos.shape[0], 2 * cos.shape[1], first,
-                               style)
+        self.struct = Csa2Rope(_ptr(self.cos), _ptr(self.sin), _int32("Rope: positions", cos.shape[0]),
+                               _int32("Rope: dim", 2 * cos.shape[1]), _int32("Rope: first", first),
+                               _int32("Rope: style", style))
 
 
 class Scores:
@@ -478,8 +486,12 @@ class Scores:
         for name, x, dt in (("slopes", slopes, torch.float32), ("prefix", prefix, torch.int32)):
             if x is not None and (x.dtype != dt or x.dim() != 1 or not x.is_contiguous()):
                 raise Csa2Error(f"Scores: {name} is a contiguous {dt} vector")
+        # (a smaller cap could become 0, which is none, in fp32)
+        if cap != 0 and not 2.0 ** -10 <= cap <= 2.0 ** 20:
+            raise Csa2Error(f"Scores: cap {cap}; it takes 0 for none, or 2^-10 .. 2^20")
         self.slopes, self.prefix = slopes, prefix
-        self.struct = Csa2Scores(cap, window, sink, _ptr(slopes), _ptr(prefix))
+        self.struct = Csa2Scores(cap, _int32("Scores: window", window), _int32("Scores: sink", sink),
+                                 _ptr(slopes), _ptr(prefix))
 
 
 # The calls below are made once per layer and token, so their checks are kept to
