@@ -112,9 +112,9 @@ __device__ __forceinline__ float kv8_rcp(float x) {
   return y;
 }
 // tanh(y) / y as a quotient of two polynomials in u = y^2 of degree 4, fitted to
-// |y| <= 9.02 for the smallest relative error (2.1e-8; 4e-7 with fp32's roundings,
-// 6e-8 on average).  Beyond, tanh is 1 in fp32.  The quotient of the odd function
-// keeps small scores' relative precision, which 1 - 2 / (1 + e^2y) would not.
+// |y| <= 9.02 for a small relative error (4.3e-8; 3.5e-7 with fp32's roundings, 6e-8 on
+// average).  Beyond, tanh is 1 in fp32.  The quotient of the odd function keeps small
+// scores' relative precision, which 1 - 2 / (1 + e^2y) would not.
 constexpr float kTanhEnd = 9.02f;
 __device__ __forceinline__ void kv8_tanh_parts(float y, float& p, float& q) {
   const float u = y * y;
@@ -137,12 +137,12 @@ __device__ __forceinline__ float kv8_cap(float x, float cap2, float add) {
   kv8_tanh_parts(max_nan(min_nan(x, kTanhEnd), -kTanhEnd), p, q);
   return fmaf(p, kv8_rcp(q) * cap2, add);
 }
-// The same for |score / cap| <= kTanhNear from polynomials of degree 2 (8.4e-8; 3e-7 with
+// The same for |score / cap| <= kTanhNear from polynomials of degree 2 (8.9e-8; 4.5e-7 with
 // fp32's roundings), for logits s that `mul` takes to scores over the cap: the
 // polynomials take s itself, their coefficients the factor.  Four logits of a query at a
-// time, packed, two to a reciprocal: a row's logits are all finite here, or all not.
-// (Beyond kNearMul a coefficient could be infinite;
-// one that is lost to 0 belongs to a term that is, too.)
+// time, packed, two to a reciprocal: a row's logits are all finite here, or all not, and
+// hidden ones are 0.  (Beyond kNearMul a coefficient could be infinite; one that is lost
+// to 0 belongs to a term that is, too.)
 constexpr float kTanhNear = 2.0f, kNearMul = 1e6f;
 struct NearCap {
   uint64_t p0, p1, p2, q1, q2, one;
