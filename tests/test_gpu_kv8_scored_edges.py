@@ -12,7 +12,7 @@ import fp4_kv_cache_rope_gb300 as K  # noqa: E402
 from oracle import kv8 as O  # noqa: E402
 from kv8_tools import Pair  # noqa: E402
 from kv8_more_tools import check_attention, ints, scored_want  # noqa: E402
-from test_gpu_kv8_scored import filled, run_scored  # noqa: E402
+from test_gpu_kv8_scored import filled, run_scored, run_tree, slopes_of  # noqa: E402
 
 
 def scored(p, q, k=None, v=None, scale=0.0, **args):
@@ -133,3 +133,15 @@ def test_slopes_that_cancel_huge_logits(T, G, D, slope):
         out, lse = scored(p, q, scale=1.0, slopes=slopes.cuda(), **drafts)
         want = scored_want(p, q, 0, 0, G, T, 1.0, "bf16", slopes=slopes.numpy(), **more)
         check_attention(out[0], lse[0], want, chain)
+
+
+@pytest.mark.parametrize("B,Hkv,G,T", [(1, 1, 1, 256), (3, 2, 2, 256), (2, 1, 1, 64)])
+@pytest.mark.parametrize("what", ["none", "window", "all"])
+def test_paths_through_every_token(B, Hkv, G, T, what):
+    """The longest path that there is; with one query row to a CTA (few rows), and without."""
+    p = filled(B, Hkv, 64, [300, 1, 77][:B], 16, 16, O.E4M3, seed=85)
+    chain = [i - 1 for i in range(T)]
+    args = {"none": {}, "window": dict(window=100, sink=310),
+            "all": dict(window=200, sink=5, cap=6.0, slopes=slopes_of(Hkv * G))}[what]
+    run_tree(p, G, T, "bf16", size=2.0, parent=[list(chain) for _ in range(B)], **args)
+    run_tree(p, G, T, "f16", q_len=[T - 1, T, 3][:B], parent=[list(chain) for _ in range(B)], **args)
