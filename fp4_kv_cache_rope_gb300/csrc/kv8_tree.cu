@@ -3,13 +3,16 @@
 //
 //   o = (sum_parts 2^(m_p - m) o_p + sum_path 2^(x_a - m) v_a) / (... the sums alike)
 //
-// A path holds a handful of rows, so they are taken one by one: eight lanes a row,
-// fp32 throughout.  The cached rows' part, which is where the bytes are, comes from
-// the kernels that attend over the cache.
+// A drafted tree's path is a handful of rows, so they are taken one by one: eight lanes
+// a row, fp32 throughout.  The cached rows' part, which is where the bytes are, comes
+// from the kernels that attend over the cache.
 //
 // Latency bounds it: lengths, the walk to the root, the parts, then a path row after
 // another.  Trees of 60 tokens of 16 sequences, 32 heads, D 128 (up to 30,720 query
-// rows): 24 us on cold caches, of 137 us for the call.
+// rows): 24 us on cold caches, of 137 us for the call.  The work grows with the paths'
+// rows in all, so chains, which kv8_attn takes too once they are in the cache, pay for their
+// squares: 256 tokens of the 16 sequences take 1424 us where none follows another takes 425
+// us and a random tree (paths up to 21) 476 us.
 #include "kv8_tree.cuh"
 #include "kv8_scores.cuh"
 
@@ -272,8 +275,11 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_tree_join_kernel(JoinParams 
 template <int D>
 cudaError_t join_as(const JoinParams& p, int num_sms, cudaStream_t s) {
   const int64_t rows = (int64_t)p.a.c.batch * p.a.T * p.a.H;
-  // Few query rows: eight warps each, for the parts of a unit that many CTAs shared.
-  if (rows <= 16 * num_sms)
+  // Few query rows: eight warps each, for the parts of a unit that many CTAs shared.  Trees
+  // over 2 sequences of 8192 rows, 32 heads, D 128, the call: 8 tokens (512 rows) 27.5 us, and
+  // 30.1 with a group a row; 16 tokens 44 and 37 us, 32 tokens 51 and 36 us.  (Long paths have
+  // more to share: a chain of 64 tokens of 8 heads 38 and 59 us, of 128 65 and 94 us.)
+  if (rows <= 4 * num_sms)
     return kv8_launch(kv8_tree_join_kernel<D, true>, dim3((unsigned)rows), kJoinThreads, 0, s, p);
   constexpr int kRows = 4 * kJoinWarps;
   return kv8_launch(kv8_tree_join_kernel<D, false>, dim3((unsigned)((rows + kRows - 1) / kRows)),

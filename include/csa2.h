@@ -584,6 +584,8 @@ csa2_status csa2_kv8_attn_scored(const csa2_kv8_cache *cache, const csa2_rows *q
  * is seq_len[b] plus how many tokens it follows; `scores` (NULL: none), which may
  * hold no prefix, goes by these.  out, lse, softmax_scale and what is left as it
  * was: as csa2_kv8_attn; out shares no memory with k and v.
+ * Made for trees of short paths: the time of the drafted rows grows with the length of
+ * the tokens' paths in all (for a chain with the square of its tokens).
  * ws: csa2_kv8_tree_workspace_size bytes (more than the other calls take, which it
  * serves too).  T is at most CSA2_KV8_MAX_TREE.
  */
